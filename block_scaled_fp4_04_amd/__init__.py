@@ -46,6 +46,7 @@ _lib = None
 
 def _declare(L):
     p, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+    f32 = ctypes.c_float
     sig = {
         "fp4_status_str": (ctypes.c_char_p, [i32]),
         "fp4blk_version": (i32, []),
@@ -89,6 +90,13 @@ def _declare(L):
                                           p]),
         "nvfp4_grouped_gemm_w4a4_prequant": (i32, [p, p, p, i64, i64, p, p, i64, i64, p, p, p, i64, p, i32,
                                                    i64, p]),
+        "kv_cache_append": (i32, [p, p, p, i32, i64, i64, i64, i64, i64, p, i32, p, p]),
+        "kv_cache_read": (i32, [p, p, i64, i64, i64, p, i64, p, p, i32, i64, i64, i64, i64, p]),
+        "attn_decode_paged_workspace": (sz, [i64, i64, p, i64]),
+        "attn_decode_paged": (i32, [p, i64, i64, i64, i64, p, p, i64, i64, p, f32, i64, p, i32, i64, i64, p, p, sz,
+                                    p]),
+        "attn_prefill": (i32, [p, i64, i64, i64, i64, p, p, i64, i64, i64, i64, i64, i64, i64, p, p, i64, f32, i32,
+                               i64, p, i32, i64, i64, p, p]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -937,4 +945,265 @@ def nvfp4_grouped_gemm_w4a4_prequant(a: PackedNVFP4, w: ExpertsNVFP4, group_offs
                                               _ptr(row_index), _ptr(group_offs), groups, rows, _ptr(w.codes),
                                               _ptr(w.scales), _ptr(w.tscale), w.rows, _ptr(out),
                                               _out_dt(out.dtype), _ld(out), _stream())
+    return out
+
+
+# -------------------------------------------- key-value cache, attention ---
+
+KV_BF16, KV_MXFP8, KV_NVFP4, KV_MXFP4 = 0, 1, 2, 3
+_KV_FORMATS = {"bf16": KV_BF16, "mxfp8": KV_MXFP8, "nvfp4": KV_NVFP4, "mxfp4": KV_MXFP4}
+
+
+class _KvCacheArg(ctypes.Structure):
+    """fp4_kv_cache"""
+    _fields_ = [("format", ctypes.c_int)] + [(n, ctypes.c_int64) for n in ("pages", "kv_heads", "page_size", "head_dim")] + [
+        (n, ctypes.c_void_p) for n in ("k_codes", "v_codes", "k_scales", "v_scales", "k_tscale", "v_tscale")]
+
+
+class KVCache:
+    """A paged cache of keys and values in format "bf16", "mxfp8", "nvfp4" or "mxfp4".
+
+    k_codes, v_codes  [pages, kv_heads, page_size, head_dim] bfloat16 ("bf16") or uint8
+                      rows of head_dim ("mxfp8") or head_dim / 2 bytes (the 4-bit formats)
+    k_scales, v_scales uint8 [pages, kv_heads, head_dim / block, page_size], block 16
+                      ("nvfp4", E4M3) or 32 (E8M0); None for "bf16"
+    k_tscale, v_tscale float32 [kv_heads], "nvfp4" only: the second-level scales
+
+    A token's slot is page * page_size + offset.  The tensors are checked once, here; the
+    cache holds them, and they must not be resized.  `alloc` makes the tensors."""
+
+    def __init__(self, fmt: str, k_codes, v_codes, k_scales=None, v_scales=None, k_tscale=None, v_tscale=None):
+        if fmt not in _KV_FORMATS:
+            raise ValueError(f"cache format must be one of {sorted(_KV_FORMATS)}, got {fmt!r}")
+        self.fmt = fmt
+        code = _KV_FORMATS[fmt]
+        if k_codes.dim() != 4:
+            raise ValueError("k_codes must be [pages, kv_heads, page_size, row]")
+        pages, heads, page, row = k_codes.shape
+        dim = row if code in (KV_BF16, KV_MXFP8) else 2 * row
+        if dim not in (64, 128, 256):
+            raise ValueError(f"head_dim must be 64, 128 or 256, got {dim}")
+        if page < 16 or page > 256 or page & (page - 1):
+            raise ValueError(f"page_size must be a power of two in [16, 256], got {page}")
+        block = 16 if code == KV_NVFP4 else 32
+        for name, t in (("k_codes", k_codes), ("v_codes", v_codes)):
+            if code != KV_BF16:
+                _u8(t, (pages, heads, page, row), name)
+            elif t.dtype != torch.bfloat16 or not t.is_contiguous():
+                raise TypeError(f"{name} must be contiguous bfloat16")
+            else:
+                _shape(t, (pages, heads, page, row), name)
+        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+            if code == KV_BF16:
+                if t is not None:
+                    raise ValueError(f"a bf16 cache has no {name}")
+                continue
+            if t is None:
+                raise ValueError(f"a {fmt} cache needs {name}")
+            _u8(t, (pages, heads, dim // block, page), name)
+        for name, t in (("k_tscale", k_tscale), ("v_tscale", v_tscale)):
+            if code != KV_NVFP4:
+                if t is not None:
+                    raise ValueError(f"a {fmt} cache has no {name}")
+                continue
+            if t is None:
+                raise ValueError(f"an nvfp4 cache needs {name}")
+            _f32_vec(t, heads, name)
+        self.pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page, dim
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
+        self.k_tscale, self.v_tscale = k_tscale, v_tscale
+        _need_cuda(k_codes, v_codes, k_scales, v_scales, k_tscale, v_tscale)
+        self.device = k_codes.device
+        self._arg = _KvCacheArg(code, pages, heads, page, dim, *(
+            None if t is None else t.data_ptr() for t in (k_codes, v_codes, k_scales, v_scales, k_tscale, v_tscale)))
+        self._ref = ctypes.byref(self._arg)
+
+    @classmethod
+    def alloc(cls, fmt: str, pages: int, kv_heads: int, page_size: int, head_dim: int, device="cuda",
+              k_tscale=None, v_tscale=None) -> "KVCache":
+        """A new cache, its contents unspecified ("nvfp4": with the given second-level scales)."""
+        if fmt not in _KV_FORMATS:
+            raise ValueError(f"cache format must be one of {sorted(_KV_FORMATS)}, got {fmt!r}")
+        row = head_dim if fmt in ("bf16", "mxfp8") else head_dim // 2
+        dtype = torch.bfloat16 if fmt == "bf16" else torch.uint8
+        codes = [torch.empty(pages, kv_heads, page_size, row, dtype=dtype, device=device) for _ in range(2)]
+        scales = [None, None]
+        if fmt != "bf16":
+            block = 16 if fmt == "nvfp4" else 32
+            scales = [torch.empty(pages, kv_heads, head_dim // block, page_size, dtype=torch.uint8, device=device)
+                      for _ in range(2)]
+        return cls(fmt, *codes, *scales, k_tscale, v_tscale)
+
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in (self.k_codes, self.v_codes, self.k_scales, self.v_scales,
+                                                          self.k_tscale, self.v_tscale) if t is not None)
+
+
+def _kv(cache: KVCache):
+    """The fp4_kv_cache argument of a cache (kept with recorded calls)."""
+    if _recording is not None:
+        _recording_keep.append(cache)
+    return cache._ref
+
+
+def _heads(t: torch.Tensor, dtypes, what: str):
+    """(tokens, heads, dim, token stride, head stride) of [tokens, heads, dim] with unit stride along dim.
+    The stride of a dimension of size 1 is never followed, and torch may report any value for it: it
+    is given as that of a contiguous tensor then."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{what} must be [tokens, heads, head_dim], got {tuple(t.shape)}")
+    n, h, d = t.shape
+    sn, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{what} needs unit stride along head_dim")
+    if h <= 1:
+        sh = d
+    if n <= 1:
+        sn = h * sh if h * sh > d else d
+    return n, h, d, sn, sh
+
+
+_F32_BF16 = (torch.float32, torch.bfloat16)
+_BF16 = (torch.bfloat16,)
+
+
+def _i32(t: torch.Tensor, shape, what: str):
+    if t.dtype != torch.int32:
+        raise TypeError(f"{what} must be int32, got {t.dtype}")
+    _shape(t, shape, what)
+    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{what} needs unit stride along its last dimension")
+
+
+def _out_heads(out, shape, dtype, like, what="out"):
+    if out is None:
+        _out_dt(dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"{what} has shape {tuple(out.shape)}, expected {tuple(shape)}")
+    return out
+
+
+def _lse(lse, shape):
+    if lse is not None:
+        if lse.dtype != torch.float32 or not lse.is_contiguous():
+            raise TypeError("lse must be contiguous float32")
+        _shape(lse, shape, "lse")
+
+
+def _block_table(block_table, what="block_table"):
+    if block_table.dim() != 2:
+        raise ValueError(f"{what} must be [sequences, pages], got {tuple(block_table.shape)}")
+    seqs, width = block_table.shape
+    _i32(block_table, (seqs, width), what)
+    return seqs, width, block_table.stride(0) if seqs > 1 else width
+
+
+def kv_cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, rule="ocp",
+                    nonfinite: torch.Tensor | None = None) -> KVCache:
+    """Quantize new tokens' k and v [tokens, kv_heads, head_dim] (fp32 or bf16, any token and
+    head strides) into the cache at `slots` (int64 [tokens]; page * page_size + offset,
+    negative: the token is skipped).  Slots of one call must differ."""
+    L = lib()
+    n, h, d, kt, kh = _heads(k, _F32_BF16, "k")
+    nv, hv, dv, vt, vh = _heads(v, _F32_BF16, "v")
+    if (n, h, d) != (nv, hv, dv) or k.dtype != v.dtype:
+        raise ValueError("k and v must have the same shape and dtype")
+    if (h, d) != (cache.kv_heads, cache.head_dim):
+        raise ValueError(f"k has {h} heads of {d}, the cache {cache.kv_heads} of {cache.head_dim}")
+    if slots.dtype != torch.int64 or slots.dim() != 1 or slots.shape[0] != n or not slots.is_contiguous():
+        raise ValueError(f"slots must be a contiguous int64 tensor of {n} element(s)")
+    if nonfinite is not None and (nonfinite.dtype != torch.int32 or nonfinite.numel() < 1):
+        raise ValueError("nonfinite must be an int32 tensor of at least one element")
+    _need_cuda(cache.k_codes, k, v, slots, nonfinite)
+    _run(L.kv_cache_append, _kv(cache), _ptr(k), _ptr(v), _dt(k), n, kt, kh, vt, vh, _ptr(slots), _rule(rule),
+         _ptr(nonfinite), _stream())
+    return cache
+
+
+def kv_cache_read(cache: KVCache, block_table: torch.Tensor, cu_seqlens: torch.Tensor, tokens: int,
+                  dtype=torch.bfloat16, k_out: torch.Tensor | None = None,
+                  v_out: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Read cached sequences back as packed rows: k and v [tokens, kv_heads, head_dim], row t
+    being position t - cu_seqlens[b] of the sequence b that holds it.  block_table int32
+    [sequences, pages], cu_seqlens int32 [sequences + 1], tokens = cu_seqlens[-1] (known to the
+    caller, so that nothing waits for the device)."""
+    L = lib()
+    seqs, width, stride = _block_table(block_table)
+    _i32(cu_seqlens, (seqs + 1,), "cu_seqlens")
+    shape = (int(tokens), cache.kv_heads, cache.head_dim)
+    k_out = _out_heads(k_out, shape, dtype, cache.k_codes, "k_out")
+    v_out = _out_heads(v_out, shape, k_out.dtype, cache.k_codes, "v_out")
+    _, _, _, kt, kh = _heads(k_out, _F32_BF16, "k_out")
+    _, _, _, vt, vh = _heads(v_out, (k_out.dtype,), "v_out")
+    _need_cuda(cache.k_codes, block_table, cu_seqlens, k_out, v_out)
+    _run(L.kv_cache_read, _kv(cache), _ptr(block_table), seqs, width, stride, _ptr(cu_seqlens), shape[0],
+         _ptr(k_out), _ptr(v_out), _dt(k_out), kt, kh, vt, vh, _stream())
+    return k_out, v_out
+
+
+def attn_decode_paged_workspace(cache: KVCache, seqs: int, heads: int, table_width: int) -> torch.Tensor:
+    n = lib().attn_decode_paged_workspace(seqs, heads, cache._ref, table_width)
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=cache.device)
+
+
+def attn_decode_paged(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                      scale: float | None = None, window: int = 0, dtype=torch.bfloat16,
+                      out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of one new token per sequence over the cache: q [sequences, heads, head_dim]
+    bf16 (heads a multiple of the cache's), block_table int32 [sequences, pages], seq_lens int32
+    [sequences] (the new token included; 0 gives zeros).  scale defaults to head_dim ** -0.5;
+    window > 0 attends to the last `window` keys only.  lse: optional float32 [sequences, heads]
+    that receives the logarithm of the softmax sum."""
+    L = lib()
+    n, h, d, qt, qh = _heads(q, _BF16, "q")
+    seqs, width, stride = _block_table(block_table)
+    if seqs != n:
+        raise ValueError(f"q has {n} sequences, block_table {seqs}")
+    if d != cache.head_dim or h == 0 or h % cache.kv_heads:
+        raise ValueError(f"q has {h} heads of {d}, the cache {cache.kv_heads} of {cache.head_dim}")
+    _i32(seq_lens, (n,), "seq_lens")
+    out = _out_heads(out, q.shape, dtype, q)
+    _, _, _, ot, oh = _heads(out, _F32_BF16, "out")
+    _lse(lse, (n, h))
+    need = L.attn_decode_paged_workspace(n, h, cache._ref, width)
+    workspace = _workspace(workspace, need, q)
+    _need_cuda(cache.k_codes, q, block_table, seq_lens, out, lse, workspace)
+    _run(L.attn_decode_paged, _ptr(q), n, h, qt, qh, _kv(cache), _ptr(block_table), width, stride, _ptr(seq_lens),
+         d ** -0.5 if scale is None else scale, window, _ptr(out), _dt(out), ot, oh, _ptr(lse), _ptr(workspace),
+         workspace.numel(), _stream())
+    return out
+
+
+def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                 cu_seqlens_k: torch.Tensor, causal: bool = True, window: int = 0, scale: float | None = None,
+                 dtype=torch.bfloat16, out: torch.Tensor | None = None,
+                 lse: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of packed prompts: q [q_tokens, heads, head_dim], k and v [k_tokens, kv_heads,
+    head_dim] bf16, any token and head strides; cu_seqlens_q and cu_seqlens_k int32
+    [sequences + 1].  A sequence's last query stands at its last key.  window > 0: a query sees
+    the last `window` keys up to its position.  lse: optional float32 [q_tokens, heads]."""
+    L = lib()
+    n, h, d, qt, qh = _heads(q, _BF16, "q")
+    nk, hk, dk, kt, kh = _heads(k, _BF16, "k")
+    nv, hv, dv, vt, vh = _heads(v, _BF16, "v")
+    if (nk, hk, dk) != (nv, hv, dv):
+        raise ValueError("k and v must have the same shape")
+    if dk != d or hk == 0 or h == 0 or h % hk:
+        raise ValueError(f"q has {h} heads of {d}, k {hk} of {dk}")
+    if cu_seqlens_q.dim() != 1 or cu_seqlens_q.shape[0] < 2:
+        raise ValueError("cu_seqlens_q must hold sequences + 1 offsets")
+    seqs = cu_seqlens_q.shape[0] - 1
+    _i32(cu_seqlens_q, (seqs + 1,), "cu_seqlens_q")
+    _i32(cu_seqlens_k, (seqs + 1,), "cu_seqlens_k")
+    out = _out_heads(out, q.shape, dtype, q)
+    _, _, _, ot, oh = _heads(out, _F32_BF16, "out")
+    _lse(lse, (n, h))
+    _need_cuda(q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse)
+    _run(L.attn_prefill, _ptr(q), n, h, qt, qh, _ptr(k), _ptr(v), nk, hk, d, kt, kh, vt, vh, _ptr(cu_seqlens_q),
+         _ptr(cu_seqlens_k), seqs, d ** -0.5 if scale is None else scale, int(bool(causal)), window, _ptr(out),
+         _dt(out), ot, oh, _ptr(lse), _stream())
     return out

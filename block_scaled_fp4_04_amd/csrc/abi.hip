@@ -921,3 +921,275 @@ fp4_status nvfp4_grouped_gemm_w4a4(const void *a, int64_t a_rows, int64_t K, int
 }
 
 }  // extern "C"
+
+// -------------------------------------------- key-value cache, attention --
+
+namespace {
+
+int kv_bits(fp4_kv_format f) { return f == FP4_KV_BF16 ? 16 : f == FP4_KV_MXFP8 ? 8 : 4; }
+
+int log2_of(int64_t v)
+{
+    int s = 0;
+    while ((int64_t(1) << s) < v) ++s;
+    return s;
+}
+
+fp4_status check_cache(const fp4_kv_cache *c)
+{
+    if (!c) return FP4_ERR_NULL;
+    if (c->format < FP4_KV_BF16 || c->format > FP4_KV_MXFP4) return FP4_ERR_DTYPE;
+    if (c->pages <= 0 || c->kv_heads <= 0 || c->kv_heads > 65535) return FP4_ERR_SHAPE;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return FP4_ERR_SHAPE;
+    if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return FP4_ERR_SHAPE;
+    if (c->pages >= k2GiB / c->page_size) return FP4_ERR_SHAPE;
+    if (!c->k_codes || !c->v_codes) return FP4_ERR_NULL;
+    if (!aligned16(c->k_codes) || !aligned16(c->v_codes)) return FP4_ERR_LAYOUT;
+    if (c->format != FP4_KV_BF16) {
+        if (!c->k_scales || !c->v_scales) return FP4_ERR_NULL;
+        if (!aligned16(c->k_scales) || !aligned16(c->v_scales)) return FP4_ERR_LAYOUT;
+    }
+    if (c->format == FP4_KV_NVFP4 && (!c->k_tscale || !c->v_tscale)) return FP4_ERR_NULL;
+    return FP4_OK;
+}
+
+// rows of head_dim elements of size es at any token / head strides that keep them
+// 16-byte aligned; outputs also need rows that do not overlap (by these strides)
+fp4_status check_heads(const void *p, int64_t tok, int64_t head, int64_t dim, size_t es, bool output)
+{
+    if (!p) return FP4_ERR_NULL;
+    const int64_t least = output ? dim : 0;
+    if (tok < least || head < least) return FP4_ERR_LAYOUT;
+    if (!aligned16(p) || ((uint64_t)tok * es) % 16 != 0 || ((uint64_t)head * es) % 16 != 0) return FP4_ERR_LAYOUT;
+    return FP4_OK;
+}
+
+fp4_status check_table(const int32_t *table, int64_t seqs, int64_t width, int64_t stride, const fp4_kv_cache *c)
+{
+    if (seqs <= 0 || seqs >= (1 << 24) || width <= 0 || width >= (int64_t(1) << 30) / c->page_size) return FP4_ERR_SHAPE;
+    if (!table) return FP4_ERR_NULL;
+    if (stride < width && seqs > 1) return FP4_ERR_LAYOUT;
+    return FP4_OK;
+}
+
+bool valid_scale(float s) { return s >= 0.0f && s <= 1.0e30f; }
+
+// Partial results of the decode kernel: two slots a workgroup
+struct DecodeSpace {
+    int part_heads;
+    size_t ml_offset, bytes;
+};
+
+DecodeSpace decode_space(int64_t seqs, int64_t heads, const fp4_kv_cache *c, int64_t width)
+{
+    const int64_t group = heads / c->kv_heads;
+    const int64_t grid = decode_grid(seqs, c->kv_heads, (group + 15) / 16, width * c->page_size);
+    DecodeSpace s;
+    s.part_heads = group < 16 ? (int)group : 16;
+    s.ml_offset = (size_t)(2 * grid * s.part_heads * c->head_dim) * 4;
+    s.bytes = align256(s.ml_offset + (size_t)(2 * grid * s.part_heads) * 8);
+    return s;
+}
+
+KvArgs kv_args(const fp4_kv_cache *c)
+{
+    KvArgs a = {};
+    a.codes[0] = reinterpret_cast<uint8_t *>(c->k_codes);
+    a.codes[1] = reinterpret_cast<uint8_t *>(c->v_codes);
+    a.scales[0] = c->k_scales;
+    a.scales[1] = c->v_scales;
+    a.tscale[0] = c->k_tscale;
+    a.tscale[1] = c->v_tscale;
+    a.kv_heads = (int)c->kv_heads;
+    a.head_dim = (int)c->head_dim;
+    a.page_shift = log2_of(c->page_size);
+    a.pages = c->pages;
+    return a;
+}
+
+// 8-value units of one call fit 32 bits
+bool kv_units_ok(const fp4_kv_cache *c, int64_t tokens)
+{
+    return tokens < k2GiB && 2 * c->kv_heads * tokens < k2GiB / (c->head_dim / 8);
+}
+
+}  // namespace
+
+extern "C" {
+
+fp4_status kv_cache_append(const fp4_kv_cache *cache, const void *k, const void *v, fp4_dtype xt,
+                           int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,
+                           int64_t v_token_stride, int64_t v_head_stride, const int64_t *slots,
+                           fp4_mx_rule rule, int32_t *nonfinite, hipStream_t stream)
+{
+    if (!valid_dtype(xt) || (rule != FP4_MX_OCP_FLOOR && rule != FP4_MX_CEIL)) return FP4_ERR_DTYPE;
+    FP4_TRY(check_cache(cache));
+    if (tokens < 0 || !kv_units_ok(cache, tokens)) return FP4_ERR_SHAPE;
+    if (tokens == 0) return FP4_OK;
+    FP4_TRY(check_heads(k, k_token_stride, k_head_stride, cache->head_dim, dsize(xt), false));
+    FP4_TRY(check_heads(v, v_token_stride, v_head_stride, cache->head_dim, dsize(xt), false));
+    if (!slots) return FP4_ERR_NULL;
+    FP4_TRY(check_device());
+    KvArgs a = kv_args(cache);
+    a.tokens = tokens;
+    a.x[0] = const_cast<void *>(k);
+    a.x[1] = const_cast<void *>(v);
+    a.tok[0] = k_token_stride;
+    a.tok[1] = v_token_stride;
+    a.head[0] = k_head_stride;
+    a.head[1] = v_head_stride;
+    a.slots = slots;
+    a.rule = rule;
+    a.nonfinite = nonfinite;
+    return launch_kv_append(a, cache->format, xt, stream);
+}
+
+fp4_status kv_cache_read(const fp4_kv_cache *cache, const int32_t *block_table, int64_t seqs,
+                         int64_t table_width, int64_t table_stride, const int32_t *cu_seqlens,
+                         int64_t tokens, void *k, void *v, fp4_dtype yt, int64_t k_token_stride,
+                         int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                         hipStream_t stream)
+{
+    if (!valid_dtype(yt)) return FP4_ERR_DTYPE;
+    FP4_TRY(check_cache(cache));
+    FP4_TRY(check_table(block_table, seqs, table_width, table_stride, cache));
+    if (!cu_seqlens) return FP4_ERR_NULL;
+    if (tokens < 0 || !kv_units_ok(cache, tokens)) return FP4_ERR_SHAPE;
+    if (tokens == 0) return FP4_OK;
+    FP4_TRY(check_heads(k, k_token_stride, k_head_stride, cache->head_dim, dsize(yt), true));
+    FP4_TRY(check_heads(v, v_token_stride, v_head_stride, cache->head_dim, dsize(yt), true));
+    FP4_TRY(check_device());
+    KvArgs a = kv_args(cache);
+    a.tokens = tokens;
+    a.x[0] = k;
+    a.x[1] = v;
+    a.tok[0] = k_token_stride;
+    a.tok[1] = v_token_stride;
+    a.head[0] = k_head_stride;
+    a.head[1] = v_head_stride;
+    a.table = block_table;
+    a.table_stride = table_stride;
+    a.table_width = (int)table_width;
+    a.seqs = (int)seqs;
+    a.cu = cu_seqlens;
+    return launch_kv_read(a, cache->format, yt, stream);
+}
+
+size_t attn_decode_paged_workspace(int64_t seqs, int64_t heads, const fp4_kv_cache *cache, int64_t table_width)
+{
+    if (!cache || seqs <= 0 || heads <= 0 || table_width <= 0 || cache->kv_heads <= 0 || cache->page_size <= 0 ||
+        cache->head_dim <= 0 || heads % cache->kv_heads != 0)
+        return 0;
+    return decode_space(seqs, heads, cache, table_width).bytes;
+}
+
+fp4_status attn_decode_paged(const void *q, int64_t seqs, int64_t heads, int64_t q_seq_stride,
+                             int64_t q_head_stride, const fp4_kv_cache *cache, const int32_t *block_table,
+                             int64_t table_width, int64_t table_stride, const int32_t *seq_lens, float scale,
+                             int64_t window, void *out, fp4_dtype ot, int64_t o_seq_stride,
+                             int64_t o_head_stride, float *lse, void *ws, size_t ws_bytes, hipStream_t stream)
+{
+    if (!valid_dtype(ot)) return FP4_ERR_DTYPE;
+    FP4_TRY(check_cache(cache));
+    FP4_TRY(check_table(block_table, seqs, table_width, table_stride, cache));
+    if (heads <= 0 || heads > 65535 || heads % cache->kv_heads != 0 || window < 0 || !valid_scale(scale)) return FP4_ERR_SHAPE;
+    const int64_t max_len = table_width * cache->page_size;
+    const int64_t group = heads / cache->kv_heads, head_tiles = (group + 15) / 16;
+    if (seqs * heads >= k2GiB || decode_units_bound(seqs, cache->kv_heads, head_tiles, max_len) >= k2GiB)
+        return FP4_ERR_SHAPE;
+    FP4_TRY(check_heads(q, q_seq_stride, q_head_stride, cache->head_dim, 2, false));
+    FP4_TRY(check_heads(out, o_seq_stride, o_head_stride, cache->head_dim, dsize(ot), true));
+    if (!seq_lens) return FP4_ERR_NULL;
+    FP4_TRY(check_device());
+    const DecodeSpace sp = decode_space(seqs, heads, cache, table_width);
+    if (!ws || !aligned16(ws) || ws_bytes < sp.bytes) return FP4_ERR_WORKSPACE;
+    DecodeArgs a = {};
+    a.q = reinterpret_cast<const uint16_t *>(q);
+    a.q_seq = q_seq_stride;
+    a.q_head = q_head_stride;
+    a.k_codes = reinterpret_cast<const uint8_t *>(cache->k_codes);
+    a.v_codes = reinterpret_cast<const uint8_t *>(cache->v_codes);
+    a.k_scales = cache->k_scales;
+    a.v_scales = cache->v_scales;
+    a.k_tscale = cache->format == FP4_KV_NVFP4 ? cache->k_tscale : nullptr;
+    a.v_tscale = cache->format == FP4_KV_NVFP4 ? cache->v_tscale : nullptr;
+    a.table = block_table;
+    a.table_stride = table_stride;
+    a.seq_lens = seq_lens;
+    a.seqs = (int)seqs;
+    a.heads = (int)heads;
+    a.kv_heads = (int)cache->kv_heads;
+    a.group = (int)group;
+    a.head_tiles = (int)head_tiles;
+    a.head_dim = (int)cache->head_dim;
+    a.page_shift = log2_of(cache->page_size);
+    a.pages = (int)cache->pages;
+    a.max_len = (int)max_len;
+    a.scale_log2 = scale * 1.44269504f;
+    a.window = window > max_len ? 0 : (int)window;
+    a.out = out;
+    a.out_bf16 = ot == FP4_BF16;
+    a.o_seq = o_seq_stride;
+    a.o_head = o_head_stride;
+    a.lse = lse;
+    a.part_o = reinterpret_cast<float *>(ws);
+    a.part_ml = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(ws) + sp.ml_offset);
+    a.part_heads = sp.part_heads;
+    return launch_attn_decode(a, cache->format, stream);
+}
+
+fp4_status attn_prefill(const void *q, int64_t q_tokens, int64_t heads, int64_t q_token_stride,
+                        int64_t q_head_stride, const void *k, const void *v, int64_t k_tokens,
+                        int64_t kv_heads, int64_t head_dim, int64_t k_token_stride, int64_t k_head_stride,
+                        int64_t v_token_stride, int64_t v_head_stride, const int32_t *cu_q,
+                        const int32_t *cu_k, int64_t seqs, float scale, int causal, int64_t window, void *out,
+                        fp4_dtype ot, int64_t o_token_stride, int64_t o_head_stride, float *lse,
+                        hipStream_t stream)
+{
+    if (!valid_dtype(ot) || (causal != 0 && causal != 1)) return FP4_ERR_DTYPE;
+    if (heads <= 0 || heads > 65535 || kv_heads <= 0 || heads % kv_heads != 0) return FP4_ERR_SHAPE;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return FP4_ERR_SHAPE;
+    if (q_tokens < 0 || k_tokens < 0 || seqs <= 0 || seqs >= (1 << 24) || window < 0 || !valid_scale(scale)) return FP4_ERR_SHAPE;
+    const int64_t group = heads / kv_heads;
+    if (k_tokens >= k2GiB || q_tokens >= k2GiB / group) return FP4_ERR_SHAPE;
+    if (prefill_grid(q_tokens, seqs, kv_heads, group) >= k2GiB) return FP4_ERR_SHAPE;
+    if (!cu_q || !cu_k) return FP4_ERR_NULL;
+    if (q_tokens == 0) return FP4_OK;
+    FP4_TRY(check_heads(q, q_token_stride, q_head_stride, head_dim, 2, false));
+    if (k_tokens > 0) {
+        FP4_TRY(check_heads(k, k_token_stride, k_head_stride, head_dim, 2, false));
+        FP4_TRY(check_heads(v, v_token_stride, v_head_stride, head_dim, 2, false));
+    }
+    FP4_TRY(check_heads(out, o_token_stride, o_head_stride, head_dim, dsize(ot), true));
+    FP4_TRY(check_device());
+    PrefillArgs a = {};
+    a.q = reinterpret_cast<const uint16_t *>(q);
+    a.k = reinterpret_cast<const uint16_t *>(k);
+    a.v = reinterpret_cast<const uint16_t *>(v);
+    a.q_tok = q_token_stride;
+    a.q_head = q_head_stride;
+    a.k_tok = k_token_stride;
+    a.k_head = k_head_stride;
+    a.v_tok = v_token_stride;
+    a.v_head = v_head_stride;
+    a.cu_q = cu_q;
+    a.cu_k = cu_k;
+    a.seqs = (int)seqs;
+    a.heads = (int)heads;
+    a.kv_heads = (int)kv_heads;
+    a.group = (int)group;
+    a.head_dim = (int)head_dim;
+    a.q_tokens = q_tokens;
+    a.k_tokens = k_tokens;
+    a.scale_log2 = scale * 1.44269504f;
+    a.causal = causal;
+    a.window = window >= k_tokens ? 0 : (int)window;
+    a.out = out;
+    a.out_bf16 = ot == FP4_BF16;
+    a.o_tok = o_token_stride;
+    a.o_head = o_head_stride;
+    a.lse = lse;
+    return launch_attn_prefill(a, stream);
+}
+
+}  // extern "C"

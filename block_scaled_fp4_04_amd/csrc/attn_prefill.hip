@@ -1,0 +1,312 @@
+// attn_prefill.hip -- attention of whole prompts: packed sequences of different
+// lengths, grouped heads, causal and windowed masks.
+//
+// For query token i of a sequence with lq queries and lk keys, at position
+// pos = i + lk - lq (the last query stands at the last key), and query head h:
+//   t_j = scale q.k_j over the keys j that i sees, o = sum_j exp(t_j - lse) v_j,
+//   lse = log sum_j exp(t_j);  j < lk, j <= pos (causal), j > pos - window (window > 0).
+//
+// Bound: 4 D flop a (query head, key) pair on the matrix core; K and V are read once
+// per row tile from L2, so for long prompts the MFMA rate is the floor.
+//
+// Rows of a tile are (token, head of the group) pairs, numbered token-major, so every
+// group size fills the tiles, a tile covers few tokens (little of it is masked) and K
+// and V are staged once for all heads of the group.
+//
+// One wave, 32 rows, 64 keys at a time, 32x32x16 MFMA:
+//   S^T = K Q^T  rows = keys, columns = query rows: a lane holds, for its one query row
+//                lane & 31, the keys 8 a + 4 h + i of each 32 (h = lane >> 5, a, i < 4).
+//                Row statistics then need one exchange, between the wave's halves.
+//   O^T += V^T P^T  the contracted keys are numbered so that slot (h, j) of step s is
+//                the key the lane already holds (16 s + 8 (j >> 2) + 4 h + (j & 3)): P
+//                goes from the softmax to the matrix core without leaving its lane.
+//                V^T comes from row-major V in LDS by transposing LDS reads (4 keys x
+//                16 d per 16 lanes).
+// K and V tiles go to LDS by direct copies (two buffers, the next tile in flight while
+// one is used); 16-byte chunks are XOR-swizzled by row so that neither kind of read
+// meets a bank twice in a phase.
+#include "device_common.h"
+#include "internal.h"
+
+namespace fp4k {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+namespace {
+
+constexpr int kKeys = 64;      // keys of a tile
+constexpr int kRows = 128;     // rows of a workgroup: four waves of 32
+constexpr float kLazy = 8.0f;  // log2 headroom before the running maximum moves
+
+struct QTile {
+    int b, tile;
+};
+
+// rows tiles of sequence b
+__device__ __forceinline__ int seq_tiles(const PrefillArgs &a, int b)
+{
+    const int64_t n = (int64_t)a.cu_q[b + 1] - a.cu_q[b];
+    if (n <= 0 || n > a.q_tokens) return 0;
+    return (int)((n * a.group + kRows - 1) / kRows);
+}
+
+// The sequence and tile of row tile x; b = -1 past the last.
+__device__ __forceinline__ QTile find_tile(const PrefillArgs &a, int x)
+{
+    const int lane = threadIdx.x & 63;
+    int base = 0;
+    for (int b0 = 0; b0 < a.seqs; b0 += 64) {
+        const int t = b0 + lane < a.seqs ? seq_tiles(a, b0 + lane) : 0;
+        int inc = t;
+        for (int off = 1; off < 64; off <<= 1) {
+            const int o = __shfl_up(inc, off, kWave);
+            if (lane >= off) inc += o;
+        }
+        const int sum = __builtin_amdgcn_readlane(inc, 63);
+        if (x < base + sum) {
+            int i = __builtin_popcountll(__ballot(base + inc <= x));
+            i = i > 63 ? 63 : i;
+            const int tiles = __builtin_amdgcn_readlane(t, i);
+            const int at = x - base - __builtin_amdgcn_readlane(inc - t, i);
+            return {b0 + i, tiles - 1 - at};  // a sequence's last tiles see the most keys: they go first
+        }
+        base += sum;
+    }
+    return {-1, 0};
+}
+
+// swizzle of the 16-byte chunks of an LDS row
+template <int D>
+__device__ __forceinline__ int swz_k(int row)
+{
+    return D == 64 ? (row >> 1) & 7 : row & 15;
+}
+template <int D>
+__device__ __forceinline__ int swz_v(int row)
+{
+    return D == 64 ? (row & 2) << 1 : (row & 3) << 2;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    const bf16x2 v = {(__bf16)lo, (__bf16)hi};
+    uint32_t r;
+    __builtin_memcpy(&r, &v, 4);
+    return r;
+}
+
+__device__ __forceinline__ float other_half(float v)
+{
+    return __shfl_xor(v, 32, kWave);
+}
+
+}  // namespace
+
+template <int D>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_prefill(PrefillArgs a)
+{
+    constexpr int kRowB = 2 * D;             // bytes of an LDS row
+    constexpr int kTileB = kKeys * kRowB;    // bytes of a tile of K or V
+    constexpr int kChunks = kRowB / 16;      // 16-byte chunks of a row
+    constexpr int kCopies = kTileB / 4096;   // 1 KiB copies per wave and tile
+    constexpr int kSteps = D / 16;           // MFMA steps of S
+    constexpr int kDT = D / 32;              // MFMA tiles of O
+    extern __shared__ __align__(16) uint8_t sm[];  // [2 buffers][K tile, V tile]
+    const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int hkv = blockIdx.x % a.kv_heads;
+    const QTile qt = find_tile(a, blockIdx.x / a.kv_heads);
+    if (qt.b < 0) return;
+
+    // the sequence's rows, clamped into the buffers
+    auto clamp = [](int64_t v, int64_t top) { return v < 0 ? (int64_t)0 : (v > top ? top : v); };
+    const int64_t q0 = clamp(a.cu_q[qt.b], a.q_tokens), q1 = clamp(a.cu_q[qt.b + 1], a.q_tokens);
+    const int64_t k0 = clamp(a.cu_k[qt.b], a.k_tokens), k1 = clamp(a.cu_k[qt.b + 1], a.k_tokens);
+    const int lq = (int)(q1 - q0), lk = k1 > k0 ? (int)(k1 - k0) : 0;
+    const int64_t rows = (int64_t)lq * a.group;
+    const int64_t row0 = (int64_t)qt.tile * kRows;
+    if (row0 >= rows) return;
+
+    // this lane's row
+    int64_t row = row0 + wave * 32 + col;
+    const bool live = row < rows;
+    if (!live) row = rows - 1;
+    const int tok = (int)((uint32_t)row / (uint32_t)a.group), hg = (int)row - tok * a.group;
+    const int head = hkv * a.group + hg;
+    const int pos = tok + lk - lq;
+    const int ub = a.causal ? pos + 1 : lk;                                  // keys [lb, ub)
+    const int lb = a.window > 0 && pos - a.window + 1 > 0 ? pos - a.window + 1 : 0;
+    // the range of keys of the wave and of the workgroup
+    auto tok_of = [&](int64_t r) { return (int)((uint32_t)(r < rows ? r : rows - 1) / (uint32_t)a.group); };
+    auto ub_of = [&](int t) { return a.causal ? t + lk - lq + 1 : lk; };
+    auto lb_of = [&](int t) { const int p = t + lk - lq; return a.window > 0 && p - a.window + 1 > 0 ? p - a.window + 1 : 0; };
+    const int w_t0 = tok_of(row0 + wave * 32), w_t1 = tok_of(row0 + wave * 32 + 31);
+    const int w_hi = ub_of(w_t1), w_lo = lb_of(w_t0);              // any row of the wave sees keys in [w_lo, w_hi)
+    const int w_full_hi = ub_of(w_t0), w_full_lo = lb_of(w_t1);    // every row sees [w_full_lo, w_full_hi)
+    const int lo = lb_of(tok_of(row0)) & ~(kKeys - 1);
+    const int hi = ub_of(tok_of(row0 + kRows - 1));
+
+    // ---- Q: the B operand, held for the whole tile
+    uint4 q[kSteps];
+    {
+        const uint16_t *qp = a.q + (q0 + tok) * a.q_tok + head * a.q_head + 8 * half;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const uint4 *>(qp + 16 * s);
+    }
+
+    f32x16 o[kDT];
+#pragma unroll
+    for (int i = 0; i < kDT; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
+    float m = -INFINITY, l = 0.0f;
+
+    const uint16_t *kb = a.k + k0 * a.k_tok + hkv * a.k_head;
+    const uint16_t *vb = a.v + k0 * a.v_tok + hkv * a.v_head;
+    auto stage = [&](int key0, int buf) {
+        uint8_t *dst = sm + buf * 2 * kTileB;
+#pragma unroll
+        for (int j = 0; j < kCopies; ++j) {
+            const int piece = (j * 4 + wave) * 1024 + lane * 16;  // byte of the tile this lane fills
+            const int r = piece / kRowB, slot = (piece % kRowB) / 16;
+            int key = key0 + r;
+            key = key < lk ? key : lk - 1;
+            const uint16_t *ks = kb + (int64_t)key * a.k_tok + (slot ^ swz_k<D>(r)) * 8;
+            const uint16_t *vs = vb + (int64_t)key * a.v_tok + (slot ^ swz_v<D>(r)) * 8;
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)ks,
+                                             (__attribute__((address_space(3))) void *)(dst + (j * 4 + wave) * 1024), 16, 0, 0);
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)vs,
+                                             (__attribute__((address_space(3))) void *)(dst + kTileB + (j * 4 + wave) * 1024), 16, 0, 0);
+        }
+    };
+
+    if (lo < hi) stage(lo, 0);
+    int buf = 0;
+    for (int key0 = lo; key0 < hi; key0 += kKeys, buf ^= 1) {
+        __syncthreads();  // this tile has arrived; the other buffer is free
+        if (key0 + kKeys < hi) stage(key0 + kKeys, buf ^ 1);
+        if (key0 >= w_hi || key0 + kKeys <= w_lo) continue;
+        const uint8_t *kt = sm + buf * 2 * kTileB, *vt = kt + kTileB;
+
+        f32x16 s[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[j][e] = 0.0f;
+            const int r = 32 * j + col;
+            const uint8_t *kr = kt + r * kRowB;
+#pragma unroll
+            for (int st = 0; st < kSteps; ++st) {
+                const uint4 f = *reinterpret_cast<const uint4 *>(kr + (((2 * st + half) ^ swz_k<D>(r)) * 16));
+                s[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(f), as_bf16x8(q[st]), s[j], 0, 0, 0);
+            }
+        }
+        const float c = a.scale_log2;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[j][e] *= c;
+        if (key0 < w_full_lo || key0 + kKeys > w_full_hi) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int key = key0 + 32 * j + 8 * (e >> 2) + 4 * half + (e & 3);
+                    s[j][e] = key >= lb && key < ub ? s[j][e] : -INFINITY;
+                }
+        }
+        float tm = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) tm = fmaxf(tm, s[j][e]);
+        if (__ballot(tm > m + kLazy)) {
+            const float mn = fmaxf(m, fmaxf(tm, other_half(tm)));
+            const float alpha = mn == m ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+            m = mn;
+            l *= alpha;
+#pragma unroll
+            for (int i = 0; i < kDT; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[i][e] *= alpha;
+        }
+        const float mm = m == -INFINITY ? 0.0f : m;
+        // P of step st: keys 16 st + 8 (j >> 2) + 4 half + (j & 3), registers 8 (st & 1) .. + 7 of s[st >> 1]
+        uint4 p[4];
+#pragma unroll
+        for (int st = 0; st < 4; ++st) {
+            float e[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                e[i] = __builtin_amdgcn_exp2f(s[st >> 1][8 * (st & 1) + i] - mm);
+                l += e[i];
+            }
+            p[st] = make_uint4(pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7]));
+        }
+        // V^T: lane c of a 16-lane group addresses key c >> 2 of 4, d 4 (c & 3) of 16
+        const int c16 = lane & 15, dgrp = (lane >> 4) & 1;
+#pragma unroll
+        for (int st = 0; st < 4; ++st) {
+#pragma unroll
+            for (int i = 0; i < kDT; ++i) {
+                uint4 f;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int r = 16 * st + 8 * x + 4 * half + (c16 >> 2);
+                    const int d = 32 * i + 16 * dgrp + 4 * (c16 & 3);
+                    const uint8_t *src = vt + r * kRowB + (((d >> 3) ^ swz_v<D>(r)) * 16) + (d & 4) * 2;
+                    const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                        (__attribute__((address_space(3))) s16x4 *)(src));
+                    if (x == 0) __builtin_memcpy(&f.x, &v, 8);
+                    else __builtin_memcpy(&f.z, &v, 8);
+                }
+                o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(f), as_bf16x8(p[st]), o[i], 0, 0, 0);
+            }
+        }
+    }
+
+    l += other_half(l);
+    if (!live) return;
+    const float f = l == 0.0f ? 0.0f : 1.0f / l;
+    if (a.lse && half == 0)
+        a.lse[(q0 + tok) * a.heads + head] = (m + __builtin_amdgcn_logf(l)) * 0.69314718f;
+    // the lane holds d = 32 i + 8 x + 4 half + (0..3) of its row
+#pragma unroll
+    for (int i = 0; i < kDT; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int64_t at = (q0 + tok) * a.o_tok + head * a.o_head + 32 * i + 8 * x + 4 * half;
+            const float4 v = make_float4(o[i][4 * x] * f, o[i][4 * x + 1] * f, o[i][4 * x + 2] * f, o[i][4 * x + 3] * f);
+            if (a.out_bf16)
+                *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(a.out) + at) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+            else
+                *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + at) = v;
+        }
+}
+
+template <int D>
+static fp4_status launch_d(const PrefillArgs &a, int64_t grid, hipStream_t st)
+{
+    constexpr int kLds = 4 * kKeys * 2 * D;
+    static std::atomic<uint64_t> done{0};
+    if (!set_max_lds_once((const void *)k_attn_prefill<D>, kLds, done)) return FP4_ERR_HIP;
+    hipLaunchKernelGGL(k_attn_prefill<D>, dim3((unsigned)grid), dim3(256), kLds, st, a);
+    return hipGetLastError() == hipSuccess ? FP4_OK : FP4_ERR_HIP;
+}
+
+// Row tiles of all sequences: at most one more per sequence than the packed rows hold.
+int64_t prefill_grid(int64_t q_tokens, int64_t seqs, int64_t kv_heads, int64_t group)
+{
+    const int64_t more = seqs < q_tokens ? seqs : q_tokens;
+    return (q_tokens * group / kRows + more) * kv_heads;
+}
+
+fp4_status launch_attn_prefill(const PrefillArgs &a, hipStream_t st)
+{
+    const int64_t grid = prefill_grid(a.q_tokens, a.seqs, a.kv_heads, a.group);
+    if (a.head_dim == 64) return launch_d<64>(a, grid, st);
+    if (a.head_dim == 128) return launch_d<128>(a, grid, st);
+    return launch_d<256>(a, grid, st);
+}
+
+}  // namespace fp4k

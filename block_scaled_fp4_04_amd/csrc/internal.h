@@ -148,6 +148,76 @@ fp4_status launch_mxfp4_gemm_seg_wrow(const MxGemmArgs &g, hipStream_t st);
 // W4A8: A MXFP8 (E4M3 bytes [M][K], E8M0 [M][K/32]), W MXFP4; K % 128 == 0
 fp4_status launch_mxfp4_gemm_w4a8(const MxGemmArgs &g, hipStream_t st);
 
+// ---- key-value cache and attention (quant.hip, attn_decode.hip, attn_prefill.hip)
+
+// Cache append / read: codes and scales as fp4_kv_cache; `units` of 8 values are
+// numbered (k or v, head, token, 8 values of the row)
+struct KvArgs {
+    uint8_t *codes[2];   // k, v
+    uint8_t *scales[2];
+    const float *tscale[2];
+    int kv_heads, head_dim, page_shift;
+    int64_t pages;
+    int64_t tokens;
+    // append: rows in; read: rows out
+    void *x[2];
+    int64_t tok[2], head[2];  // strides in elements
+    const int64_t *slots;     // append
+    int rule;
+    int32_t *nonfinite;
+    const int32_t *table;     // read
+    int64_t table_stride;
+    int table_width, seqs;
+    const int32_t *cu;
+};
+
+fp4_status launch_kv_append(const KvArgs &a, fp4_kv_format fmt, fp4_dtype xt, hipStream_t st);
+fp4_status launch_kv_read(const KvArgs &a, fp4_kv_format fmt, fp4_dtype yt, hipStream_t st);
+
+struct DecodeArgs {
+    const uint16_t *q;
+    int64_t q_seq, q_head;
+    const uint8_t *k_codes, *v_codes, *k_scales, *v_scales;
+    const float *k_tscale, *v_tscale;  // NVFP4 only, else null
+    const int32_t *table;
+    int64_t table_stride;
+    const int32_t *seq_lens;
+    int seqs, heads, kv_heads, group, head_tiles, head_dim;
+    int page_shift, pages, max_len;  // max_len: keys a row of the block table can hold
+    float scale_log2;                // scale * log2(e)
+    int window;
+    void *out;
+    int out_bf16;
+    int64_t o_seq, o_head;
+    float *lse;
+    // partial results: slots 2 w, 2 w + 1 of workgroup w, `part_heads` heads each
+    float *part_o;   // [slot][part_heads][head_dim]
+    float *part_ml;  // [slot][part_heads][2]
+    int part_heads;
+};
+
+// workgroups of the decode kernel, and an upper bound of its work units
+int decode_grid(int64_t seqs, int64_t kv_heads, int64_t head_tiles, int64_t max_len);
+int64_t decode_units_bound(int64_t seqs, int64_t kv_heads, int64_t head_tiles, int64_t max_len);
+fp4_status launch_attn_decode(const DecodeArgs &a, fp4_kv_format fmt, hipStream_t st);
+
+struct PrefillArgs {
+    const uint16_t *q, *k, *v;
+    int64_t q_tok, q_head, k_tok, k_head, v_tok, v_head;  // strides in elements
+    const int32_t *cu_q, *cu_k;
+    int seqs, heads, kv_heads, group, head_dim;
+    int64_t q_tokens, k_tokens;
+    float scale_log2;
+    int causal, window;
+    void *out;
+    int out_bf16;
+    int64_t o_tok, o_head;
+    float *lse;
+};
+
+int64_t prefill_grid(int64_t q_tokens, int64_t seqs, int64_t kv_heads, int64_t group);
+fp4_status launch_attn_prefill(const PrefillArgs &a, hipStream_t st);
+
 }  // namespace fp4k
 
 // host-side construction of the device divider

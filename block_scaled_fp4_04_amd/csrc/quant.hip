@@ -618,6 +618,209 @@ __global__ __launch_bounds__(256) void k_mxfp4_dequant(const uint8_t *__restrict
     }
 }
 
+// ------------------------------------------------- key-value cache rows --
+//
+// New tokens' keys and values go into a paged cache in its format, and cached
+// sequences come back as rows (include/fp4blk.h, fp4_kv_cache).  Unit as above: one
+// lane, 8 values of a row.  Units are numbered (k or v, head, token, 8 values) with the
+// tokens of one head next to each other, because that is their order in a page: a
+// workgroup's 256 units are 8 to 32 whole rows (head_dim / 8 lanes each), whose codes
+// and scale bytes join up to whole lines when the slots are consecutive.
+// Both are bound by memory: 2 or 4 bytes a value on one side, 0.53 to 2 on the other.
+
+// codes of 8 values and their block's scale byte, in the cache's format; the lanes of a
+// block (two for NVFP4, four for the MX formats) are neighbours
+template <int FMT>
+__device__ __forceinline__ uint2 kv_encode8(const float (&v)[8], float s, int rule, uint32_t &byte, int &bad)
+{
+    if constexpr (FMT == FP4_KV_NVFP4) {
+        uint32_t w;
+        const float bm8 = amax8(v, bad);
+        const float six_s = 6.0f * s;
+        if (nv_fast_scale(s)) {
+            byte = nvfp4_unit_fast(v, bm8, s, six_s, rcp_refined(six_s), w);
+        } else {
+            const float bm = fmaxf(bm8, xor1(bm8));
+            byte = bm == 0.0f ? 0u : e4m3x4_code_sat(bm / six_s, 0.0f, 0.0f, 0.0f) & 0xFFu;
+            w = nvfp4_codes8(v, e4m3_value(byte) * s);
+        }
+        return make_uint2(w, 0u);
+    } else {
+        constexpr int kTop = FMT == FP4_KV_MXFP8 ? 8 : 2;  // the element type's largest exponent
+        float bm = amax8(v, bad);
+        bm = fmaxf(bm, xor1(bm));
+        bm = fmaxf(bm, xor2(bm));
+        int k = 0;
+        byte = 0;
+        if (bm != 0.0f) {
+            k = __builtin_amdgcn_frexp_expf(bm) - 1 - kTop;  // floor(log2 bm) - kTop, exact
+            if (rule == 1 && __builtin_amdgcn_frexp_mantf(bm) > (FMT == FP4_KV_MXFP8 ? 0.875f : 0.75f)) ++k;
+            k = k < -127 ? -127 : (k > 127 ? 127 : k);
+            byte = (uint32_t)(k + 127);
+        }
+        if constexpr (FMT == FP4_KV_MXFP4) {
+            float q[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) q[i] = __builtin_amdgcn_ldexpf(v[i], -k);  // exact; a zero keeps its sign
+            return make_uint2(e2m1x8_code(q), 0u);
+        } else {
+            float q[8];
+            uint32_t lo = 0, hi = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                q[i] = __builtin_amdgcn_ldexpf(__builtin_fabsf(v[i]), -k);
+                const uint32_t sign = __float_as_uint(v[i]) >> 31;
+                (i < 4 ? lo : hi) |= sign << (8 * (i & 3) + 7);
+            }
+            return make_uint2(e4m3x4_code_sat(q[0], q[1], q[2], q[3]) | lo, e4m3x4_code_sat(q[4], q[5], q[6], q[7]) | hi);
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t bf16x2_rne(float lo, float hi)
+{
+    const bf16x2 v = {(__bf16)lo, (__bf16)hi};
+    uint32_t r;
+    __builtin_memcpy(&r, &v, 4);
+    return r;
+}
+
+template <int FMT, typename T>
+__global__ __launch_bounds__(256) void k_kv_append(KvArgs a, uint32_t units, int lane_shift, FastDiv by_tokens)
+{
+    int bad_any = 0;
+    for (uint32_t u = blockIdx.x * 256u + threadIdx.x; u < units; u += gridDim.x * 256u) {
+        const uint32_t c8 = u & ((1u << lane_shift) - 1u), row = u >> lane_shift;
+        const uint32_t hp = fdiv(row, by_tokens), t = row - hp * by_tokens.d;
+        const int side = hp >= (uint32_t)a.kv_heads;
+        const int h = (int)hp - (side ? a.kv_heads : 0);
+        const int64_t slot = a.slots[t];
+        const bool stored = slot >= 0 && slot < (a.pages << a.page_shift);
+        const T *xp = reinterpret_cast<const T *>(a.x[side]) + (int64_t)t * a.tok[side] + h * a.head[side] + c8 * 8;
+        const int64_t page = stored ? slot >> a.page_shift : 0;
+        const int64_t off = stored ? slot & ((1 << a.page_shift) - 1) : 0;
+        const int64_t block = (page * a.kv_heads + h) << a.page_shift;
+        if constexpr (FMT == FP4_KV_BF16) {
+            uint4 w;
+            if constexpr (sizeof(T) == 2) {
+                w = *reinterpret_cast<const uint4 *>(xp);
+            } else {
+                float v[8];
+                Vec8<T>::load(xp, v);
+                w = make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
+            }
+            if (stored) *reinterpret_cast<uint4 *>(a.codes[side] + ((block + off) * a.head_dim + c8 * 8) * 2) = w;
+        } else {
+            constexpr int kBlkShift = FMT == FP4_KV_NVFP4 ? 1 : 2;  // lanes of a block
+            constexpr int kUnitB = FMT == FP4_KV_MXFP8 ? 8 : 4;     // code bytes of a unit
+            float v[8];
+            Vec8<T>::load(xp, v);
+            uint32_t byte;
+            int bad = 0;
+            const uint2 w = kv_encode8<FMT>(v, FMT == FP4_KV_NVFP4 ? a.tscale[side][h] : 0.0f, a.rule, byte, bad);
+            if (stored) {
+                bad_any |= bad;
+                uint8_t *cp = a.codes[side] + (((block + off) << lane_shift) + c8) * kUnitB;
+                if constexpr (kUnitB == 8) *reinterpret_cast<uint2 *>(cp) = w;
+                else *reinterpret_cast<uint32_t *>(cp) = w.x;
+                if ((c8 & ((1u << kBlkShift) - 1u)) == 0u) {
+                    const int64_t blocks = 1 << (lane_shift - kBlkShift);
+                    a.scales[side][block * blocks + ((int64_t)(c8 >> kBlkShift) << a.page_shift) + off] = (uint8_t)byte;
+                }
+            }
+        }
+    }
+    if (bad_any && a.nonfinite) *a.nonfinite = 1;
+}
+
+// The sequence b with cu[b] <= t < cu[b + 1], or -1.
+__device__ __forceinline__ int kv_seq_of(const int32_t *cu, int seqs, int64_t t)
+{
+    int lo = 0, hi = seqs;  // cu[lo] <= t < cu[hi], once both hold
+    if (t < cu[0] || t >= cu[seqs]) return -1;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (t >= cu[mid]) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+template <int FMT, bool OUT_BF16>
+__global__ __launch_bounds__(256) void k_kv_read(KvArgs a, uint32_t units, int lane_shift, FastDiv by_tokens)
+{
+    for (uint32_t u = blockIdx.x * 256u + threadIdx.x; u < units; u += gridDim.x * 256u) {
+        const uint32_t c8 = u & ((1u << lane_shift) - 1u), row = u >> lane_shift;
+        const uint32_t hp = fdiv(row, by_tokens), t = row - hp * by_tokens.d;
+        const int side = hp >= (uint32_t)a.kv_heads;
+        const int h = (int)hp - (side ? a.kv_heads : 0);
+        float o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        uint4 raw = make_uint4(0, 0, 0, 0);  // a bf16 cache's values, as they are
+        const int b = kv_seq_of(a.cu, a.seqs, t);
+        int64_t page = -1;
+        int64_t pos = 0;
+        if (b >= 0) {
+            pos = (int64_t)t - a.cu[b];
+            const int64_t i = pos >> a.page_shift;
+            if (i < a.table_width) page = a.table[b * a.table_stride + i];
+        }
+        if (page >= 0 && page < a.pages) {
+            const int64_t off = pos & ((1 << a.page_shift) - 1);
+            const int64_t block = (page * a.kv_heads + h) << a.page_shift;
+            if constexpr (FMT == FP4_KV_BF16) {
+                raw = *reinterpret_cast<const uint4 *>(a.codes[side] + ((block + off) * a.head_dim + c8 * 8) * 2);
+            } else {
+                typedef float f32x2 __attribute__((ext_vector_type(2)));
+                constexpr int kBlkShift = FMT == FP4_KV_NVFP4 ? 1 : 2;
+                const int64_t blocks = 1 << (lane_shift - kBlkShift);
+                const uint32_t byte = a.scales[side][block * blocks + ((int64_t)(c8 >> kBlkShift) << a.page_shift) + off];
+                const uint8_t *cp = a.codes[side] + (((block + off) << lane_shift) + c8) * (FMT == FP4_KV_MXFP8 ? 8 : 4);
+                if constexpr (FMT == FP4_KV_MXFP8) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(cp);
+                    const f32x2 p0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.x, false), p1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.x, true);
+                    const f32x2 p2 = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.y, false), p3 = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.y, true);
+                    o[0] = p0[0]; o[1] = p0[1]; o[2] = p1[0]; o[3] = p1[1];
+                    o[4] = p2[0]; o[5] = p2[1]; o[6] = p3[0]; o[7] = p3[1];
+                } else {
+                    const uint32_t w = *reinterpret_cast<const uint32_t *>(cp);
+                    const f32x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0), p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
+                    const f32x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2), p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
+                    o[0] = p0[0]; o[1] = p0[1]; o[2] = p1[0]; o[3] = p1[1];
+                    o[4] = p2[0]; o[5] = p2[1]; o[6] = p3[0]; o[7] = p3[1];
+                }
+                if constexpr (FMT == FP4_KV_NVFP4) {
+                    const float bs = e4m3_value(byte), s = a.tscale[side][h];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[i] = o[i] * bs * s;  // the inner product is exact
+                } else {
+                    // 2^(byte - 127): exact also where it is subnormal (byte 0); byte 0xFF is NaN
+                    const float f = __uint_as_float(byte == 255u ? 0x7FC00000u : (byte ? byte << 23 : 0x00400000u));
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[i] *= f;
+                }
+            }
+        }
+        const int64_t at = (int64_t)t * a.tok[side] + h * a.head[side] + c8 * 8;
+        if constexpr (OUT_BF16) {
+            if constexpr (FMT != FP4_KV_BF16)
+                raw = make_uint4(bf16x2_rne(o[0], o[1]), bf16x2_rne(o[2], o[3]), bf16x2_rne(o[4], o[5]), bf16x2_rne(o[6], o[7]));
+            *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(a.x[side]) + at) = raw;
+        } else {
+            if constexpr (FMT == FP4_KV_BF16) {
+                const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    o[2 * i] = __uint_as_float(w[i] << 16);
+                    o[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+                }
+            }
+            float *yp = reinterpret_cast<float *>(a.x[side]) + at;
+            *reinterpret_cast<float4 *>(yp) = make_float4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<float4 *>(yp + 4) = make_float4(o[4], o[5], o[6], o[7]);
+        }
+    }
+}
+
 // ------------------------------------------------------------- launchers --
 
 static unsigned grid_for(uint64_t units, unsigned cap)
@@ -777,6 +980,50 @@ fp4_status launch_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, 
     else
         hipLaunchKernelGGL(k_mxfp4_dequant<false>, dim3(g), dim3(256), 0, st, codes, scales, units,
                            cv, cols, y, ldy);
+    return hipGetLastError() == hipSuccess ? FP4_OK : FP4_ERR_HIP;
+}
+
+static int kv_lane_shift(const KvArgs &a) { return a.head_dim == 64 ? 3 : a.head_dim == 128 ? 4 : 5; }
+
+template <int FMT>
+static void launch_append_fmt(const KvArgs &a, fp4_dtype xt, uint32_t units, hipStream_t st)
+{
+    const FastDiv ct = make_fastdiv((uint32_t)a.tokens);
+    const unsigned g = grid_for(units, 16384);
+    if (xt == FP4_BF16)
+        hipLaunchKernelGGL((k_kv_append<FMT, uint16_t>), dim3(g), dim3(256), 0, st, a, units, kv_lane_shift(a), ct);
+    else
+        hipLaunchKernelGGL((k_kv_append<FMT, float>), dim3(g), dim3(256), 0, st, a, units, kv_lane_shift(a), ct);
+}
+
+fp4_status launch_kv_append(const KvArgs &a, fp4_kv_format fmt, fp4_dtype xt, hipStream_t st)
+{
+    const uint32_t units = (uint32_t)(2 * a.kv_heads * a.tokens) << kv_lane_shift(a);
+    if (fmt == FP4_KV_BF16) launch_append_fmt<FP4_KV_BF16>(a, xt, units, st);
+    else if (fmt == FP4_KV_MXFP8) launch_append_fmt<FP4_KV_MXFP8>(a, xt, units, st);
+    else if (fmt == FP4_KV_NVFP4) launch_append_fmt<FP4_KV_NVFP4>(a, xt, units, st);
+    else launch_append_fmt<FP4_KV_MXFP4>(a, xt, units, st);
+    return hipGetLastError() == hipSuccess ? FP4_OK : FP4_ERR_HIP;
+}
+
+template <int FMT>
+static void launch_read_fmt(const KvArgs &a, fp4_dtype yt, uint32_t units, hipStream_t st)
+{
+    const FastDiv ct = make_fastdiv((uint32_t)a.tokens);
+    const unsigned g = grid_for(units, 16384);
+    if (yt == FP4_BF16)
+        hipLaunchKernelGGL((k_kv_read<FMT, true>), dim3(g), dim3(256), 0, st, a, units, kv_lane_shift(a), ct);
+    else
+        hipLaunchKernelGGL((k_kv_read<FMT, false>), dim3(g), dim3(256), 0, st, a, units, kv_lane_shift(a), ct);
+}
+
+fp4_status launch_kv_read(const KvArgs &a, fp4_kv_format fmt, fp4_dtype yt, hipStream_t st)
+{
+    const uint32_t units = (uint32_t)(2 * a.kv_heads * a.tokens) << kv_lane_shift(a);
+    if (fmt == FP4_KV_BF16) launch_read_fmt<FP4_KV_BF16>(a, yt, units, st);
+    else if (fmt == FP4_KV_MXFP8) launch_read_fmt<FP4_KV_MXFP8>(a, yt, units, st);
+    else if (fmt == FP4_KV_NVFP4) launch_read_fmt<FP4_KV_NVFP4>(a, yt, units, st);
+    else launch_read_fmt<FP4_KV_MXFP4>(a, yt, units, st);
     return hipGetLastError() == hipSuccess ? FP4_OK : FP4_ERR_HIP;
 }
 

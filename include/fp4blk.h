@@ -432,6 +432,126 @@ fp4_status nvfp4_grouped_gemm_w4a4_prequant(const uint8_t *a_codes, const uint8_
                                             const uint8_t *w_scales, const float *w_tscale, int64_t N,
                                             void *c, fp4_dtype ct, int64_t ldc, hipStream_t stream);
 
+/* --------------------------------------- key-value cache and attention ---
+ *
+ * What surrounds the quantized linear layers when a model is served: a paged cache
+ * of keys and values, kept in one of the library's block-scaled formats ("NVFP4",
+ * Technical principle; edge-FP4 article, eefocus.com, "FP4 as the next core
+ * standard" for the E8M0 formats, and "Compute, memory and precision": the decode
+ * phase is bound by the bytes it reads, and in long contexts those are the cache's),
+ * the attention of a new token that reads it, and the attention of whole prompts.
+ *
+ * Cache layout.  A page holds page_size tokens of every key head; a token's slot is
+ * page * page_size + offset.  Keys and values alike:
+ *  - codes  [pages][kv_heads][page_size][row bytes]: FP4_KV_BF16 rows of head_dim
+ *           bf16, FP4_KV_MXFP8 head_dim E4M3FN bytes, FP4_KV_NVFP4 / FP4_KV_MXFP4
+ *           head_dim/2 bytes (low nibble even);
+ *  - scales [pages][kv_heads][head_dim/block][page_size] bytes: E8M0 per 32 values
+ *           (MX formats), E4M3FN per 16 (NVFP4); null for FP4_KV_BF16.  Tokens run
+ *           along the last axis, so that the scales of neighbouring tokens are read
+ *           together;
+ *  - tscale [kv_heads] fp32, NVFP4 only: the second-level scale, given by the caller
+ *           (a token cannot change it after others are stored).  Finite and >= 0.
+ * Blocks run along head_dim; recipes as nvfp4_quantize (with the given tscale: values
+ * past 2688 tscale saturate), mxfp4_quantize and mxfp8_quantize.
+ *
+ * Limits (FP4_ERR_SHAPE): head_dim 64, 128 or 256; page_size a power of two in
+ * [16, 256]; pages * page_size < 2^31.  All base pointers 16-byte aligned, all token and
+ * head strides (in elements) keep rows of head_dim 16-byte aligned and are >= 0
+ * (0 repeats a row; outputs need strides of at least head_dim); the innermost stride
+ * is 1.  Other values are FP4_ERR_LAYOUT. */
+typedef enum { FP4_KV_BF16 = 0, FP4_KV_MXFP8 = 1, FP4_KV_NVFP4 = 2, FP4_KV_MXFP4 = 3 } fp4_kv_format;
+
+typedef struct {
+    fp4_kv_format format;
+    int64_t pages, kv_heads, page_size, head_dim;
+    void *k_codes, *v_codes;
+    uint8_t *k_scales, *v_scales;     /* null for FP4_KV_BF16 */
+    const float *k_tscale, *v_tscale; /* FP4_KV_NVFP4 only */
+} fp4_kv_cache;
+
+/* Quantize new tokens' keys and values into the cache.
+ *  k, v   [tokens][kv_heads][head_dim] fp32 or bf16 (xt), read only, any token and
+ *         head stride (rows of a fused projection's output are taken in place).
+ *  slots  device int64 [tokens]; a slot outside [0, pages * page_size) skips its token
+ *         (padding).  Slots of one call must differ.
+ *  rule   of the MX formats' block exponents.  FP4_KV_BF16 stores bf16 inputs bit for
+ *         bit and rounds fp32 ones to nearest even.
+ *  nonfinite optional device int32, set to 1 if a token that is stored holds NaN/Inf
+ *         (quantized formats; their stored values are then unspecified).
+ * tokens == 0 returns FP4_OK once the cache, xt and rule check out. */
+fp4_status kv_cache_append(const fp4_kv_cache *cache, const void *k, const void *v, fp4_dtype xt,
+                           int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,
+                           int64_t v_token_stride, int64_t v_head_stride, const int64_t *slots,
+                           fp4_mx_rule rule, int32_t *nonfinite, hipStream_t stream);
+
+/* Read cached sequences back as packed rows of fp32 or bf16 (yt): row t of k and v
+ * [tokens][kv_heads][head_dim] is position t - cu_seqlens[b] of sequence b, where
+ * cu_seqlens[b] <= t < cu_seqlens[b+1].
+ *  block_table device int32 [seqs][table_stride]: page of positions i * page_size ..,
+ *         i < table_width.  Entries past a sequence's last page are not read.
+ *  cu_seqlens device int32 [seqs+1], nondecreasing.
+ * Values as nvfp4_dequantize / mxfp4_dequantize: exact in fp32, bf16 rounded to nearest
+ * even.  A row that no sequence holds, or whose page is outside the table or the cache,
+ * is zero.  tokens == 0 returns FP4_OK once the other arguments check out. */
+fp4_status kv_cache_read(const fp4_kv_cache *cache, const int32_t *block_table, int64_t seqs,
+                         int64_t table_width, int64_t table_stride, const int32_t *cu_seqlens,
+                         int64_t tokens, void *k, void *v, fp4_dtype yt, int64_t k_token_stride,
+                         int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                         hipStream_t stream);
+
+/* Workspace bytes of attn_decode_paged on the current device (0 on bad sizes). */
+size_t attn_decode_paged_workspace(int64_t seqs, int64_t heads, const fp4_kv_cache *cache,
+                                   int64_t table_width);
+
+/* Attention of one new token per sequence over the cache (its own key and value
+ * already appended):  with keys j in [max(0, len - window), len) (window 0: all),
+ *   out[b][h] = sum_j softmax_j(scale * q[b][h] . k_j) v_j
+ * over the cache's key head h / (heads / kv_heads).  heads % kv_heads == 0.
+ *  q      [seqs][heads][head_dim] bf16, any strides as above.
+ *  block_table, table_width, table_stride: as kv_cache_read.
+ *  seq_lens device int32 [seqs], keys of each sequence, the new one included; clamped
+ *         to [0, table_width * page_size].  Length 0 gives a zero row and lse = -inf.
+ *         Page ids are clamped into the cache: a bad id gives wrong values, no access
+ *         outside the buffers.
+ *  scale  in [0, 1e30] (FP4_ERR_SHAPE otherwise).
+ *  out    [seqs][heads][head_dim] fp32 or bf16 (ot).
+ *  lse    optional fp32 [seqs][heads]: log sum_j exp(scale q.k_j), natural logarithm,
+ *         with which results over parts of a context can be joined.
+ *  ws     attn_decode_paged_workspace() bytes, 16-byte aligned.
+ * Scores, softmax sums and output sums are fp32; the softmax weights are rounded to 16
+ * bits (bf16; f16 for NVFP4) as operands of the matrix core.  Nothing outside a
+ * sequence's range is ever used, whatever it holds.  The same inputs give the same
+ * bits.  seqs * kv_heads * (table_width * page_size / 128) < 2^31 (FP4_ERR_SHAPE). */
+fp4_status attn_decode_paged(const void *q, int64_t seqs, int64_t heads, int64_t q_seq_stride,
+                             int64_t q_head_stride, const fp4_kv_cache *cache, const int32_t *block_table,
+                             int64_t table_width, int64_t table_stride, const int32_t *seq_lens, float scale,
+                             int64_t window, void *out, fp4_dtype ot, int64_t o_seq_stride,
+                             int64_t o_head_stride, float *lse, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* Attention of whole prompts, packed one behind the other.
+ *  q      [q_tokens][heads][head_dim], k, v [k_tokens][kv_heads][head_dim], bf16, any
+ *         strides as above; heads % kv_heads == 0; head_dim 64, 128 or 256.
+ *  cu_q, cu_k device int32 [seqs+1], nondecreasing from 0 to q_tokens / k_tokens:
+ *         sequence b has lq = cu_q[b+1] - cu_q[b] queries and lk = cu_k[b+1] - cu_k[b]
+ *         keys.  The last query stands at the last key (query i at position
+ *         i + lk - lq), so a prompt's next chunk attends to what is cached before it.
+ *         Other offsets give unspecified results but no access outside the buffers.
+ *  causal 0 or 1: key j is seen when j <= position.  window > 0: and when
+ *         j > position - window.
+ *  scale, out (fp32 or bf16), lse (fp32 [q_tokens][heads]): as attn_decode_paged.  A
+ *         query that sees no key gives a zero row and lse = -inf.
+ * k and v must be finite within a sequence's range.  q_tokens == 0 returns FP4_OK once
+ * the other arguments check out; k_tokens == 0 gives zero rows.
+ * q_tokens * heads / kv_heads and k_tokens < 2^31 (FP4_ERR_SHAPE). */
+fp4_status attn_prefill(const void *q, int64_t q_tokens, int64_t heads, int64_t q_token_stride,
+                        int64_t q_head_stride, const void *k, const void *v, int64_t k_tokens,
+                        int64_t kv_heads, int64_t head_dim, int64_t k_token_stride, int64_t k_head_stride,
+                        int64_t v_token_stride, int64_t v_head_stride, const int32_t *cu_q,
+                        const int32_t *cu_k, int64_t seqs, float scale, int causal, int64_t window, void *out,
+                        fp4_dtype ot, int64_t o_token_stride, int64_t o_head_stride, float *lse,
+                        hipStream_t stream);
+
 /* ---------------------------------------------------------- measurement --
  * fp4blk_read_ceiling: reads `bytes` bytes at `buf` once, with `grid`
  * workgroups of 512 threads striding over 16-byte words, and computes nothing
