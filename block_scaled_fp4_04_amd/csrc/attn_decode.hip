@@ -45,8 +45,8 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kTile = 32 * kWaves;  // keys of one work unit
+constexpr int kTile = 128;          // keys of one work unit
+constexpr int kOver = 2;            // what a row costs beside its tiles, in units
 constexpr float kLazy = 8.0f;       // log2 headroom before the running maximum moves
 
 constexpr int kv_bits(int fmt) { return fmt == FP4_KV_BF16 ? 16 : fmt == FP4_KV_MXFP8 ? 8 : 4; }
@@ -58,12 +58,18 @@ constexpr int kv_block(int fmt) { return fmt == FP4_KV_NVFP4 ? 16 : 32; }
 // an empty sequence has one (empty) tile, whose workgroup writes the zero row.
 struct SeqSpan {
     int len, start, a0, tiles;
+    __device__ __forceinline__ int cost() const { return tiles + kOver; }
 };
+
+// Block table and lengths are read through the constant address space: they do not
+// change during the kernel, and a wave-uniform index then takes a scalar load.
+typedef const __attribute__((address_space(4))) int32_t *const_i32;
+__device__ __forceinline__ const_i32 as_const(const int32_t *p) { return (const_i32)(uintptr_t)p; }
 
 __device__ __forceinline__ SeqSpan seq_span(const DecodeArgs &a, int b)
 {
     SeqSpan s;
-    int n = a.seq_lens[b];
+    int n = as_const(a.seq_lens)[b];
     n = n < 0 ? 0 : n;
     s.len = n > a.max_len ? a.max_len : n;
     s.start = a.window > 0 && s.len > a.window ? s.len - a.window : 0;
@@ -84,11 +90,11 @@ __device__ __forceinline__ int wave_inclusive_sum(int v)
 }
 
 // Total tiles of all sequences (of one row each).
-__device__ __forceinline__ int total_tiles(const DecodeArgs &a)
+__device__ __forceinline__ int total_cost(const DecodeArgs &a)
 {
     const int lane = threadIdx.x & 63;
     int sum = 0;
-    for (int b0 = 0; b0 < a.seqs; b0 += 64) sum += b0 + lane < a.seqs ? seq_span(a, b0 + lane).tiles : 0;
+    for (int b0 = 0; b0 < a.seqs; b0 += 64) sum += b0 + lane < a.seqs ? seq_span(a, b0 + lane).cost() : 0;
     sum = wave_inclusive_sum(sum);
     return __builtin_amdgcn_readlane(sum, 63);
 }
@@ -100,7 +106,7 @@ __device__ __forceinline__ void find_seq(const DecodeArgs &a, int x, int &b, int
     const int lane = threadIdx.x & 63;
     int base = 0;
     for (int b0 = 0;; b0 += 64) {
-        const int t = b0 + lane < a.seqs ? seq_span(a, b0 + lane).tiles : 0;
+        const int t = b0 + lane < a.seqs ? seq_span(a, b0 + lane).cost() : 0;
         const int inc = wave_inclusive_sum(t);
         const int sum = __builtin_amdgcn_readlane(inc, 63);
         if (x < base + sum || b0 + 64 >= a.seqs) {
@@ -116,11 +122,11 @@ __device__ __forceinline__ void find_seq(const DecodeArgs &a, int x, int &b, int
 }
 
 // Tiles before sequence b.
-__device__ __forceinline__ int tiles_before(const DecodeArgs &a, int b)
+__device__ __forceinline__ int cost_before(const DecodeArgs &a, int b)
 {
     const int lane = threadIdx.x & 63;
     int sum = 0;
-    for (int b0 = 0; b0 < b; b0 += 64) sum += b0 + lane < b ? seq_span(a, b0 + lane).tiles : 0;
+    for (int b0 = 0; b0 < b; b0 += 64) sum += b0 + lane < b ? seq_span(a, b0 + lane).cost() : 0;
     sum = wave_inclusive_sum(sum);
     return __builtin_amdgcn_readlane(sum, 63);
 }
@@ -179,16 +185,6 @@ __device__ __forceinline__ void load_dwords(const uint8_t *p, uint32_t *w)
         w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
     }
 }
-
-// The raw bytes of 32 keys and values, as they come from memory.
-template <int FMT, int D>
-struct Raw {
-    using C = Cfg<FMT, D>;
-    uint32_t k[2][C::kKW];
-    uint32_t ks[2][C::kScaled ? C::kKL * C::kKS : 1];
-    uint32_t v[8][C::kVL][C::kVW];
-    uint32_t vs[2][C::kVL];  // scale bytes of keys 4g .. 4g+3 of each sub-tile
-};
 
 // 8 values -> the 16-bit MFMA fragment (4 dwords)
 template <int FMT>
@@ -299,41 +295,136 @@ __device__ __forceinline__ float xor16_sum(float v)
 
 }  // namespace
 
+// Waves of a workgroup, and waves a SIMD is to hold (which bounds the registers).
+// FIXME measured table
 template <int FMT, int D>
-__global__ __launch_bounds__(256) void k_attn_decode(DecodeArgs a)
+struct Shape {
+    static constexpr int kHold = D < 256 ? (D * kv_bits(FMT) <= 512 ? 4 : 3) : (FMT == FP4_KV_BF16 ? 1 : 2);
+    static constexpr int kWaves = 4;
+    static constexpr int kPerCu = kHold * 4 / kWaves;  // workgroups a CU holds
+};
+
+// SPLIT: the workgroups share all units; else one workgroup per row.
+template <int FMT, int D, bool SPLIT>
+__global__ __launch_bounds__((64 * Shape<FMT, D>::kWaves), (Shape<FMT, D>::kHold)) void k_attn_decode(DecodeArgs a)
 {
     using C = Cfg<FMT, D>;
-    using R = Raw<FMT, D>;
-    __shared__ f32x4 sm_o[2][C::kDT][64];
+    constexpr int kWaves = Shape<FMT, D>::kWaves;
+    constexpr int kStride = 32 * kWaves;  // keys the workgroup takes at a time
+    static_assert(kTile % kStride == 0, "a unit is a whole number of passes");
+    __shared__ f32x4 sm_o[kWaves / 2][C::kDT][64];
     __shared__ float sm_m[kWaves][16], sm_l[kWaves][16];
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
     const int rows = a.kv_heads * a.head_tiles;
-    const int units = total_tiles(a) * rows;
-    const int grid = (int)gridDim.x < units ? (int)gridDim.x : units;
     const int wg = blockIdx.x;
-    if (wg >= grid) return;
-    const Share sh = share_of(units, grid);
-    const int u_begin = share_start(sh, wg), u_end = share_start(sh, wg + 1);
-
-    int b, before;
-    find_seq(a, u_begin / rows, b, before);
-    SeqSpan sp = seq_span(a, b);
-    int base = before * rows;  // first unit of sequence b
-    int slot = 2 * wg;
-    for (int u = u_begin; u < u_end;) {
-        while (u >= base + sp.tiles * rows) {
-            base += sp.tiles * rows;
-            sp = seq_span(a, ++b);
+    int u = wg, u_end = wg + 1, b = 0, base = 0;
+    SeqSpan sp;
+    if constexpr (SPLIT) {
+        const int units = total_cost(a) * rows;
+        const int grid = (int)gridDim.x < units ? (int)gridDim.x : units;
+        if (wg >= grid) return;
+        const Share sh = share_of(units, grid);
+        u = share_start(sh, wg);
+        u_end = share_start(sh, wg + 1);
+        int before;
+        find_seq(a, u / rows, b, before);
+        base = before * rows;  // first unit of sequence b
+        sp = seq_span(a, b);
+    } else {
+        b = wg / rows;
+        sp = seq_span(a, b);
+    }
+    // the lane's offsets from a sub-tile's first key
+    const uint32_t k_lane = n * C::kRow + g * C::kKB, v_lane = 4 * g * C::kRow + n * C::kVB;
+    const uint32_t ks_lane = ((g * C::kKV / C::kBlk) << a.page_shift) + n;
+    const uint32_t vs_lane = ((n * C::kVV / C::kBlk) << a.page_shift) + 4 * g;
+    while (u < u_end) {
+        int r, t0, t1;
+        if constexpr (SPLIT) {
+            while (u >= base + sp.cost() * rows) {
+                base += sp.cost() * rows;
+                sp = seq_span(a, ++b);
+            }
+            // a row's units: kOver that stand for its fixed cost, then its tiles
+            r = (u - base) / sp.cost();
+            const int row_u = base + r * sp.cost(), first = u - row_u;
+            const int left = u_end - row_u;
+            t0 = first > kOver ? first - kOver : 0;
+            t1 = left >= sp.cost() ? sp.tiles : left - kOver;
+            u = row_u + sp.cost();
+            if (t1 <= t0) continue;  // only (a part of) the fixed cost
+        } else {
+            r = wg - b * rows;
+            t0 = 0;
+            t1 = sp.tiles;
         }
-        const int r = (u - base) / sp.tiles;
-        const int t0 = (u - base) - r * sp.tiles;
-        int t1 = t0 + (u_end - u);
-        t1 = t1 > sp.tiles ? sp.tiles : t1;
         const int hkv = r / a.head_tiles, h0 = (r - hkv * a.head_tiles) * 16;
         const int nh = a.group - h0 < 16 ? a.group - h0 : 16;  // query heads of this tile
         const int head0 = hkv * a.group + h0;
+
+        // ---- raw bytes of 32 keys and of their values, fetched ahead of their use
+        uint32_t kr[2][C::kKW], ksr[2][C::kScaled ? C::kKL * C::kKS : 1];
+        uint32_t vr[8][C::kVL][C::kVW], vsr[2][C::kVL];
+        const const_i32 table = as_const(a.table + b * a.table_stride);
+        const int page_mask = (1 << a.page_shift) - 1, top_page = (sp.len - 1) >> a.page_shift;
+        // first row of a sub-tile within its pool, counted in tokens of one head; a sub-tile
+        // past the sequence's end reads its last page (its keys are masked)
+        auto block_of = [&](int key, int64_t &block, int &off) {
+            int page = key >> a.page_shift;
+            page = page < top_page ? page : top_page;
+            int id = table[page];
+            id = id < 0 ? 0 : (id >= a.pages ? a.pages - 1 : id);
+            block = ((int64_t)id * a.kv_heads + hkv) << a.page_shift;
+            off = key & page_mask;
+        };
+        auto fetch_k = [&](int key0) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                int64_t block;
+                int off;
+                block_of(key0 + 16 * j, block, off);
+                const uint8_t *kp = a.k_codes + (block + off) * C::kRow;
+#pragma unroll
+                for (int i = 0; i < C::kKL; ++i) load_dwords<C::kKB>(kp + i * 4 * C::kKB + k_lane, &kr[j][i * (C::kKB / 4)]);
+                if constexpr (C::kScaled) {
+                    const uint8_t *ksp = a.k_scales + block * (D / C::kBlk) + off;
+#pragma unroll
+                    for (int i = 0; i < C::kKL; ++i)
+#pragma unroll
+                        for (int e = 0; e < C::kKS; ++e)
+                            ksr[j][i * C::kKS + e] = (ksp + ((i * 4 * C::kKV / C::kBlk + e) << a.page_shift))[ks_lane];
+                }
+            }
+        };
+        auto fetch_v = [&](int key0) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                int64_t block;
+                int off;
+                block_of(key0 + 16 * j, block, off);
+                const uint8_t *vp = a.v_codes + (block + off) * C::kRow;
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int h = 0; h < C::kVL; ++h) load_dwords<C::kVB>(vp + t * C::kRow + h * 16 * C::kVB + v_lane, vr[4 * j + t][h]);
+                if constexpr (C::kScaled) {
+                    const uint8_t *vsp = a.v_scales + block * (D / C::kBlk) + off;
+#pragma unroll
+                    for (int h = 0; h < C::kVL; ++h)
+                        vsr[j][h] = *reinterpret_cast<const uint32_t *>(vsp + ((h * 16 * C::kVV / C::kBlk) << a.page_shift) + vs_lane);
+                }
+            }
+        };
+
+        int key0 = sp.a0 + t0 * kTile + wave * 32;
+        const int seg_end = sp.a0 + t1 * kTile < sp.len ? sp.a0 + t1 * kTile : sp.len;
+        const bool any = key0 < seg_end;
+        if (any) {
+            fetch_k(key0);
+            fetch_v(key0);
+        }
 
         // ---- q: the B operand, lane n = head, the same order of d as K's loads
         uint4 q[C::kSteps];
@@ -371,81 +462,52 @@ __global__ __launch_bounds__(256) void k_attn_decode(DecodeArgs a)
             }
         }
 
+        c = fmaxf(c, 0x1p-140f);  // a scale of 0: -inf of a masked key stays -inf, every other score becomes 0
+
         f32x4 o[C::kDT];
 #pragma unroll
         for (int i = 0; i < C::kDT; ++i) o[i] = f32x4{0, 0, 0, 0};
         float m = -INFINITY, l = 0.0f;
 
-        const int32_t *table = a.table + b * a.table_stride;
-        const int page_mask = (1 << a.page_shift) - 1;
-        auto load = [&](int key0, R &x) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int s = key0 + 16 * j;
-                const int last = s < sp.len ? s : sp.len - 1;  // a sub-tile past the end reads the last page
-                int id = table[last >> a.page_shift];
-                id = id < 0 ? 0 : (id >= a.pages ? a.pages - 1 : id);
-                const int off = s & page_mask;
-                const int64_t block = ((int64_t)id * a.kv_heads + hkv) << a.page_shift;
-                const uint8_t *kp = a.k_codes + (block + off) * C::kRow + n * C::kRow + g * C::kKB;
-#pragma unroll
-                for (int i = 0; i < C::kKL; ++i) load_dwords<C::kKB>(kp + i * 4 * C::kKB, &x.k[j][i * (C::kKB / 4)]);
-                const uint8_t *vp = a.v_codes + (block + off + 4 * g) * C::kRow + n * C::kVB;
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int h = 0; h < C::kVL; ++h) load_dwords<C::kVB>(vp + t * C::kRow + h * 16 * C::kVB, x.v[4 * j + t][h]);
-                if constexpr (C::kScaled) {
-                    constexpr int kBlocks = D / C::kBlk;
-                    const uint8_t *ksp = a.k_scales + block * kBlocks + off + n;
-#pragma unroll
-                    for (int i = 0; i < C::kKL; ++i)
-#pragma unroll
-                        for (int e = 0; e < C::kKS; ++e) {
-                            const int blk = (i * 4 * C::kKV + g * C::kKV) / C::kBlk + e;
-                            x.ks[j][i * C::kKS + e] = ksp[blk << a.page_shift];
-                        }
-                    const uint8_t *vsp = a.v_scales + block * kBlocks + off + 4 * g;
-#pragma unroll
-                    for (int h = 0; h < C::kVL; ++h) {
-                        const int blk = (h * 16 * C::kVV + n * C::kVV) / C::kBlk;
-                        x.vs[j][h] = *reinterpret_cast<const uint32_t *>(vsp + (blk << a.page_shift));
-                    }
-                }
-            }
-        };
-        auto compute = [&](int key0, R &x) {
-            f32x4 s[2];
+        // scores of the 32 keys in kr: s[j] holds keys 16 j + 4 g .. + 3 of head n
+        auto scores = [&](f32x4 (&s)[2]) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 s[j] = f32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int st = 0; st < C::kSteps; ++st) {
                     const int i = 8 * st / C::kKV, e = 8 * st % C::kKV;
-                    const uint32_t sc = C::kScaled ? x.ks[j][i * C::kKS + e / C::kBlk] : 0;
-                    s[j] = mfma16<C::kF16>(widen8<FMT>(&x.k[j][8 * st * C::kBits / 32], sc), q[st], s[j]);
+                    const uint32_t sc = C::kScaled ? ksr[j][i * C::kKS + e / C::kBlk] : 0;
+                    s[j] = mfma16<C::kF16>(widen8<FMT>(&kr[j][8 * st * C::kBits / 32], sc), q[st], s[j]);
                 }
             }
-            float t[8];
+        };
+        // keys out of range: no score, and their values (which may be anything) become 0
+        auto mask_scores = [&](int key, f32x4 (&s)[2]) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) t[i] = s[i >> 2][i & 3] * c;
-            if (key0 < sp.start || key0 + 32 > sp.len) {
-                // keys out of range: no score, and their values (which may be anything) become 0
+            for (int i = 0; i < 8; ++i) {
+                const int k = key + 16 * (i >> 2) + 4 * g + (i & 3);
+                s[i >> 2][i & 3] = k >= sp.start && k < sp.len ? s[i >> 2][i & 3] : -INFINITY;
+            }
+        };
+        auto mask_values = [&](int key) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int key = key0 + 16 * (i >> 2) + 4 * g + (i & 3);
-                    const bool in = key >= sp.start && key < sp.len;
-                    t[i] = in ? t[i] : -INFINITY;
+            for (int i = 0; i < 8; ++i) {
+                const int k = key + 16 * (i >> 2) + 4 * g + (i & 3);
+                const bool in = k >= sp.start && k < sp.len;
 #pragma unroll
-                    for (int h = 0; h < C::kVL; ++h) {
+                for (int h = 0; h < C::kVL; ++h) {
 #pragma unroll
-                        for (int w = 0; w < C::kVW; ++w) x.v[i][h][w] = in ? x.v[i][h][w] : 0u;
-                        if constexpr (C::kScaled)
-                            x.vs[i >> 2][h] = in ? x.vs[i >> 2][h] : x.vs[i >> 2][h] & ~(0xFFu << (8 * (i & 3)));
-                    }
+                    for (int w = 0; w < C::kVW; ++w) vr[i][h][w] = in ? vr[i][h][w] : 0u;
+                    if constexpr (C::kScaled)
+                        vsr[i >> 2][h] = in ? vsr[i >> 2][h] : vsr[i >> 2][h] & ~(0xFFu << (8 * (i & 3)));
                 }
             }
-            const float tm = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
+        };
+        // softmax weights of the scores, as the B operand of O
+        auto weights = [&](f32x4 (&s)[2]) -> uint4 {
+            const float tm = c * fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
+                                       fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
             if (__ballot(tm > m + kLazy)) {
                 const float mn = fmaxf(m, xor16_max(tm));
                 const float alpha = mn == m ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
@@ -454,16 +516,16 @@ __global__ __launch_bounds__(256) void k_attn_decode(DecodeArgs a)
 #pragma unroll
                 for (int i = 0; i < C::kDT; ++i) o[i] *= alpha;
             }
-            const float mm = m == -INFINITY ? 0.0f : m;
+            const float mm = m == -INFINITY ? 0.0f : -m;
             float p[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                p[i] = __builtin_amdgcn_exp2f(t[i] - mm);
-                l += p[i];
-            }
-            const uint4 pf = make_uint4(pack2<C::kF16>(p[0], p[1]), pack2<C::kF16>(p[2], p[3]), pack2<C::kF16>(p[4], p[5]),
-                                        pack2<C::kF16>(p[6], p[7]));
-            // O^T: a pair of d at a time, its two rows of V^T gathered from the 8 keys
+            for (int i = 0; i < 8; ++i) p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][i & 3], c, mm));
+            l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+            return make_uint4(pack2<C::kF16>(p[0], p[1]), pack2<C::kF16>(p[2], p[3]), pack2<C::kF16>(p[4], p[5]),
+                              pack2<C::kF16>(p[6], p[7]));
+        };
+        // O^T: a pair of d at a time, its two rows of V^T gathered from the 8 keys
+        auto values = [&](const uint4 &pf) {
 #pragma unroll
             for (int h = 0; h < C::kVL; ++h)
 #pragma unroll
@@ -471,7 +533,7 @@ __global__ __launch_bounds__(256) void k_attn_decode(DecodeArgs a)
                     uint32_t w[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        w[i] = widen_pair<FMT>(x.v[i][h], pr, C::kScaled ? (x.vs[i >> 2][h] >> (8 * (i & 3))) & 0xFFu : 0u);
+                        w[i] = widen_pair<FMT>(vr[i][h], pr, C::kScaled ? (vsr[i >> 2][h] >> (8 * (i & 3))) & 0xFFu : 0u);
                     uint4 lo, hi;
                     lo.x = __builtin_amdgcn_perm(w[1], w[0], 0x05040100u);
                     lo.y = __builtin_amdgcn_perm(w[3], w[2], 0x05040100u);
@@ -486,171 +548,206 @@ __global__ __launch_bounds__(256) void k_attn_decode(DecodeArgs a)
                     o[i0 + 1] = mfma16<C::kF16>(hi, pf, o[i0 + 1]);
                 }
         };
-        for (int t = t0; t < t1; ++t) {
-            const int key0 = sp.a0 + t * kTile + wave * 32;
-            if (key0 >= sp.len) break;
-            R x;
-            load(key0, x);
-            compute(key0, x);
+
+        if (any) {
+            f32x4 s[2];
+            // the next keys are requested as soon as this pass's keys are used up, the next
+            // values as soon as its values are: one set of registers, loads always in flight
+            for (; key0 + kStride < seg_end; key0 += kStride) {
+                scores(s);
+                fetch_k(key0 + kStride);
+                __builtin_amdgcn_sched_barrier(0);
+                const bool cut = key0 < sp.start;  // (a further pass follows, so the end is not cut)
+                if (cut) mask_scores(key0, s);
+                const uint4 pf = weights(s);
+                if (cut) mask_values(key0);
+                values(pf);
+                fetch_v(key0 + kStride);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            scores(s);
+            const bool cut = key0 < sp.start || key0 + 32 > sp.len;
+            if (cut) mask_scores(key0, s);
+            const uint4 pf = weights(s);
+            if (cut) mask_values(key0);
+            values(pf);
         }
 
-        // ---- the four waves' results become one
+        // ---- the waves' results become one
         l = xor16_sum(l);
         if (lane < 16) {
             sm_m[wave][n] = m;
             sm_l[wave][n] = l;
         }
         __syncthreads();
-        const float M = fmaxf(fmaxf(sm_m[0][n], sm_m[1][n]), fmaxf(sm_m[2][n], sm_m[3][n]));
+        float M = -INFINITY, L = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) M = fmaxf(M, sm_m[w][n]);
         const float Ms = M == -INFINITY ? 0.0f : M;
-        float L = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) L += sm_l[w][n] * __builtin_amdgcn_exp2f(sm_m[w][n] - Ms);
         const float beta = __builtin_amdgcn_exp2f(m - Ms);
 #pragma unroll
         for (int i = 0; i < C::kDT; ++i) o[i] *= beta;
-        if (wave >= 2)
 #pragma unroll
-            for (int i = 0; i < C::kDT; ++i) sm_o[wave - 2][i][lane] = o[i];
-        __syncthreads();
-        if (wave < 2)
+        for (int half = kWaves / 2; half >= 1; half >>= 1) {
+            if (wave >= half && wave < 2 * half) {
 #pragma unroll
-            for (int i = 0; i < C::kDT; ++i) o[i] += sm_o[wave][i][lane];
-        __syncthreads();
-        if (wave == 1)
+                for (int i = 0; i < C::kDT; ++i) sm_o[wave - half][i][lane] = o[i];
+            }
+            __syncthreads();
+            if (wave < half) {
 #pragma unroll
-            for (int i = 0; i < C::kDT; ++i) sm_o[0][i][lane] = o[i];
-        __syncthreads();
-        if (wave == 0) {
-#pragma unroll
-            for (int i = 0; i < C::kDT; ++i) o[i] += sm_o[0][i][lane];
-            if (n < nh) {
-                const bool whole = t0 == 0 && t1 == sp.tiles;
-                float *po = nullptr;
-                float f = 1.0f;
-                if (whole) {
-                    f = L > 0.0f || L != L ? 1.0f / L : 0.0f;
-                    if constexpr (C::kF16) f = L == 0.0f ? 0.0f : f * a.v_tscale[hkv];
-                    if (a.lse && g == 0) a.lse[(int64_t)b * a.heads + head0 + n] = (M + __builtin_amdgcn_logf(L)) * 0.69314718f;
-                } else {
-                    po = a.part_o + ((int64_t)slot * a.part_heads + n) * D;
-                    if (g == 0) {
-                        a.part_ml[((int64_t)slot * a.part_heads + n) * 2] = M;
-                        a.part_ml[((int64_t)slot * a.part_heads + n) * 2 + 1] = L;
-                    }
+                for (int i = 0; i < C::kDT; ++i) o[i] += sm_o[wave][i][lane];
+            }
+            if (half > 1) __syncthreads();
+        }
+        if (wave == 0 && n < nh) {
+            const bool whole = t0 == 0 && t1 == sp.tiles;
+            const int slot = 2 * wg + (t0 == 0);  // a range begins within at most one row and ends within one
+            float *po = nullptr;
+            float f = 1.0f;
+            if (whole) {
+                f = L == 0.0f ? 0.0f : 1.0f / L;
+                if constexpr (C::kF16) f *= a.v_tscale[hkv];
+                if (a.lse && g == 0) a.lse[(int64_t)b * a.heads + head0 + n] = (M + __builtin_amdgcn_logf(L)) * 0.69314718f;
+            } else {
+                po = a.part_o + ((int64_t)slot * a.part_heads + n) * D;
+                if (g == 0) {
+                    a.part_ml[((int64_t)slot * a.part_heads + n) * 2] = M;
+                    a.part_ml[((int64_t)slot * a.part_heads + n) * 2 + 1] = L;
                 }
+            }
 #pragma unroll
-                for (int h = 0; h < C::kVL; ++h)
+            for (int h = 0; h < C::kVL; ++h)
 #pragma unroll
-                    for (int rr = 0; rr < 4; ++rr) {
-                        const int d = h * 16 * C::kVV + (4 * g + rr) * C::kVV;
+                for (int rr = 0; rr < 4; ++rr) {
+                    const int d = h * 16 * C::kVV + (4 * g + rr) * C::kVV;
 #pragma unroll
-                        for (int i = 0; i < C::kVV; i += 4) {
-                            const int k = h * C::kVV + i;
-                            const float4 v = make_float4(o[k][rr] * f, o[k + 1][rr] * f, o[k + 2][rr] * f, o[k + 3][rr] * f);
-                            if (!whole) {
-                                *reinterpret_cast<float4 *>(po + d + i) = v;
-                            } else if (a.out_bf16) {
-                                uint16_t *p = reinterpret_cast<uint16_t *>(a.out) + b * a.o_seq + (head0 + n) * a.o_head + d + i;
-                                *reinterpret_cast<uint2 *>(p) = make_uint2(pack2<false>(v.x, v.y), pack2<false>(v.z, v.w));
-                            } else {
-                                float *p = reinterpret_cast<float *>(a.out) + b * a.o_seq + (head0 + n) * a.o_head + d + i;
-                                *reinterpret_cast<float4 *>(p) = v;
-                            }
+                    for (int i = 0; i < C::kVV; i += 4) {
+                        const int k = h * C::kVV + i;
+                        const float4 v = make_float4(o[k][rr] * f, o[k + 1][rr] * f, o[k + 2][rr] * f, o[k + 3][rr] * f);
+                        if (!whole) {
+                            *reinterpret_cast<float4 *>(po + d + i) = v;
+                        } else if (a.out_bf16) {
+                            uint16_t *p = reinterpret_cast<uint16_t *>(a.out) + b * a.o_seq + (head0 + n) * a.o_head + d + i;
+                            *reinterpret_cast<uint2 *>(p) = make_uint2(pack2<false>(v.x, v.y), pack2<false>(v.z, v.w));
+                        } else {
+                            float *p = reinterpret_cast<float *>(a.out) + b * a.o_seq + (head0 + n) * a.o_head + d + i;
+                            *reinterpret_cast<float4 *>(p) = v;
                         }
                     }
-            }
+                }
         }
-        __syncthreads();
-        u += t1 - t0;
-        slot = 2 * wg + 1;
+        if (SPLIT && u < u_end) __syncthreads();  // the next segment writes sm_m, sm_l and sm_o again
+        if constexpr (!SPLIT) break;
     }
 }
 
 // One workgroup per (sequence, query head): adds up the partial results of a row
-// that several workgroups of k_attn_decode share.
+// that several workgroups of k_attn_decode share.  Four d a thread, the partial
+// results dealt to 1024 / D groups of threads.
 template <int D>
 __global__ __launch_bounds__(256) void k_attn_decode_join(DecodeArgs a, int grid_full)
 {
-    constexpr int kParts = 256 / D;
-    __shared__ float sm[kParts][D];
+    constexpr int kLanes = D / 4, kParts = 256 / kLanes;
+    __shared__ f32x4 sm[kParts][kLanes];
     __shared__ float sm_l[kParts];
     const int b = blockIdx.x / a.heads, head = blockIdx.x - b * a.heads;
     const int hkv = head / a.group, hg = head - hkv * a.group, n = hg & 15;
     const int rows = a.kv_heads * a.head_tiles;
-    const int units = total_tiles(a) * rows;
+    const int units = total_cost(a) * rows;
     const int grid = grid_full < units ? grid_full : units;
     const Share sh = share_of(units, grid);
-    const int tiles = seq_span(a, b).tiles;
+    const SeqSpan sp = seq_span(a, b);
     const int r = hkv * a.head_tiles + (hg >> 4);
-    const int u0 = tiles_before(a, b) * rows + r * tiles;
-    const int w0 = share_owner(sh, u0), w1 = share_owner(sh, u0 + tiles - 1);
+    const int u0 = cost_before(a, b) * rows + r * sp.cost() + kOver;  // its first tile
+    const int w0 = share_owner(sh, u0), w1 = share_owner(sh, u0 + sp.tiles - 1);
     if (w0 == w1) return;
-    const int first = share_start(sh, w0) >= u0 ? 2 * w0 : 2 * w0 + 1;
-    auto at = [&](int w) -> int64_t { return (int64_t)(w == w0 ? first : 2 * w) * a.part_heads + n; };
+    auto at = [&](int w) -> int64_t { return (int64_t)(2 * w + (w == w0)) * a.part_heads + n; };
     float M = -INFINITY;
     for (int w = w0 + (threadIdx.x & 63); w <= w1; w += 64) M = fmaxf(M, a.part_ml[at(w) * 2]);
     M = wave_max(M);
     const float Ms = M == -INFINITY ? 0.0f : M;
-    const int d = threadIdx.x % D, part = threadIdx.x / D;
-    float acc = 0.0f, L = 0.0f;
+    const int d = threadIdx.x % kLanes, part = threadIdx.x / kLanes;
+    f32x4 acc = {0, 0, 0, 0};
+    float L = 0.0f;
+#pragma unroll 4
     for (int w = w0 + part; w <= w1; w += kParts) {
         const int64_t i = at(w);
         const float f = __builtin_amdgcn_exp2f(a.part_ml[i * 2] - Ms);
         L += f * a.part_ml[i * 2 + 1];
-        acc += f * a.part_o[i * D + d];
+        acc += f * *reinterpret_cast<const f32x4 *>(a.part_o + i * D + 4 * d);
     }
     sm[part][d] = acc;
     if (d == 0) sm_l[part] = L;
     __syncthreads();
     if (part != 0) return;
-    acc = 0.0f;
-    L = 0.0f;
+    L = sm_l[0];
 #pragma unroll
-    for (int i = 0; i < kParts; ++i) {
+    for (int i = 1; i < kParts; ++i) {
         acc += sm[i][d];
         L += sm_l[i];
     }
     float f = L == 0.0f ? 0.0f : 1.0f / L;
     if (a.v_tscale) f *= a.v_tscale[hkv];
     acc *= f;
-    const int64_t p = b * a.o_seq + head * a.o_head + d;
-    if (a.out_bf16) reinterpret_cast<__bf16 *>(a.out)[p] = (__bf16)acc;
-    else reinterpret_cast<float *>(a.out)[p] = acc;
+    const int64_t p = b * a.o_seq + head * a.o_head + 4 * d;
+    if (a.out_bf16)
+        *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(a.out) + p) = make_uint2(pack2<false>(acc[0], acc[1]), pack2<false>(acc[2], acc[3]));
+    else
+        *reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(a.out) + p) = acc;
     if (a.lse && d == 0) a.lse[(int64_t)b * a.heads + head] = (M + __builtin_amdgcn_logf(L)) * 0.69314718f;
-}
-
-int decode_grid(int64_t seqs, int64_t kv_heads, int64_t head_tiles, int64_t max_len)
-{
-    const int64_t units = seqs * kv_heads * head_tiles * ((max_len + 31 + kTile - 1) / kTile);
-    const int64_t most = 4 * (int64_t)device_cu_count();
-    return (int)(units < most ? units : most);
 }
 
 int64_t decode_units_bound(int64_t seqs, int64_t kv_heads, int64_t head_tiles, int64_t max_len)
 {
-    return seqs * kv_heads * head_tiles * ((max_len + 31 + kTile - 1) / kTile);
+    return seqs * kv_heads * head_tiles * ((max_len + 31 + kTile - 1) / kTile + kOver);
+}
+
+// Whether rows are split among workgroups: not when a row's longest context is a few
+// passes of one workgroup, whose latency is below that of a second launch.
+static bool decode_splits(int64_t max_len) { return max_len > 1024; }
+
+// Workgroups of a split launch: as many as the device holds at once.
+int decode_grid(int64_t seqs, int64_t kv_heads, int64_t head_tiles, int64_t max_len)
+{
+    if (!decode_splits(max_len)) return 0;
+    const int64_t units = decode_units_bound(seqs, kv_heads, head_tiles, max_len);
+    const int64_t most = 4 * (int64_t)device_cu_count();  // at most 4 workgroups a CU (Shape::kPerCu)
+    return (int)(units < most ? units : most);
+}
+
+template <int FMT, int D>
+static void launch_decode(const DecodeArgs &a, hipStream_t st)
+{
+    using S = Shape<FMT, D>;
+    const int rows = a.kv_heads * a.head_tiles;
+    if (!decode_splits(a.max_len)) {
+        hipLaunchKernelGGL((k_attn_decode<FMT, D, false>), dim3((unsigned)(a.seqs * rows)), dim3(64 * S::kWaves), 0, st, a);
+        return;
+    }
+    const int64_t units = decode_units_bound(a.seqs, a.kv_heads, a.head_tiles, a.max_len);
+    const int64_t most = S::kPerCu * (int64_t)device_cu_count();
+    const int grid = (int)(units < most ? units : most);
+    hipLaunchKernelGGL((k_attn_decode<FMT, D, true>), dim3(grid), dim3(64 * S::kWaves), 0, st, a);
+    hipLaunchKernelGGL(k_attn_decode_join<D>, dim3((unsigned)(a.seqs * a.heads)), dim3(256), 0, st, a, grid);
 }
 
 template <int FMT>
-static void launch_fmt(const DecodeArgs &a, int grid, hipStream_t st)
+static void launch_fmt(const DecodeArgs &a, hipStream_t st)
 {
-    if (a.head_dim == 64) hipLaunchKernelGGL((k_attn_decode<FMT, 64>), dim3(grid), dim3(256), 0, st, a);
-    else if (a.head_dim == 128) hipLaunchKernelGGL((k_attn_decode<FMT, 128>), dim3(grid), dim3(256), 0, st, a);
-    else hipLaunchKernelGGL((k_attn_decode<FMT, 256>), dim3(grid), dim3(256), 0, st, a);
+    if (a.head_dim == 64) launch_decode<FMT, 64>(a, st);
+    else if (a.head_dim == 128) launch_decode<FMT, 128>(a, st);
+    else launch_decode<FMT, 256>(a, st);
 }
 
 fp4_status launch_attn_decode(const DecodeArgs &a, fp4_kv_format fmt, hipStream_t st)
 {
-    const int grid = decode_grid(a.seqs, a.kv_heads, a.head_tiles, a.max_len);
-    if (fmt == FP4_KV_BF16) launch_fmt<FP4_KV_BF16>(a, grid, st);
-    else if (fmt == FP4_KV_MXFP8) launch_fmt<FP4_KV_MXFP8>(a, grid, st);
-    else if (fmt == FP4_KV_NVFP4) launch_fmt<FP4_KV_NVFP4>(a, grid, st);
-    else launch_fmt<FP4_KV_MXFP4>(a, grid, st);
-    const dim3 jg((unsigned)(a.seqs * a.heads));
-    if (a.head_dim == 64) hipLaunchKernelGGL(k_attn_decode_join<64>, jg, dim3(256), 0, st, a, grid);
-    else if (a.head_dim == 128) hipLaunchKernelGGL(k_attn_decode_join<128>, jg, dim3(256), 0, st, a, grid);
-    else hipLaunchKernelGGL(k_attn_decode_join<256>, jg, dim3(256), 0, st, a, grid);
+    if (fmt == FP4_KV_BF16) launch_fmt<FP4_KV_BF16>(a, st);
+    else if (fmt == FP4_KV_MXFP8) launch_fmt<FP4_KV_MXFP8>(a, st);
+    else if (fmt == FP4_KV_NVFP4) launch_fmt<FP4_KV_NVFP4>(a, st);
+    else launch_fmt<FP4_KV_MXFP4>(a, st);
     return hipGetLastError() == hipSuccess ? FP4_OK : FP4_ERR_HIP;
 }
 
