@@ -182,14 +182,15 @@ def prepare(thunk, *keep) -> Prepared:
     return Prepared(calls, (result, keep, held))
 
 
-def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+def _stream() -> int:
+    """The current device's current stream (its handle, without a Stream object around it)."""
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _ptr(t):
     if t is not None and _recording is not None:
         _recording_keep.append(t)  # prepare(): the replayed calls keep using this memory
-    return ctypes.c_void_p(0 if t is None else t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _dt(t: torch.Tensor) -> int:
@@ -210,12 +211,17 @@ def _out_dt(dtype) -> int:
 
 def _need_cuda(*ts):
     """Every tensor given is a device tensor, and all are on one device."""
-    devs = {t.device for t in ts if t is not None}
+    first = None
     for t in ts:
-        if t is not None and not t.is_cuda:
+        if t is None:
+            continue
+        d = t.get_device()  # -1 for a host tensor
+        if d < 0:
             raise ValueError("libfp4blk takes device tensors")
-    if len(devs) > 1:
-        raise ValueError(f"tensors on several devices: {sorted(str(d) for d in devs)}")
+        if first is None:
+            first = d
+        elif d != first:
+            raise ValueError(f"tensors on several devices: {sorted({str(x.device) for x in ts if x is not None})}")
 
 
 # Argument checks.  The C ABI receives bare pointers and sizes, so it cannot see a
@@ -1069,36 +1075,41 @@ _F32_BF16 = (torch.float32, torch.bfloat16)
 _BF16 = (torch.bfloat16,)
 
 
-def _i32(t: torch.Tensor, shape, what: str):
-    if t.dtype != torch.int32:
-        raise TypeError(f"{what} must be int32, got {t.dtype}")
-    _shape(t, shape, what)
-    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{what} needs unit stride along its last dimension")
+def _i32_vec(t: torch.Tensor, n: int, what: str):
+    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        if t.dtype != torch.int32:
+            raise TypeError(f"{what} must be int32, got {t.dtype}")
+        raise ValueError(f"{what} must be a contiguous vector of {n} element(s), got {tuple(t.shape)}")
 
 
-def _out_heads(out, shape, dtype, like, what="out"):
+def _out_heads(out, n: int, h: int, d: int, dtype, like, what="out"):
+    """(output, token stride, head stride): allocated when None, else checked."""
     if out is None:
         _out_dt(dtype)
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    if tuple(out.shape) != tuple(shape):
-        raise ValueError(f"{what} has shape {tuple(out.shape)}, expected {tuple(shape)}")
-    return out
+        return torch.empty((n, h, d), dtype=dtype, device=like.device), h * d, d
+    on, oh, od, st, sh = _heads(out, _F32_BF16, what)
+    if (on, oh, od) != (n, h, d):
+        raise ValueError(f"{what} has shape {tuple(out.shape)}, expected {(n, h, d)}")
+    return out, st, sh
 
 
-def _lse(lse, shape):
-    if lse is not None:
-        if lse.dtype != torch.float32 or not lse.is_contiguous():
-            raise TypeError("lse must be contiguous float32")
-        _shape(lse, shape, "lse")
+def _lse(lse, n: int, h: int):
+    if lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise TypeError("lse must be contiguous float32")
+    _shape(lse, (n, h), "lse")
 
 
 def _block_table(block_table, what="block_table"):
+    """(sequences, pages of a row, row stride)"""
+    if block_table.dtype != torch.int32:
+        raise TypeError(f"{what} must be int32, got {block_table.dtype}")
     if block_table.dim() != 2:
         raise ValueError(f"{what} must be [sequences, pages], got {tuple(block_table.shape)}")
     seqs, width = block_table.shape
-    _i32(block_table, (seqs, width), what)
-    return seqs, width, block_table.stride(0) if seqs > 1 else width
+    stride, unit = block_table.stride()
+    if width > 1 and unit != 1:
+        raise ValueError(f"{what} needs unit stride along its last dimension")
+    return seqs, width, stride if seqs > 1 else width
 
 
 def kv_cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, rule="ocp",
@@ -1106,19 +1117,18 @@ def kv_cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: tor
     """Quantize new tokens' k and v [tokens, kv_heads, head_dim] (fp32 or bf16, any token and
     head strides) into the cache at `slots` (int64 [tokens]; page * page_size + offset,
     negative: the token is skipped).  Slots of one call must differ."""
-    L = lib()
     n, h, d, kt, kh = _heads(k, _F32_BF16, "k")
     nv, hv, dv, vt, vh = _heads(v, _F32_BF16, "v")
-    if (n, h, d) != (nv, hv, dv) or k.dtype != v.dtype:
+    if n != nv or h != hv or d != dv or k.dtype != v.dtype:
         raise ValueError("k and v must have the same shape and dtype")
-    if (h, d) != (cache.kv_heads, cache.head_dim):
+    if h != cache.kv_heads or d != cache.head_dim:
         raise ValueError(f"k has {h} heads of {d}, the cache {cache.kv_heads} of {cache.head_dim}")
     if slots.dtype != torch.int64 or slots.dim() != 1 or slots.shape[0] != n or not slots.is_contiguous():
         raise ValueError(f"slots must be a contiguous int64 tensor of {n} element(s)")
     if nonfinite is not None and (nonfinite.dtype != torch.int32 or nonfinite.numel() < 1):
         raise ValueError("nonfinite must be an int32 tensor of at least one element")
     _need_cuda(cache.k_codes, k, v, slots, nonfinite)
-    _run(L.kv_cache_append, _kv(cache), _ptr(k), _ptr(v), _dt(k), n, kt, kh, vt, vh, _ptr(slots), _rule(rule),
+    _run(lib().kv_cache_append, _kv(cache), _ptr(k), _ptr(v), _dt(k), n, kt, kh, vt, vh, _ptr(slots), _rule(rule),
          _ptr(nonfinite), _stream())
     return cache
 
@@ -1130,23 +1140,22 @@ def kv_cache_read(cache: KVCache, block_table: torch.Tensor, cu_seqlens: torch.T
     being position t - cu_seqlens[b] of the sequence b that holds it.  block_table int32
     [sequences, pages], cu_seqlens int32 [sequences + 1], tokens = cu_seqlens[-1] (known to the
     caller, so that nothing waits for the device)."""
-    L = lib()
     seqs, width, stride = _block_table(block_table)
-    _i32(cu_seqlens, (seqs + 1,), "cu_seqlens")
-    shape = (int(tokens), cache.kv_heads, cache.head_dim)
-    k_out = _out_heads(k_out, shape, dtype, cache.k_codes, "k_out")
-    v_out = _out_heads(v_out, shape, k_out.dtype, cache.k_codes, "v_out")
-    _, _, _, kt, kh = _heads(k_out, _F32_BF16, "k_out")
-    _, _, _, vt, vh = _heads(v_out, (k_out.dtype,), "v_out")
+    _i32_vec(cu_seqlens, seqs + 1, "cu_seqlens")
+    tokens, h, d = int(tokens), cache.kv_heads, cache.head_dim
+    k_out, kt, kh = _out_heads(k_out, tokens, h, d, dtype, cache.k_codes, "k_out")
+    v_out, vt, vh = _out_heads(v_out, tokens, h, d, k_out.dtype, cache.k_codes, "v_out")
+    if v_out.dtype != k_out.dtype:
+        raise TypeError("k_out and v_out must have the same dtype")
     _need_cuda(cache.k_codes, block_table, cu_seqlens, k_out, v_out)
-    _run(L.kv_cache_read, _kv(cache), _ptr(block_table), seqs, width, stride, _ptr(cu_seqlens), shape[0],
+    _run(lib().kv_cache_read, _kv(cache), _ptr(block_table), seqs, width, stride, _ptr(cu_seqlens), tokens,
          _ptr(k_out), _ptr(v_out), _dt(k_out), kt, kh, vt, vh, _stream())
     return k_out, v_out
 
 
 def attn_decode_paged_workspace(cache: KVCache, seqs: int, heads: int, table_width: int) -> torch.Tensor:
-    n = lib().attn_decode_paged_workspace(seqs, heads, cache._ref, table_width)
-    return torch.empty(max(n, 1), dtype=torch.uint8, device=cache.device)
+    return torch.empty(lib().attn_decode_paged_workspace(seqs, heads, cache._ref, table_width), dtype=torch.uint8,
+                       device=cache.device)
 
 
 def attn_decode_paged(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -1158,23 +1167,24 @@ def attn_decode_paged(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor
     [sequences] (the new token included; 0 gives zeros).  scale defaults to head_dim ** -0.5;
     window > 0 attends to the last `window` keys only.  lse: optional float32 [sequences, heads]
     that receives the logarithm of the softmax sum."""
-    L = lib()
     n, h, d, qt, qh = _heads(q, _BF16, "q")
     seqs, width, stride = _block_table(block_table)
     if seqs != n:
         raise ValueError(f"q has {n} sequences, block_table {seqs}")
     if d != cache.head_dim or h == 0 or h % cache.kv_heads:
         raise ValueError(f"q has {h} heads of {d}, the cache {cache.kv_heads} of {cache.head_dim}")
-    _i32(seq_lens, (n,), "seq_lens")
-    out = _out_heads(out, q.shape, dtype, q)
-    _, _, _, ot, oh = _heads(out, _F32_BF16, "out")
-    _lse(lse, (n, h))
+    _i32_vec(seq_lens, n, "seq_lens")
+    out, ot, oh = _out_heads(out, n, h, d, dtype, q)
+    if lse is not None:
+        _lse(lse, n, h)
+    L = lib()
     need = L.attn_decode_paged_workspace(n, h, cache._ref, width)
-    workspace = _workspace(workspace, need, q)
+    if need or workspace is not None:
+        workspace = _workspace(workspace, need, q)
     _need_cuda(cache.k_codes, q, block_table, seq_lens, out, lse, workspace)
     _run(L.attn_decode_paged, _ptr(q), n, h, qt, qh, _kv(cache), _ptr(block_table), width, stride, _ptr(seq_lens),
          d ** -0.5 if scale is None else scale, window, _ptr(out), _dt(out), ot, oh, _ptr(lse), _ptr(workspace),
-         workspace.numel(), _stream())
+         need, _stream())
     return out
 
 
@@ -1186,24 +1196,23 @@ def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q
     head_dim] bf16, any token and head strides; cu_seqlens_q and cu_seqlens_k int32
     [sequences + 1].  A sequence's last query stands at its last key.  window > 0: a query sees
     the last `window` keys up to its position.  lse: optional float32 [q_tokens, heads]."""
-    L = lib()
     n, h, d, qt, qh = _heads(q, _BF16, "q")
     nk, hk, dk, kt, kh = _heads(k, _BF16, "k")
     nv, hv, dv, vt, vh = _heads(v, _BF16, "v")
-    if (nk, hk, dk) != (nv, hv, dv):
+    if nk != nv or hk != hv or dk != dv:
         raise ValueError("k and v must have the same shape")
     if dk != d or hk == 0 or h == 0 or h % hk:
         raise ValueError(f"q has {h} heads of {d}, k {hk} of {dk}")
     if cu_seqlens_q.dim() != 1 or cu_seqlens_q.shape[0] < 2:
         raise ValueError("cu_seqlens_q must hold sequences + 1 offsets")
     seqs = cu_seqlens_q.shape[0] - 1
-    _i32(cu_seqlens_q, (seqs + 1,), "cu_seqlens_q")
-    _i32(cu_seqlens_k, (seqs + 1,), "cu_seqlens_k")
-    out = _out_heads(out, q.shape, dtype, q)
-    _, _, _, ot, oh = _heads(out, _F32_BF16, "out")
-    _lse(lse, (n, h))
+    _i32_vec(cu_seqlens_q, seqs + 1, "cu_seqlens_q")
+    _i32_vec(cu_seqlens_k, seqs + 1, "cu_seqlens_k")
+    out, ot, oh = _out_heads(out, n, h, d, dtype, q)
+    if lse is not None:
+        _lse(lse, n, h)
     _need_cuda(q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse)
-    _run(L.attn_prefill, _ptr(q), n, h, qt, qh, _ptr(k), _ptr(v), nk, hk, d, kt, kh, vt, vh, _ptr(cu_seqlens_q),
+    _run(lib().attn_prefill, _ptr(q), n, h, qt, qh, _ptr(k), _ptr(v), nk, hk, d, kt, kh, vt, vh, _ptr(cu_seqlens_q),
          _ptr(cu_seqlens_k), seqs, d ** -0.5 if scale is None else scale, int(bool(causal)), window, _ptr(out),
          _dt(out), ot, oh, _ptr(lse), _stream())
     return out

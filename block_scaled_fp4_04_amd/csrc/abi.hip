@@ -1102,7 +1102,7 @@ fp4_status attn_decode_paged(const void *q, int64_t seqs, int64_t heads, int64_t
     if (!seq_lens) return FP4_ERR_NULL;
     FP4_TRY(check_device());
     const DecodeSpace sp = decode_space(seqs, heads, cache, table_width);
-    if (!ws || !aligned16(ws) || ws_bytes < sp.bytes) return FP4_ERR_WORKSPACE;
+    if (sp.bytes > 0 && (!ws || !aligned16(ws) || ws_bytes < sp.bytes)) return FP4_ERR_WORKSPACE;
     DecodeArgs a = {};
     a.q = reinterpret_cast<const uint16_t *>(q);
     a.q_seq = q_seq_stride;

@@ -500,7 +500,9 @@ fp4_status kv_cache_read(const fp4_kv_cache *cache, const int32_t *block_table, 
                          int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
                          hipStream_t stream);
 
-/* Workspace bytes of attn_decode_paged on the current device (0 on bad sizes). */
+/* Workspace bytes of attn_decode_paged on the current device: 0 when the block table is
+ * so narrow that one launch without partial results serves it (ws may be null then), and
+ * on bad sizes. */
 size_t attn_decode_paged_workspace(int64_t seqs, int64_t heads, const fp4_kv_cache *cache,
                                    int64_t table_width);
 

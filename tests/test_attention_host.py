@@ -116,7 +116,7 @@ def test_decode(fp4):
     for bad in (dict(q=FAKE + 4), dict(qs=100), dict(oh=32), dict(stride=2), dict(out=FAKE + 8)):
         assert _decode(fp4, **bad) == LAYOUT, bad
     L = fp4.lib()
-    need = L.attn_decode_paged_workspace(3, 4, _cache(fp4), 4)
+    need = L.attn_decode_paged_workspace(3, 4, _cache(fp4), 400)
     assert need > 0
     assert L.attn_decode_paged_workspace(0, 4, _cache(fp4), 4) == 0
     assert L.attn_decode_paged_workspace(3, 5, _cache(fp4), 4) == 0
