@@ -150,8 +150,7 @@ fp4_status launch_mxfp4_gemm_w4a8(const MxGemmArgs &g, hipStream_t st);
 
 // ---- key-value cache and attention (quant.hip, attn_decode.hip, attn_prefill.hip)
 
-// Cache append / read: codes and scales as fp4_kv_cache; `units` of 8 values are
-// numbered (k or v, head, token, 8 values of the row)
+// Cache append / read: codes and scales as fp4_kv_cache
 struct KvArgs {
     uint8_t *codes[2];   // k, v
     uint8_t *scales[2];

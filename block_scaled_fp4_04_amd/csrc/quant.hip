@@ -622,10 +622,10 @@ __global__ __launch_bounds__(256) void k_mxfp4_dequant(const uint8_t *__restrict
 //
 // New tokens' keys and values go into a paged cache in its format, and cached
 // sequences come back as rows (include/fp4blk.h, fp4_kv_cache).  Unit as above: one
-// lane, 8 values of a row.  Units are numbered (k or v, head, token, 8 values) with the
-// tokens of one head next to each other, because that is their order in a page: a
-// workgroup's 256 units are 8 to 32 whole rows (head_dim / 8 lanes each), whose codes
-// and scale bytes join up to whole lines when the slots are consecutive.
+// lane, 8 values of a row.  A workgroup takes consecutive tokens of one head, because
+// that is their order in a page: a pass of its 256 lanes is 8 to 32 whole rows
+// (head_dim / 8 lanes each), whose codes and scale bytes join up to whole lines when
+// the slots are consecutive.
 // Both are bound by memory: 2 or 4 bytes a value on one side, 0.53 to 2 on the other.
 
 // codes of 8 values and their block's scale byte, in the cache's format; the lanes of a
@@ -685,136 +685,198 @@ __device__ __forceinline__ uint32_t bf16x2_rne(float lo, float hi)
     return r;
 }
 
-template <int FMT, typename T>
-__global__ __launch_bounds__(256) void k_kv_append(KvArgs a, uint32_t units, int lane_shift, FastDiv by_tokens)
+// The (k or v, head) and the first token of this workgroup: U passes of 2048 / head_dim
+// tokens of one head.
+struct KvTile {
+    int side, head;
+    uint32_t t0;
+};
+__device__ __forceinline__ KvTile kv_tile(const KvArgs &a, uint32_t tiles_of_head, uint32_t tile_tokens)
 {
+    const uint32_t hp = blockIdx.x / tiles_of_head;
+    KvTile k;
+    k.side = hp >= (uint32_t)a.kv_heads;
+    k.head = (int)hp - (k.side ? a.kv_heads : 0);
+    k.t0 = (blockIdx.x - hp * tiles_of_head) * tile_tokens;
+    return k;
+}
+
+template <int FMT, typename T, int U>
+__global__ __launch_bounds__(256) void k_kv_append(KvArgs a, uint32_t tiles_of_head, int lane_shift)
+{
+    const uint32_t pass = 256u >> lane_shift;  // tokens of a pass
+    const KvTile tile = kv_tile(a, tiles_of_head, pass * U);
+    const uint32_t c8 = threadIdx.x & ((1u << lane_shift) - 1u), row = threadIdx.x >> lane_shift;
+    const T *xp = reinterpret_cast<const T *>(tile.side ? a.x[1] : a.x[0]) + tile.head * (tile.side ? a.head[1] : a.head[0]) + c8 * 8;
+    const int64_t tok = tile.side ? a.tok[1] : a.tok[0];
+    uint8_t *codes = tile.side ? a.codes[1] : a.codes[0], *scales = tile.side ? a.scales[1] : a.scales[0];
+    int64_t slot[U];
+    float v[U][8];
+    uint4 raw[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const uint32_t t = tile.t0 + i * pass + row;
+        slot[i] = -1;
+        if (t < a.tokens) {  // whole rows, so whole blocks, of lanes
+            slot[i] = a.slots[t];
+            if constexpr (FMT == FP4_KV_BF16 && sizeof(T) == 2) raw[i] = *reinterpret_cast<const uint4 *>(xp + t * tok);
+            else Vec8<T>::load(xp + t * tok, v[i]);
+        }
+    }
     int bad_any = 0;
-    for (uint32_t u = blockIdx.x * 256u + threadIdx.x; u < units; u += gridDim.x * 256u) {
-        const uint32_t c8 = u & ((1u << lane_shift) - 1u), row = u >> lane_shift;
-        const uint32_t hp = fdiv(row, by_tokens), t = row - hp * by_tokens.d;
-        const int side = hp >= (uint32_t)a.kv_heads;
-        const int h = (int)hp - (side ? a.kv_heads : 0);
-        const int64_t slot = a.slots[t];
-        const bool stored = slot >= 0 && slot < (a.pages << a.page_shift);
-        const T *xp = reinterpret_cast<const T *>(a.x[side]) + (int64_t)t * a.tok[side] + h * a.head[side] + c8 * 8;
-        const int64_t page = stored ? slot >> a.page_shift : 0;
-        const int64_t off = stored ? slot & ((1 << a.page_shift) - 1) : 0;
-        const int64_t block = (page * a.kv_heads + h) << a.page_shift;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const bool stored = slot[i] >= 0 && slot[i] < (a.pages << a.page_shift);
+        if (!stored) continue;
+        const int64_t page = slot[i] >> a.page_shift;
+        const uint32_t off = (uint32_t)slot[i] & ((1u << a.page_shift) - 1u);
+        const int64_t block = (page * a.kv_heads + tile.head) << a.page_shift;
         if constexpr (FMT == FP4_KV_BF16) {
-            uint4 w;
-            if constexpr (sizeof(T) == 2) {
-                w = *reinterpret_cast<const uint4 *>(xp);
-            } else {
-                float v[8];
-                Vec8<T>::load(xp, v);
-                w = make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
-            }
-            if (stored) *reinterpret_cast<uint4 *>(a.codes[side] + ((block + off) * a.head_dim + c8 * 8) * 2) = w;
+            if constexpr (sizeof(T) == 4)
+                raw[i] = make_uint4(bf16x2_rne(v[i][0], v[i][1]), bf16x2_rne(v[i][2], v[i][3]), bf16x2_rne(v[i][4], v[i][5]),
+                                    bf16x2_rne(v[i][6], v[i][7]));
+            *reinterpret_cast<uint4 *>(codes + ((((block + off) << lane_shift) + c8) << 4)) = raw[i];
         } else {
             constexpr int kBlkShift = FMT == FP4_KV_NVFP4 ? 1 : 2;  // lanes of a block
             constexpr int kUnitB = FMT == FP4_KV_MXFP8 ? 8 : 4;     // code bytes of a unit
-            float v[8];
-            Vec8<T>::load(xp, v);
             uint32_t byte;
-            int bad = 0;
-            const uint2 w = kv_encode8<FMT>(v, FMT == FP4_KV_NVFP4 ? a.tscale[side][h] : 0.0f, a.rule, byte, bad);
-            if (stored) {
-                bad_any |= bad;
-                uint8_t *cp = a.codes[side] + (((block + off) << lane_shift) + c8) * kUnitB;
-                if constexpr (kUnitB == 8) *reinterpret_cast<uint2 *>(cp) = w;
-                else *reinterpret_cast<uint32_t *>(cp) = w.x;
-                if ((c8 & ((1u << kBlkShift) - 1u)) == 0u) {
-                    const int64_t blocks = 1 << (lane_shift - kBlkShift);
-                    a.scales[side][block * blocks + ((int64_t)(c8 >> kBlkShift) << a.page_shift) + off] = (uint8_t)byte;
-                }
-            }
+            const float s = FMT == FP4_KV_NVFP4 ? (tile.side ? a.tscale[1] : a.tscale[0])[tile.head] : 0.0f;
+            const uint2 w = kv_encode8<FMT>(v[i], s, a.rule, byte, bad_any);
+            uint8_t *cp = codes + (((block + off) << lane_shift) + c8) * kUnitB;
+            if constexpr (kUnitB == 8) *reinterpret_cast<uint2 *>(cp) = w;
+            else *reinterpret_cast<uint32_t *>(cp) = w.x;
+            if ((c8 & ((1u << kBlkShift) - 1u)) == 0u)
+                scales[(block << (lane_shift - kBlkShift)) + ((c8 >> kBlkShift) << a.page_shift) + off] = (uint8_t)byte;
         }
     }
     if (bad_any && a.nonfinite) *a.nonfinite = 1;
 }
 
-// The sequence b with cu[b] <= t < cu[b + 1], or -1.
+// The last sequence b with cu[b] <= t (0 when there is none): 64 offsets at a time.
 __device__ __forceinline__ int kv_seq_of(const int32_t *cu, int seqs, int64_t t)
 {
-    int lo = 0, hi = seqs;  // cu[lo] <= t < cu[hi], once both hold
-    if (t < cu[0] || t >= cu[seqs]) return -1;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (t >= cu[mid]) lo = mid;
-        else hi = mid;
+    const int lane = threadIdx.x & 63;
+    int lo = 0, span = seqs;  // the answer is in [lo, lo + span)
+    while (span > 1) {
+        const int step = (span + 63) >> 6;
+        const int at = lo + lane * step;
+        const bool past = lane * step < span && cu[at] <= t;
+        const int n = __builtin_popcountll(__ballot(past));
+        const int skip = n > 0 ? (n - 1) * step : 0;
+        lo += skip;
+        span = span - skip < step ? span - skip : step;
     }
     return lo;
 }
 
-template <int FMT, bool OUT_BF16>
-__global__ __launch_bounds__(256) void k_kv_read(KvArgs a, uint32_t units, int lane_shift, FastDiv by_tokens)
+template <int FMT, bool OUT_BF16, int U>
+__global__ __launch_bounds__(256) void k_kv_read(KvArgs a, uint32_t tiles_of_head, int lane_shift)
 {
-    for (uint32_t u = blockIdx.x * 256u + threadIdx.x; u < units; u += gridDim.x * 256u) {
-        const uint32_t c8 = u & ((1u << lane_shift) - 1u), row = u >> lane_shift;
-        const uint32_t hp = fdiv(row, by_tokens), t = row - hp * by_tokens.d;
-        const int side = hp >= (uint32_t)a.kv_heads;
-        const int h = (int)hp - (side ? a.kv_heads : 0);
-        float o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        uint4 raw = make_uint4(0, 0, 0, 0);  // a bf16 cache's values, as they are
-        const int b = kv_seq_of(a.cu, a.seqs, t);
-        int64_t page = -1;
-        int64_t pos = 0;
-        if (b >= 0) {
-            pos = (int64_t)t - a.cu[b];
-            const int64_t i = pos >> a.page_shift;
-            if (i < a.table_width) page = a.table[b * a.table_stride + i];
-        }
-        if (page >= 0 && page < a.pages) {
-            const int64_t off = pos & ((1 << a.page_shift) - 1);
-            const int64_t block = (page * a.kv_heads + h) << a.page_shift;
-            if constexpr (FMT == FP4_KV_BF16) {
-                raw = *reinterpret_cast<const uint4 *>(a.codes[side] + ((block + off) * a.head_dim + c8 * 8) * 2);
-            } else {
-                typedef float f32x2 __attribute__((ext_vector_type(2)));
-                constexpr int kBlkShift = FMT == FP4_KV_NVFP4 ? 1 : 2;
-                const int64_t blocks = 1 << (lane_shift - kBlkShift);
-                const uint32_t byte = a.scales[side][block * blocks + ((int64_t)(c8 >> kBlkShift) << a.page_shift) + off];
-                const uint8_t *cp = a.codes[side] + (((block + off) << lane_shift) + c8) * (FMT == FP4_KV_MXFP8 ? 8 : 4);
-                if constexpr (FMT == FP4_KV_MXFP8) {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(cp);
-                    const f32x2 p0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.x, false), p1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.x, true);
-                    const f32x2 p2 = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.y, false), p3 = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.y, true);
-                    o[0] = p0[0]; o[1] = p0[1]; o[2] = p1[0]; o[3] = p1[1];
-                    o[4] = p2[0]; o[5] = p2[1]; o[6] = p3[0]; o[7] = p3[1];
-                } else {
-                    const uint32_t w = *reinterpret_cast<const uint32_t *>(cp);
-                    const f32x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0), p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
-                    const f32x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2), p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
-                    o[0] = p0[0]; o[1] = p0[1]; o[2] = p1[0]; o[3] = p1[1];
-                    o[4] = p2[0]; o[5] = p2[1]; o[6] = p3[0]; o[7] = p3[1];
-                }
-                if constexpr (FMT == FP4_KV_NVFP4) {
-                    const float bs = e4m3_value(byte), s = a.tscale[side][h];
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    constexpr int kBlkShift = FMT == FP4_KV_NVFP4 ? 1 : 2;
+    const uint32_t pass = 256u >> lane_shift;
+    const KvTile tile = kv_tile(a, tiles_of_head, pass * U);
+    const uint32_t c8 = threadIdx.x & ((1u << lane_shift) - 1u), row = threadIdx.x >> lane_shift;
+    const uint8_t *codes = tile.side ? a.codes[1] : a.codes[0], *scales = tile.side ? a.scales[1] : a.scales[0];
+    const int64_t tok = tile.side ? a.tok[1] : a.tok[0];
+    const int64_t out0 = tile.head * (tile.side ? a.head[1] : a.head[0]) + c8 * 8;
+    void *out = tile.side ? a.x[1] : a.x[0];
+    const int b0 = kv_seq_of(a.cu, a.seqs, tile.t0);
+    int64_t block[U];
+    uint32_t off[U];
+    bool held[U];
+    int b = b0;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] = o[i] * bs * s;  // the inner product is exact
-                } else {
-                    // 2^(byte - 127): exact also where it is subnormal (byte 0); byte 0xFF is NaN
-                    const float f = __uint_as_float(byte == 255u ? 0x7FC00000u : (byte ? byte << 23 : 0x00400000u));
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] *= f;
+    for (int i = 0; i < U; ++i) {
+        const int64_t t = tile.t0 + i * pass + row;
+        held[i] = false;
+        block[i] = 0;
+        off[i] = 0;
+        if (t < a.tokens) {
+            while (b < a.seqs && t >= a.cu[b + 1]) ++b;
+            if (b < a.seqs && t >= a.cu[b]) {
+                const int64_t pos = t - a.cu[b];
+                const int64_t at = pos >> a.page_shift;
+                if (at < a.table_width) {
+                    const int page = a.table[b * a.table_stride + at];
+                    held[i] = page >= 0 && page < a.pages;
+                    block[i] = ((int64_t)(held[i] ? page : 0) * a.kv_heads + tile.head) << a.page_shift;
+                    off[i] = (uint32_t)pos & ((1u << a.page_shift) - 1u);
                 }
             }
         }
-        const int64_t at = (int64_t)t * a.tok[side] + h * a.head[side] + c8 * 8;
+    }
+    uint4 raw[U];
+    uint32_t byte[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        raw[i] = make_uint4(0, 0, 0, 0);
+        byte[i] = 0;
+        if (held[i]) {
+            const int64_t unit = ((block[i] + off[i]) << lane_shift) + c8;
+            if constexpr (FMT == FP4_KV_BF16) {
+                raw[i] = *reinterpret_cast<const uint4 *>(codes + (unit << 4));
+            } else {
+                if constexpr (FMT == FP4_KV_MXFP8) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(codes + unit * 8);
+                    raw[i].x = w.x;
+                    raw[i].y = w.y;
+                } else {
+                    raw[i].x = *reinterpret_cast<const uint32_t *>(codes + unit * 4);
+                }
+                byte[i] = scales[(block[i] << (lane_shift - kBlkShift)) + ((c8 >> kBlkShift) << a.page_shift) + off[i]];
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const int64_t t = tile.t0 + i * pass + row;
+        if (t >= a.tokens) break;
+        const int64_t at = t * tok + out0;
+        float o[8];
+        if constexpr (FMT == FP4_KV_BF16) {
+            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                o[2 * e] = __uint_as_float(w[e] << 16);
+                o[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+            }
+        } else {
+            f32x2 p[4];
+            if constexpr (FMT == FP4_KV_MXFP8) {
+                p[0] = __builtin_amdgcn_cvt_pk_f32_fp8((int)raw[i].x, false);
+                p[1] = __builtin_amdgcn_cvt_pk_f32_fp8((int)raw[i].x, true);
+                p[2] = __builtin_amdgcn_cvt_pk_f32_fp8((int)raw[i].y, false);
+                p[3] = __builtin_amdgcn_cvt_pk_f32_fp8((int)raw[i].y, true);
+            } else {
+                p[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(raw[i].x, 1.0f, 0);
+                p[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(raw[i].x, 1.0f, 1);
+                p[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(raw[i].x, 1.0f, 2);
+                p[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(raw[i].x, 1.0f, 3);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                o[2 * e] = p[e][0];
+                o[2 * e + 1] = p[e][1];
+            }
+            if constexpr (FMT == FP4_KV_NVFP4) {
+                const float bs = e4m3_value(byte[i]), s = (tile.side ? a.tscale[1] : a.tscale[0])[tile.head];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = o[e] * bs * s;  // the inner product is exact
+            } else {
+                // 2^(byte - 127): exact also where it is subnormal (byte 0); byte 0xFF is NaN.
+                // (A row that is not held has codes and byte 0: zeros.)
+                const float f = __uint_as_float(byte[i] == 255u ? 0x7FC00000u : (byte[i] ? byte[i] << 23 : 0x00400000u));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] *= f;
+            }
+        }
         if constexpr (OUT_BF16) {
             if constexpr (FMT != FP4_KV_BF16)
-                raw = make_uint4(bf16x2_rne(o[0], o[1]), bf16x2_rne(o[2], o[3]), bf16x2_rne(o[4], o[5]), bf16x2_rne(o[6], o[7]));
-            *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(a.x[side]) + at) = raw;
+                raw[i] = make_uint4(bf16x2_rne(o[0], o[1]), bf16x2_rne(o[2], o[3]), bf16x2_rne(o[4], o[5]), bf16x2_rne(o[6], o[7]));
+            *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(out) + at) = raw[i];
         } else {
-            if constexpr (FMT == FP4_KV_BF16) {
-                const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    o[2 * i] = __uint_as_float(w[i] << 16);
-                    o[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-                }
-            }
-            float *yp = reinterpret_cast<float *>(a.x[side]) + at;
+            float *yp = reinterpret_cast<float *>(out) + at;
             *reinterpret_cast<float4 *>(yp) = make_float4(o[0], o[1], o[2], o[3]);
             *reinterpret_cast<float4 *>(yp + 4) = make_float4(o[4], o[5], o[6], o[7]);
         }
@@ -985,45 +1047,59 @@ fp4_status launch_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, 
 
 static int kv_lane_shift(const KvArgs &a) { return a.head_dim == 64 ? 3 : a.head_dim == 128 ? 4 : 5; }
 
-template <int FMT>
-static void launch_append_fmt(const KvArgs &a, fp4_dtype xt, uint32_t units, hipStream_t st)
+// Passes of a workgroup: four (their loads in flight together) when that still leaves
+// two workgroups a CU, else one, so that a small call spreads over the chip.
+static bool kv_four(const KvArgs &a)
 {
-    const FastDiv ct = make_fastdiv((uint32_t)a.tokens);
-    const unsigned g = grid_for(units, 16384);
-    if (xt == FP4_BF16)
-        hipLaunchKernelGGL((k_kv_append<FMT, uint16_t>), dim3(g), dim3(256), 0, st, a, units, kv_lane_shift(a), ct);
-    else
-        hipLaunchKernelGGL((k_kv_append<FMT, float>), dim3(g), dim3(256), 0, st, a, units, kv_lane_shift(a), ct);
+    const int64_t pass = 256 >> kv_lane_shift(a);
+    return (a.tokens + 4 * pass - 1) / (4 * pass) * 2 * a.kv_heads >= 2 * device_cu_count();
+}
+
+template <int FMT, typename T, int U>
+static void launch_append_u(const KvArgs &a, hipStream_t st)
+{
+    const uint32_t tile = (256u >> kv_lane_shift(a)) * U, tiles = (uint32_t)((a.tokens + tile - 1) / tile);
+    hipLaunchKernelGGL((k_kv_append<FMT, T, U>), dim3(tiles * 2 * a.kv_heads), dim3(256), 0, st, a, tiles, kv_lane_shift(a));
+}
+
+template <int FMT>
+static void launch_append_fmt(const KvArgs &a, fp4_dtype xt, hipStream_t st)
+{
+    const bool four = kv_four(a);
+    if (xt == FP4_BF16) four ? launch_append_u<FMT, uint16_t, 4>(a, st) : launch_append_u<FMT, uint16_t, 1>(a, st);
+    else four ? launch_append_u<FMT, float, 4>(a, st) : launch_append_u<FMT, float, 1>(a, st);
 }
 
 fp4_status launch_kv_append(const KvArgs &a, fp4_kv_format fmt, fp4_dtype xt, hipStream_t st)
 {
-    const uint32_t units = (uint32_t)(2 * a.kv_heads * a.tokens) << kv_lane_shift(a);
-    if (fmt == FP4_KV_BF16) launch_append_fmt<FP4_KV_BF16>(a, xt, units, st);
-    else if (fmt == FP4_KV_MXFP8) launch_append_fmt<FP4_KV_MXFP8>(a, xt, units, st);
-    else if (fmt == FP4_KV_NVFP4) launch_append_fmt<FP4_KV_NVFP4>(a, xt, units, st);
-    else launch_append_fmt<FP4_KV_MXFP4>(a, xt, units, st);
+    if (fmt == FP4_KV_BF16) launch_append_fmt<FP4_KV_BF16>(a, xt, st);
+    else if (fmt == FP4_KV_MXFP8) launch_append_fmt<FP4_KV_MXFP8>(a, xt, st);
+    else if (fmt == FP4_KV_NVFP4) launch_append_fmt<FP4_KV_NVFP4>(a, xt, st);
+    else launch_append_fmt<FP4_KV_MXFP4>(a, xt, st);
     return hipGetLastError() == hipSuccess ? FP4_OK : FP4_ERR_HIP;
 }
 
-template <int FMT>
-static void launch_read_fmt(const KvArgs &a, fp4_dtype yt, uint32_t units, hipStream_t st)
+template <int FMT, bool BF, int U>
+static void launch_read_u(const KvArgs &a, hipStream_t st)
 {
-    const FastDiv ct = make_fastdiv((uint32_t)a.tokens);
-    const unsigned g = grid_for(units, 16384);
-    if (yt == FP4_BF16)
-        hipLaunchKernelGGL((k_kv_read<FMT, true>), dim3(g), dim3(256), 0, st, a, units, kv_lane_shift(a), ct);
-    else
-        hipLaunchKernelGGL((k_kv_read<FMT, false>), dim3(g), dim3(256), 0, st, a, units, kv_lane_shift(a), ct);
+    const uint32_t tile = (256u >> kv_lane_shift(a)) * U, tiles = (uint32_t)((a.tokens + tile - 1) / tile);
+    hipLaunchKernelGGL((k_kv_read<FMT, BF, U>), dim3(tiles * 2 * a.kv_heads), dim3(256), 0, st, a, tiles, kv_lane_shift(a));
+}
+
+template <int FMT>
+static void launch_read_fmt(const KvArgs &a, fp4_dtype yt, hipStream_t st)
+{
+    const bool four = kv_four(a);
+    if (yt == FP4_BF16) four ? launch_read_u<FMT, true, 4>(a, st) : launch_read_u<FMT, true, 1>(a, st);
+    else four ? launch_read_u<FMT, false, 4>(a, st) : launch_read_u<FMT, false, 1>(a, st);
 }
 
 fp4_status launch_kv_read(const KvArgs &a, fp4_kv_format fmt, fp4_dtype yt, hipStream_t st)
 {
-    const uint32_t units = (uint32_t)(2 * a.kv_heads * a.tokens) << kv_lane_shift(a);
-    if (fmt == FP4_KV_BF16) launch_read_fmt<FP4_KV_BF16>(a, yt, units, st);
-    else if (fmt == FP4_KV_MXFP8) launch_read_fmt<FP4_KV_MXFP8>(a, yt, units, st);
-    else if (fmt == FP4_KV_NVFP4) launch_read_fmt<FP4_KV_NVFP4>(a, yt, units, st);
-    else launch_read_fmt<FP4_KV_MXFP4>(a, yt, units, st);
+    if (fmt == FP4_KV_BF16) launch_read_fmt<FP4_KV_BF16>(a, yt, st);
+    else if (fmt == FP4_KV_MXFP8) launch_read_fmt<FP4_KV_MXFP8>(a, yt, st);
+    else if (fmt == FP4_KV_NVFP4) launch_read_fmt<FP4_KV_NVFP4>(a, yt, st);
+    else launch_read_fmt<FP4_KV_MXFP4>(a, yt, st);
     return hipGetLastError() == hipSuccess ? FP4_OK : FP4_ERR_HIP;
 }
 
