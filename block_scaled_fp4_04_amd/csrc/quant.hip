@@ -691,21 +691,21 @@ struct KvTile {
     int side, head;
     uint32_t t0;
 };
-__device__ __forceinline__ KvTile kv_tile(const KvArgs &a, uint32_t tiles_of_head, uint32_t tile_tokens)
+__device__ __forceinline__ KvTile kv_tile(const KvArgs &a, uint32_t tile_tokens)
 {
-    const uint32_t hp = blockIdx.x / tiles_of_head;
+    const uint32_t hps = 2 * a.kv_heads, tile = blockIdx.x / hps, hp = blockIdx.x - tile * hps;
     KvTile k;
     k.side = hp >= (uint32_t)a.kv_heads;
     k.head = (int)hp - (k.side ? a.kv_heads : 0);
-    k.t0 = (blockIdx.x - hp * tiles_of_head) * tile_tokens;
+    k.t0 = tile * tile_tokens;
     return k;
 }
 
 template <int FMT, typename T, int U>
-__global__ __launch_bounds__(256) void k_kv_append(KvArgs a, uint32_t tiles_of_head, int lane_shift)
+__global__ __launch_bounds__(256) void k_kv_append(KvArgs a, int lane_shift)
 {
     const uint32_t pass = 256u >> lane_shift;  // tokens of a pass
-    const KvTile tile = kv_tile(a, tiles_of_head, pass * U);
+    const KvTile tile = kv_tile(a, pass * U);
     const uint32_t c8 = threadIdx.x & ((1u << lane_shift) - 1u), row = threadIdx.x >> lane_shift;
     const T *xp = reinterpret_cast<const T *>(tile.side ? a.x[1] : a.x[0]) + tile.head * (tile.side ? a.head[1] : a.head[0]) + c8 * 8;
     const int64_t tok = tile.side ? a.tok[1] : a.tok[0];
@@ -770,50 +770,48 @@ __device__ __forceinline__ int kv_seq_of(const int32_t *cu, int seqs, int64_t t)
 }
 
 template <int FMT, bool OUT_BF16, int U>
-__global__ __launch_bounds__(256) void k_kv_read(KvArgs a, uint32_t tiles_of_head, int lane_shift)
+__global__ __launch_bounds__(256) void k_kv_read(KvArgs a, int lane_shift)
 {
     typedef float f32x2 __attribute__((ext_vector_type(2)));
     constexpr int kBlkShift = FMT == FP4_KV_NVFP4 ? 1 : 2;
     const uint32_t pass = 256u >> lane_shift;
-    const KvTile tile = kv_tile(a, tiles_of_head, pass * U);
+    const KvTile tile = kv_tile(a, pass * U);
     const uint32_t c8 = threadIdx.x & ((1u << lane_shift) - 1u), row = threadIdx.x >> lane_shift;
     const uint8_t *codes = tile.side ? a.codes[1] : a.codes[0], *scales = tile.side ? a.scales[1] : a.scales[0];
     const int64_t tok = tile.side ? a.tok[1] : a.tok[0];
     const int64_t out0 = tile.head * (tile.side ? a.head[1] : a.head[0]) + c8 * 8;
     void *out = tile.side ? a.x[1] : a.x[0];
+
+    // one thread per token of the tile finds its slot (-1: not held)
+    __shared__ int32_t sm_slot[32 * U];
     const int b0 = kv_seq_of(a.cu, a.seqs, tile.t0);
-    int64_t block[U];
-    uint32_t off[U];
-    bool held[U];
-    int b = b0;
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-        const int64_t t = tile.t0 + i * pass + row;
-        held[i] = false;
-        block[i] = 0;
-        off[i] = 0;
-        if (t < a.tokens) {
-            while (b < a.seqs && t >= a.cu[b + 1]) ++b;
-            if (b < a.seqs && t >= a.cu[b]) {
-                const int64_t pos = t - a.cu[b];
-                const int64_t at = pos >> a.page_shift;
-                if (at < a.table_width) {
-                    const int page = a.table[b * a.table_stride + at];
-                    held[i] = page >= 0 && page < a.pages;
-                    block[i] = ((int64_t)(held[i] ? page : 0) * a.kv_heads + tile.head) << a.page_shift;
-                    off[i] = (uint32_t)pos & ((1u << a.page_shift) - 1u);
-                }
+    if (threadIdx.x < pass * U) {
+        const int64_t t = (int64_t)tile.t0 + threadIdx.x;
+        int b = b0, slot = -1;
+        while (b < a.seqs && t >= a.cu[b + 1]) ++b;
+        if (b < a.seqs && t >= a.cu[b]) {
+            const uint32_t pos = (uint32_t)(t - a.cu[b]), at = pos >> a.page_shift;
+            if (at < (uint32_t)a.table_width) {
+                const int page = a.table[b * a.table_stride + at];
+                if (page >= 0 && page < a.pages) slot = (page << a.page_shift) | (int)(pos & ((1u << a.page_shift) - 1u));
             }
         }
+        sm_slot[threadIdx.x] = slot;
     }
+    __syncthreads();
+    int slot[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) slot[i] = sm_slot[i * pass + row];
     uint4 raw[U];
     uint32_t byte[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
         raw[i] = make_uint4(0, 0, 0, 0);
         byte[i] = 0;
-        if (held[i]) {
-            const int64_t unit = ((block[i] + off[i]) << lane_shift) + c8;
+        if (slot[i] >= 0) {
+            const uint32_t off = (uint32_t)slot[i] & ((1u << a.page_shift) - 1u);
+            const int64_t block = ((int64_t)(slot[i] >> a.page_shift) * a.kv_heads + tile.head) << a.page_shift;
+            const int64_t unit = ((block + off) << lane_shift) + c8;
             if constexpr (FMT == FP4_KV_BF16) {
                 raw[i] = *reinterpret_cast<const uint4 *>(codes + (unit << 4));
             } else {
@@ -824,7 +822,7 @@ __global__ __launch_bounds__(256) void k_kv_read(KvArgs a, uint32_t tiles_of_hea
                 } else {
                     raw[i].x = *reinterpret_cast<const uint32_t *>(codes + unit * 4);
                 }
-                byte[i] = scales[(block[i] << (lane_shift - kBlkShift)) + ((c8 >> kBlkShift) << a.page_shift) + off[i]];
+                byte[i] = scales[(block << (lane_shift - kBlkShift)) + ((c8 >> kBlkShift) << a.page_shift) + off];
             }
         }
     }
@@ -1059,7 +1057,7 @@ template <int FMT, typename T, int U>
 static void launch_append_u(const KvArgs &a, hipStream_t st)
 {
     const uint32_t tile = (256u >> kv_lane_shift(a)) * U, tiles = (uint32_t)((a.tokens + tile - 1) / tile);
-    hipLaunchKernelGGL((k_kv_append<FMT, T, U>), dim3(tiles * 2 * a.kv_heads), dim3(256), 0, st, a, tiles, kv_lane_shift(a));
+    hipLaunchKernelGGL((k_kv_append<FMT, T, U>), dim3(tiles * 2 * a.kv_heads), dim3(256), 0, st, a, kv_lane_shift(a));
 }
 
 template <int FMT>
@@ -1083,7 +1081,7 @@ template <int FMT, bool BF, int U>
 static void launch_read_u(const KvArgs &a, hipStream_t st)
 {
     const uint32_t tile = (256u >> kv_lane_shift(a)) * U, tiles = (uint32_t)((a.tokens + tile - 1) / tile);
-    hipLaunchKernelGGL((k_kv_read<FMT, BF, U>), dim3(tiles * 2 * a.kv_heads), dim3(256), 0, st, a, tiles, kv_lane_shift(a));
+    hipLaunchKernelGGL((k_kv_read<FMT, BF, U>), dim3(tiles * 2 * a.kv_heads), dim3(256), 0, st, a, kv_lane_shift(a));
 }
 
 template <int FMT>
