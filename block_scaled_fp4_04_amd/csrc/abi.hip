@@ -972,6 +972,9 @@ fp4_status check_table(const int32_t *table, int64_t seqs, int64_t width, int64_
     return FP4_OK;
 }
 
+// the prompt kernel addresses a tile of 64 keys with 32-bit offsets
+constexpr int64_t kMaxTokenStride = int64_t(1) << 24;
+
 bool valid_scale(float s) { return s >= 0.0f && s <= 1.0e30f; }
 
 // Partial results of the decode kernel: two slots a workgroup
@@ -1159,6 +1162,7 @@ fp4_status attn_prefill(const void *q, int64_t q_tokens, int64_t heads, int64_t 
     if (k_tokens > 0) {
         FP4_TRY(check_heads(k, k_token_stride, k_head_stride, head_dim, 2, false));
         FP4_TRY(check_heads(v, v_token_stride, v_head_stride, head_dim, 2, false));
+        if (k_token_stride >= kMaxTokenStride || v_token_stride >= kMaxTokenStride) return FP4_ERR_LAYOUT;
     }
     FP4_TRY(check_heads(out, o_token_stride, o_head_stride, head_dim, dsize(ot), true));
     FP4_TRY(check_device());

@@ -31,10 +31,10 @@
 namespace fp4k {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void lds_void;
 
 namespace {
 
-constexpr int kKeys = 64;      // keys of a tile
 constexpr int kRows = 128;     // rows of a workgroup: four waves of 32
 constexpr float kLazy = 8.0f;  // log2 headroom before the running maximum moves
 
@@ -105,13 +105,16 @@ __device__ __forceinline__ float other_half(float v)
 template <int D>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_prefill(PrefillArgs a)
 {
+    constexpr int kKeys = D == 256 ? 32 : 64;  // keys of a tile
+    constexpr int kSub = kKeys / 32;
     constexpr int kRowB = 2 * D;             // bytes of an LDS row
     constexpr int kTileB = kKeys * kRowB;    // bytes of a tile of K or V
-    constexpr int kChunks = kRowB / 16;      // 16-byte chunks of a row
     constexpr int kCopies = kTileB / 4096;   // 1 KiB copies per wave and tile
     constexpr int kSteps = D / 16;           // MFMA steps of S
     constexpr int kDT = D / 32;              // MFMA tiles of O
-    extern __shared__ __align__(16) uint8_t sm[];  // [2 buffers][K tile, V tile]
+    // Two buffers each for K and V, as objects of their own: the compiler then knows that a
+    // copy into one does not touch the others, and does not wait for it at every LDS read.
+    __shared__ __align__(16) uint8_t sm_k0[kTileB], sm_k1[kTileB], sm_v0[kTileB], sm_v1[kTileB];
     const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int hkv = blockIdx.x % a.kv_heads;
@@ -141,8 +144,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_prefill(PrefillA
     auto ub_of = [&](int t) { return a.causal ? t + lk - lq + 1 : lk; };
     auto lb_of = [&](int t) { const int p = t + lk - lq; return a.window > 0 && p - a.window + 1 > 0 ? p - a.window + 1 : 0; };
     const int w_t0 = tok_of(row0 + wave * 32), w_t1 = tok_of(row0 + wave * 32 + 31);
-    const int w_hi = ub_of(w_t1), w_lo = lb_of(w_t0);              // any row of the wave sees keys in [w_lo, w_hi)
-    const int w_full_hi = ub_of(w_t0), w_full_lo = lb_of(w_t1);    // every row sees [w_full_lo, w_full_hi)
+    const int w_full_hi = ub_of(w_t0), w_full_lo = lb_of(w_t1);    // every row of the wave sees [w_full_lo, w_full_hi)
     const int lo = lb_of(tok_of(row0)) & ~(kKeys - 1);
     const int hi = ub_of(tok_of(row0 + kRows - 1));
 
@@ -161,65 +163,72 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_prefill(PrefillA
         for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
     float m = -INFINITY, l = 0.0f;
 
+    // K and V tiles go to LDS through a descriptor that ends with the tile's last row: rows
+    // past the sequence arrive as zeros.  A wave's copies are kStep rows apart, which
+    // leaves their swizzle alone (D = 256: alternates it).
+    constexpr int kStep = 4096 / kRowB;
+    constexpr int kOfs = D == 256 ? 2 : 1;
+    uint32_t k_ofs[kOfs], v_ofs[kOfs];
+#pragma unroll
+    for (int i = 0; i < kOfs; ++i) {
+        const int r = i * kStep + (wave * 1024 + lane * 16) / kRowB, slot = (lane * 16 % kRowB) / 16;
+        k_ofs[i] = (uint32_t)(r * (int)a.k_tok + (slot ^ swz_k<D>(r)) * 8) * 2 - i * kStep * (uint32_t)a.k_tok * 2;
+        v_ofs[i] = (uint32_t)(r * (int)a.v_tok + (slot ^ swz_v<D>(r)) * 8) * 2 - i * kStep * (uint32_t)a.v_tok * 2;
+    }
     const uint16_t *kb = a.k + k0 * a.k_tok + hkv * a.k_head;
     const uint16_t *vb = a.v + k0 * a.v_tok + hkv * a.v_head;
-    auto stage = [&](int key0, int buf) {
-        uint8_t *dst = sm + buf * 2 * kTileB;
+    auto rsrc = [&](const uint16_t *p, int64_t tok, int key0) {
+        const int n = lk - key0 < kKeys ? lk - key0 : kKeys;
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(p + key0 * tok), (short)0, ((n - 1) * (int)tok + D) * 2,
+                                                 0x00020000);
+    };
+    auto stage_k = [&](int key0, uint8_t *dst) __attribute__((always_inline)) {
+        const __amdgpu_buffer_rsrc_t r = rsrc(kb, a.k_tok, key0);
 #pragma unroll
-        for (int j = 0; j < kCopies; ++j) {
-            const int piece = (j * 4 + wave) * 1024 + lane * 16;  // byte of the tile this lane fills
-            const int r = piece / kRowB, slot = (piece % kRowB) / 16;
-            int key = key0 + r;
-            key = key < lk ? key : lk - 1;
-            const uint16_t *ks = kb + (int64_t)key * a.k_tok + (slot ^ swz_k<D>(r)) * 8;
-            const uint16_t *vs = vb + (int64_t)key * a.v_tok + (slot ^ swz_v<D>(r)) * 8;
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)ks,
-                                             (__attribute__((address_space(3))) void *)(dst + (j * 4 + wave) * 1024), 16, 0, 0);
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)vs,
-                                             (__attribute__((address_space(3))) void *)(dst + kTileB + (j * 4 + wave) * 1024), 16, 0, 0);
-        }
+        for (int j = 0; j < kCopies; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(dst + wave * 1024 + j * 4096), 16, (int)k_ofs[j % kOfs],
+                                                     j * kStep * (int)a.k_tok * 2, 0, 0);
+    };
+    auto stage_v = [&](int key0, uint8_t *dst) __attribute__((always_inline)) {
+        const __amdgpu_buffer_rsrc_t r = rsrc(vb, a.v_tok, key0);
+#pragma unroll
+        for (int j = 0; j < kCopies; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(dst + wave * 1024 + j * 4096), 16, (int)v_ofs[j % kOfs],
+                                                     j * kStep * (int)a.v_tok * 2, 0, 0);
     };
 
-    if (lo < hi) stage(lo, 0);
-    int buf = 0;
-    for (int key0 = lo; key0 < hi; key0 += kKeys, buf ^= 1) {
-        __syncthreads();  // this tile has arrived; the other buffer is free
-        if (key0 + kKeys < hi) stage(key0 + kKeys, buf ^ 1);
-        if (key0 >= w_hi || key0 + kKeys <= w_lo) continue;
-        const uint8_t *kt = sm + buf * 2 * kTileB, *vt = kt + kTileB;
-
-        f32x16 s[2];
+    const float c = fmaxf(a.scale_log2, 0x1p-140f);  // a scale of 0: a masked key's -inf stays
+    const int c16 = lane & 15, dgrp = (lane >> 4) & 1;
+    auto scores = [&](const uint8_t *kt, f32x16 (&s)[kSub]) __attribute__((always_inline)) {
+        const uint8_t *kr = kt + col * kRowB;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int e = 0; e < 16 * kSub; ++e) s[e >> 4][e & 15] = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) s[j][e] = 0.0f;
-            const int r = 32 * j + col;
-            const uint8_t *kr = kt + r * kRowB;
+        for (int st = 0; st < kSteps; ++st)
 #pragma unroll
-            for (int st = 0; st < kSteps; ++st) {
-                const uint4 f = *reinterpret_cast<const uint4 *>(kr + (((2 * st + half) ^ swz_k<D>(r)) * 16));
+            for (int j = 0; j < kSub; ++j) {
+                // (the swizzle acts on the low four bits of a chunk's number: beyond, a constant offset)
+                const uint4 f = *reinterpret_cast<const uint4 *>(kr + 32 * j * kRowB + (st >> 3) * 256 + ((((2 * st & 15) + half) ^ swz_k<D>(col)) * 16));
                 s[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(f), as_bf16x8(q[st]), s[j], 0, 0, 0);
             }
-        }
-        const float c = a.scale_log2;
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) s[j][e] *= c;
+    };
+    // masks the scores of tile key0 and moves the running maximum
+    auto settle = [&](int key0, f32x16 (&s)[kSub]) __attribute__((always_inline)) {
         if (key0 < w_full_lo || key0 + kKeys > w_full_hi) {
+            // of the lane's keys 8 x + 4 half + i, those in [lb, ub)
+            const int first = lb - key0 - 4 * half, last = ub - key0 - 4 * half;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < kSub; ++j)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const int key = key0 + 32 * j + 8 * (e >> 2) + 4 * half + (e & 3);
-                    s[j][e] = key >= lb && key < ub ? s[j][e] : -INFINITY;
+                    const int key = 32 * j + 8 * (e >> 2) + (e & 3);
+                    s[j][e] = key >= first && key < last ? s[j][e] : -INFINITY;
                 }
         }
-        float tm = -INFINITY;
+        float tm = s[0][0];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) tm = fmaxf(tm, s[j][e]);
+        for (int e = 1; e < 16 * kSub; ++e) tm = fmaxf(tm, s[e >> 4][e & 15]);
+        tm *= c;
         if (__ballot(tm > m + kLazy)) {
             const float mn = fmaxf(m, fmaxf(tm, other_half(tm)));
             const float alpha = mn == m ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
@@ -230,38 +239,75 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_prefill(PrefillA
 #pragma unroll
                 for (int e = 0; e < 16; ++e) o[i][e] *= alpha;
         }
-        const float mm = m == -INFINITY ? 0.0f : m;
-        // P of step st: keys 16 st + 8 (j >> 2) + 4 half + (j & 3), registers 8 (st & 1) .. + 7 of s[st >> 1]
-        uint4 p[4];
+    };
+    // P of step st: keys 16 st + 8 (j >> 2) + 4 half + (j & 3), registers 8 (st & 1) .. + 7 of s[st >> 1]
+    auto weights = [&](const f32x16 (&s)[kSub], uint4 (&p)[2 * kSub]) __attribute__((always_inline)) {
+        const float mm = m == -INFINITY ? 0.0f : -m;
 #pragma unroll
-        for (int st = 0; st < 4; ++st) {
+        for (int st = 0; st < 2 * kSub; ++st) {
             float e[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                e[i] = __builtin_amdgcn_exp2f(s[st >> 1][8 * (st & 1) + i] - mm);
-                l += e[i];
-            }
+            for (int i = 0; i < 8; ++i) e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[st >> 1][8 * (st & 1) + i], c, mm));
+            l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
             p[st] = make_uint4(pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7]));
         }
-        // V^T: lane c of a 16-lane group addresses key c >> 2 of 4, d 4 (c & 3) of 16
-        const int c16 = lane & 15, dgrp = (lane >> 4) & 1;
+    };
+    // V^T: lane c of a 16-lane group addresses key c >> 2 of 4, d 4 (c & 3) of 16
+    auto values = [&](const uint8_t *vt, const uint4 (&p)[2 * kSub]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int st = 0; st < 4; ++st) {
+        for (int st = 0; st < 2 * kSub; ++st)
 #pragma unroll
             for (int i = 0; i < kDT; ++i) {
                 uint4 f;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const int r = 16 * st + 8 * x + 4 * half + (c16 >> 2);
-                    const int d = 32 * i + 16 * dgrp + 4 * (c16 & 3);
-                    const uint8_t *src = vt + r * kRowB + (((d >> 3) ^ swz_v<D>(r)) * 16) + (d & 4) * 2;
-                    const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                        (__attribute__((address_space(3))) s16x4 *)(src));
+                    const int chunk = (4 * (i & 3) + 2 * dgrp + ((c16 & 3) >> 1)) ^ swz_v<D>(c16 >> 2);
+                    const uint8_t *src = vt + (4 * half + (c16 >> 2)) * kRowB + chunk * 16 + (c16 & 1) * 8 + (16 * st + 8 * x) * kRowB + (i >> 2) * 256;
+                    const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(src));
                     if (x == 0) __builtin_memcpy(&f.x, &v, 8);
                     else __builtin_memcpy(&f.z, &v, 8);
                 }
                 o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(f), as_bf16x8(p[st]), o[i], 0, 0, 0);
             }
+    };
+
+    // The next tile's scores are formed while this tile's weights are: the matrix core and
+    // the vector units then work at once within a wave, not only between the two waves of a SIMD.
+    if (lo < hi) {
+        f32x16 s0[kSub], s1[kSub];
+        uint4 p[2 * kSub];
+        stage_k(lo, sm_k0);
+        __syncthreads();
+        if (lo + kKeys < hi) stage_k(lo + kKeys, sm_k1);
+        stage_v(lo, sm_v0);
+        scores(sm_k0, s0);
+        settle(lo, s0);
+        int key0 = lo;
+        // `now`: scores of tile key0; k_next, v_now: the buffers that hold what this pass reads
+        auto pass = [&](f32x16 (&now)[kSub], f32x16 (&next)[kSub], uint8_t *k_now, const uint8_t *k_next, const uint8_t *v_now,
+                        uint8_t *v_next) __attribute__((always_inline)) {
+            __syncthreads();  // K of the next tile and V of this one have arrived; the other buffers are free
+            if (key0 + 2 * kKeys < hi) stage_k(key0 + 2 * kKeys, k_now);
+            stage_v(key0 + kKeys, v_next);
+            scores(k_next, next);
+            weights(now, p);
+            values(v_now, p);
+            settle(key0 + kKeys, next);
+            key0 += kKeys;
+        };
+        while (key0 + 2 * kKeys < hi) {
+            pass(s0, s1, sm_k0, sm_k1, sm_v0, sm_v1);
+            pass(s1, s0, sm_k1, sm_k0, sm_v1, sm_v0);
+        }
+        if (key0 + kKeys < hi) {
+            pass(s0, s1, sm_k0, sm_k1, sm_v0, sm_v1);
+            __syncthreads();
+            weights(s1, p);
+            values(sm_v1, p);
+        } else {
+            __syncthreads();
+            weights(s0, p);
+            values(sm_v0, p);
         }
     }
 
@@ -287,10 +333,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_prefill(PrefillA
 template <int D>
 static fp4_status launch_d(const PrefillArgs &a, int64_t grid, hipStream_t st)
 {
-    constexpr int kLds = 4 * kKeys * 2 * D;
-    static std::atomic<uint64_t> done{0};
-    if (!set_max_lds_once((const void *)k_attn_prefill<D>, kLds, done)) return FP4_ERR_HIP;
-    hipLaunchKernelGGL(k_attn_prefill<D>, dim3((unsigned)grid), dim3(256), kLds, st, a);
+    hipLaunchKernelGGL(k_attn_prefill<D>, dim3((unsigned)grid), dim3(256), 0, st, a);
     return hipGetLastError() == hipSuccess ? FP4_OK : FP4_ERR_HIP;
 }
 

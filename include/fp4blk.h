@@ -533,7 +533,8 @@ fp4_status attn_decode_paged(const void *q, int64_t seqs, int64_t heads, int64_t
 
 /* Attention of whole prompts, packed one behind the other.
  *  q      [q_tokens][heads][head_dim], k, v [k_tokens][kv_heads][head_dim], bf16, any
- *         strides as above; heads % kv_heads == 0; head_dim 64, 128 or 256.
+ *         strides as above (token strides of k and v below 2^24 elements: FP4_ERR_LAYOUT);
+ *         heads % kv_heads == 0; head_dim 64, 128 or 256.
  *  cu_q, cu_k device int32 [seqs+1], nondecreasing from 0 to q_tokens / k_tokens:
  *         sequence b has lq = cu_q[b+1] - cu_q[b] queries and lk = cu_k[b+1] - cu_k[b]
  *         keys.  The last query stands at the last key (query i at position
