@@ -96,7 +96,8 @@ def _declare(L):
         "attn_decode_paged": (i32, [p, i64, i64, i64, i64, p, p, i64, i64, p, f32, i64, p, i32, i64, i64, p, p, sz,
                                     p]),
         "attn_prefill": (i32, [p, i64, i64, i64, i64, p, p, i64, i64, i64, i64, i64, i64, i64, p, p, i64, f32, i32,
-                               i64, p, i32, i64, i64, p, p]),
+                               i64, p, i32, i64, i64, p, p, sz, p]),
+        "attn_prefill_workspace": (sz, [i64, i64, i64, i64, i64, i64]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -1190,8 +1191,8 @@ def attn_decode_paged(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor
 
 def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: torch.Tensor,
                  cu_seqlens_k: torch.Tensor, causal: bool = True, window: int = 0, scale: float | None = None,
-                 dtype=torch.bfloat16, out: torch.Tensor | None = None,
-                 lse: torch.Tensor | None = None) -> torch.Tensor:
+                 dtype=torch.bfloat16, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None) -> torch.Tensor:
     """Attention of packed prompts: q [q_tokens, heads, head_dim], k and v [k_tokens, kv_heads,
     head_dim] bf16, any token and head strides; cu_seqlens_q and cu_seqlens_k int32
     [sequences + 1].  A sequence's last query stands at its last key.  window > 0: a query sees
@@ -1211,8 +1212,12 @@ def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q
     out, ot, oh = _out_heads(out, n, h, d, dtype, q)
     if lse is not None:
         _lse(lse, n, h)
-    _need_cuda(q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse)
-    _run(lib().attn_prefill, _ptr(q), n, h, qt, qh, _ptr(k), _ptr(v), nk, hk, d, kt, kh, vt, vh, _ptr(cu_seqlens_q),
+    L = lib()
+    need = L.attn_prefill_workspace(n, h, nk, hk, d, seqs)
+    if need or workspace is not None:
+        workspace = _workspace(workspace, need, q)
+    _need_cuda(q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse, workspace)
+    _run(L.attn_prefill, _ptr(q), n, h, qt, qh, _ptr(k), _ptr(v), nk, hk, d, kt, kh, vt, vh, _ptr(cu_seqlens_q),
          _ptr(cu_seqlens_k), seqs, d ** -0.5 if scale is None else scale, int(bool(causal)), window, _ptr(out),
-         _dt(out), ot, oh, _ptr(lse), _stream())
+         _dt(out), ot, oh, _ptr(lse), _ptr(workspace), need, _stream())
     return out

@@ -1141,13 +1141,22 @@ fp4_status attn_decode_paged(const void *q, int64_t seqs, int64_t heads, int64_t
     return launch_attn_decode(a, cache->format, stream);
 }
 
+size_t attn_prefill_workspace(int64_t q_tokens, int64_t heads, int64_t k_tokens, int64_t kv_heads, int64_t head_dim,
+                              int64_t seqs)
+{
+    if (q_tokens <= 0 || heads <= 0 || kv_heads <= 0 || heads % kv_heads != 0 || head_dim <= 0 || seqs <= 0) return 0;
+    const int64_t group = heads / kv_heads;
+    const int splits = prefill_splits(q_tokens, k_tokens, seqs, kv_heads, group, head_dim);
+    return align256(prefill_part_rows(q_tokens, seqs, kv_heads, group, splits) * (size_t)(head_dim + 2) * 4);
+}
+
 fp4_status attn_prefill(const void *q, int64_t q_tokens, int64_t heads, int64_t q_token_stride,
                         int64_t q_head_stride, const void *k, const void *v, int64_t k_tokens,
                         int64_t kv_heads, int64_t head_dim, int64_t k_token_stride, int64_t k_head_stride,
                         int64_t v_token_stride, int64_t v_head_stride, const int32_t *cu_q,
                         const int32_t *cu_k, int64_t seqs, float scale, int causal, int64_t window, void *out,
-                        fp4_dtype ot, int64_t o_token_stride, int64_t o_head_stride, float *lse,
-                        hipStream_t stream)
+                        fp4_dtype ot, int64_t o_token_stride, int64_t o_head_stride, float *lse, void *ws,
+                        size_t ws_bytes, hipStream_t stream)
 {
     if (!valid_dtype(ot) || (causal != 0 && causal != 1)) return FP4_ERR_DTYPE;
     if (heads <= 0 || heads > 65535 || kv_heads <= 0 || heads % kv_heads != 0) return FP4_ERR_SHAPE;
@@ -1166,7 +1175,12 @@ fp4_status attn_prefill(const void *q, int64_t q_tokens, int64_t heads, int64_t 
     }
     FP4_TRY(check_heads(out, o_token_stride, o_head_stride, head_dim, dsize(ot), true));
     FP4_TRY(check_device());
+    const size_t need = attn_prefill_workspace(q_tokens, heads, k_tokens, kv_heads, head_dim, seqs);
+    if (need > 0 && (!ws || !aligned16(ws) || ws_bytes < need)) return FP4_ERR_WORKSPACE;
     PrefillArgs a = {};
+    a.splits = prefill_splits(q_tokens, k_tokens, seqs, kv_heads, group, head_dim);
+    a.part_o = reinterpret_cast<float *>(ws);
+    a.part_ml = a.part_o + prefill_part_rows(q_tokens, seqs, kv_heads, group, a.splits) * head_dim;
     a.q = reinterpret_cast<const uint16_t *>(q);
     a.k = reinterpret_cast<const uint16_t *>(k);
     a.v = reinterpret_cast<const uint16_t *>(v);

@@ -38,25 +38,28 @@ namespace {
 constexpr int kRows = 128;     // rows of a workgroup: four waves of 32
 constexpr float kLazy = 8.0f;  // log2 headroom before the running maximum moves
 
+// A row tile: its sequence (-1: past the last), its number there, and the sequence's rows,
+// clamped into the buffers.
 struct QTile {
     int b, tile;
+    int q0, lq, k0, lk;
 };
 
-// rows tiles of sequence b
-__device__ __forceinline__ int seq_tiles(const PrefillArgs &a, int b)
-{
-    const int64_t n = (int64_t)a.cu_q[b + 1] - a.cu_q[b];
-    if (n <= 0 || n > a.q_tokens) return 0;
-    return (int)((n * a.group + kRows - 1) / kRows);
-}
+__device__ __forceinline__ int clamp_offset(int v, int64_t top) { return v < 0 ? 0 : ((int64_t)v > top ? (int)top : v); }
 
-// The sequence and tile of row tile x; b = -1 past the last.
+// Row tile x of the concatenated sequences, a sequence's last tiles first: they see the most
+// keys.  (The longest sequence first as well gained nothing measurable and costs a pass
+// over the lanes.)
 __device__ __forceinline__ QTile find_tile(const PrefillArgs &a, int x)
 {
     const int lane = threadIdx.x & 63;
     int base = 0;
     for (int b0 = 0; b0 < a.seqs; b0 += 64) {
-        const int t = b0 + lane < a.seqs ? seq_tiles(a, b0 + lane) : 0;
+        const int b = b0 + lane < a.seqs ? b0 + lane : a.seqs - 1;
+        const int q0 = clamp_offset(a.cu_q[b], a.q_tokens), q1 = clamp_offset(a.cu_q[b + 1], a.q_tokens);
+        const int k0 = clamp_offset(a.cu_k[b], a.k_tokens), k1 = clamp_offset(a.cu_k[b + 1], a.k_tokens);
+        const int lq = b0 + lane < a.seqs && q1 > q0 ? q1 - q0 : 0;
+        const int t = (int)(((int64_t)lq * a.group + kRows - 1) / kRows);
         int inc = t;
         for (int off = 1; off < 64; off <<= 1) {
             const int o = __shfl_up(inc, off, kWave);
@@ -66,13 +69,18 @@ __device__ __forceinline__ QTile find_tile(const PrefillArgs &a, int x)
         if (x < base + sum) {
             int i = __builtin_popcountll(__ballot(base + inc <= x));
             i = i > 63 ? 63 : i;
-            const int tiles = __builtin_amdgcn_readlane(t, i);
-            const int at = x - base - __builtin_amdgcn_readlane(inc - t, i);
-            return {b0 + i, tiles - 1 - at};  // a sequence's last tiles see the most keys: they go first
+            QTile r;
+            r.b = b0 + i;
+            r.tile = base + __builtin_amdgcn_readlane(inc, i) - 1 - x;
+            r.q0 = __builtin_amdgcn_readlane(q0, i);
+            r.lq = __builtin_amdgcn_readlane(lq, i);
+            r.k0 = __builtin_amdgcn_readlane(k0, i);
+            r.lk = __builtin_amdgcn_readlane(k1 > k0 ? k1 - k0 : 0, i);
+            return r;
         }
         base += sum;
     }
-    return {-1, 0};
+    return {-1, 0, 0, 0, 0, 0};
 }
 
 // swizzle of the 16-byte chunks of an LDS row
@@ -117,18 +125,16 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_prefill(PrefillA
     __shared__ __align__(16) uint8_t sm_k0[kTileB], sm_k1[kTileB], sm_v0[kTileB], sm_v1[kTileB];
     const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int hkv = blockIdx.x % a.kv_heads;
-    const QTile qt = find_tile(a, blockIdx.x / a.kv_heads);
+    // blocks: (row tile, split, key head), the key head fastest
+    const int xs = blockIdx.x / a.kv_heads, hkv = blockIdx.x - xs * a.kv_heads;
+    const int x = xs / a.splits, split = xs - x * a.splits;
+    const QTile qt = find_tile(a, x);
     if (qt.b < 0) return;
 
-    // the sequence's rows, clamped into the buffers
-    auto clamp = [](int64_t v, int64_t top) { return v < 0 ? (int64_t)0 : (v > top ? top : v); };
-    const int64_t q0 = clamp(a.cu_q[qt.b], a.q_tokens), q1 = clamp(a.cu_q[qt.b + 1], a.q_tokens);
-    const int64_t k0 = clamp(a.cu_k[qt.b], a.k_tokens), k1 = clamp(a.cu_k[qt.b + 1], a.k_tokens);
-    const int lq = (int)(q1 - q0), lk = k1 > k0 ? (int)(k1 - k0) : 0;
+    const int64_t q0 = qt.q0, k0 = qt.k0;
+    const int lq = qt.lq, lk = qt.lk;
     const int64_t rows = (int64_t)lq * a.group;
     const int64_t row0 = (int64_t)qt.tile * kRows;
-    if (row0 >= rows) return;
 
     // this lane's row
     int64_t row = row0 + wave * 32 + col;
@@ -145,16 +151,21 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_prefill(PrefillA
     auto lb_of = [&](int t) { const int p = t + lk - lq; return a.window > 0 && p - a.window + 1 > 0 ? p - a.window + 1 : 0; };
     const int w_t0 = tok_of(row0 + wave * 32), w_t1 = tok_of(row0 + wave * 32 + 31);
     const int w_full_hi = ub_of(w_t0), w_full_lo = lb_of(w_t1);    // every row of the wave sees [w_full_lo, w_full_hi)
-    const int lo = lb_of(tok_of(row0)) & ~(kKeys - 1);
-    const int hi = ub_of(tok_of(row0 + kRows - 1));
+    int lo = lb_of(tok_of(row0)) & ~(kKeys - 1);
+    int hi = ub_of(tok_of(row0 + kRows - 1));
+    if (a.splits > 1 && lo < hi) {
+        const int share = ((hi - lo + kKeys - 1) / kKeys + a.splits - 1) / a.splits * kKeys;
+        lo += split * share;
+        hi = lo + share < hi ? lo + share : hi;
+    }
 
     // ---- Q: the B operand, held for the whole tile
     uint4 q[kSteps];
-    {
+    auto load_q = [&]() __attribute__((always_inline)) {
         const uint16_t *qp = a.q + (q0 + tok) * a.q_tok + head * a.q_head + 8 * half;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const uint4 *>(qp + 16 * s);
-    }
+    };
 
     f32x16 o[kDT];
 #pragma unroll
@@ -277,6 +288,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_prefill(PrefillA
         f32x16 s0[kSub], s1[kSub];
         uint4 p[2 * kSub];
         stage_k(lo, sm_k0);
+        load_q();
         __syncthreads();
         if (lo + kKeys < hi) stage_k(lo + kKeys, sm_k1);
         stage_v(lo, sm_v0);
@@ -313,6 +325,20 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_prefill(PrefillA
 
     l += other_half(l);
     if (!live) return;
+    if (a.splits > 1) {
+        // unnormalised sums of this part of the keys; k_attn_prefill_join adds the parts
+        const int64_t at = ((int64_t)(x * a.kv_heads + hkv) * a.splits + split) * kRows + wave * 32 + col;
+        if (half == 0) *reinterpret_cast<float2 *>(a.part_ml + 2 * at) = make_float2(m, l);
+        if (lo < hi) {
+#pragma unroll
+            for (int i = 0; i < kDT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    *reinterpret_cast<float4 *>(a.part_o + at * D + 32 * i + 8 * e + 4 * half) =
+                        make_float4(o[i][4 * e], o[i][4 * e + 1], o[i][4 * e + 2], o[i][4 * e + 3]);
+        }
+        return;
+    }
     const float f = l == 0.0f ? 0.0f : 1.0f / l;
     if (a.lse && half == 0)
         a.lse[(q0 + tok) * a.heads + head] = (m + __builtin_amdgcn_logf(l)) * 0.69314718f;
@@ -330,18 +356,74 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_prefill(PrefillA
         }
 }
 
+// Adds up the parts of a row tile's keys: 1024 / D rows a workgroup, four d a thread.
 template <int D>
-static fp4_status launch_d(const PrefillArgs &a, int64_t grid, hipStream_t st)
+__global__ __launch_bounds__(256) void k_attn_prefill_join(PrefillArgs a)
 {
-    hipLaunchKernelGGL(k_attn_prefill<D>, dim3((unsigned)grid), dim3(256), 0, st, a);
-    return hipGetLastError() == hipSuccess ? FP4_OK : FP4_ERR_HIP;
+    constexpr int kLanes = D / 4, kPer = 256 / kLanes;
+    const int xh = blockIdx.x / (kRows / kPer), r = (blockIdx.x - xh * (kRows / kPer)) * kPer + threadIdx.x / kLanes;
+    const int x = xh / a.kv_heads, hkv = xh - x * a.kv_heads;
+    const QTile qt = find_tile(a, x);
+    if (qt.b < 0) return;
+    const int64_t q0 = qt.q0, row = (int64_t)qt.tile * kRows + r;
+    if (row >= (int64_t)qt.lq * a.group) return;
+    const int tok = (int)((uint32_t)row / (uint32_t)a.group), head = hkv * a.group + (int)row - tok * a.group;
+    const int64_t first = (int64_t)xh * a.splits * kRows + r;
+    float M = -INFINITY;
+    for (int s = 0; s < a.splits; ++s) M = fmaxf(M, a.part_ml[2 * (first + s * kRows)]);
+    const float Ms = M == -INFINITY ? 0.0f : M;
+    const int d = threadIdx.x % kLanes * 4;
+    f32x4 acc = {0, 0, 0, 0};
+    float L = 0.0f;
+#pragma unroll 4
+    for (int s = 0; s < a.splits; ++s) {
+        const int64_t at = first + s * kRows;
+        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + 2 * at);
+        if (ml.y == 0.0f) continue;  // saw no key; its sums may not have been written
+        const float f = __builtin_amdgcn_exp2f(ml.x - Ms);
+        L += f * ml.y;
+        acc += f * *reinterpret_cast<const f32x4 *>(a.part_o + at * D + d);
+    }
+    acc *= L == 0.0f ? 0.0f : 1.0f / L;
+    const int64_t p = (q0 + tok) * a.o_tok + head * a.o_head + d;
+    if (a.out_bf16)
+        *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(a.out) + p) = make_uint2(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]));
+    else
+        *reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(a.out) + p) = acc;
+    if (a.lse && d == 0) a.lse[(q0 + tok) * a.heads + head] = (M + __builtin_amdgcn_logf(L)) * 0.69314718f;
 }
 
-// Row tiles of all sequences: at most one more per sequence than the packed rows hold.
+// Row tiles of all sequences and key heads: at most one more per sequence than the packed
+// rows hold.
 int64_t prefill_grid(int64_t q_tokens, int64_t seqs, int64_t kv_heads, int64_t group)
 {
     const int64_t more = seqs < q_tokens ? seqs : q_tokens;
     return (q_tokens * group / kRows + more) * kv_heads;
+}
+
+// Parts of every row tile's keys: where the row tiles do not fill half of the workgroups the
+// chip holds (two a CU, one at head_dim 256), as many as do, of at least 512 keys.
+int prefill_splits(int64_t q_tokens, int64_t k_tokens, int64_t seqs, int64_t kv_heads, int64_t group, int64_t head_dim)
+{
+    const int64_t grid = prefill_grid(q_tokens, seqs, kv_heads, group);
+    const int64_t room = device_cu_count() * (head_dim == 256 ? 1 : 2) / (grid > 0 ? grid : 1);
+    const int64_t most = k_tokens / 512;
+    const int64_t s = room < most ? room : most;
+    return s < 1 ? 1 : (s > 64 ? 64 : (int)s);
+}
+
+size_t prefill_part_rows(int64_t q_tokens, int64_t seqs, int64_t kv_heads, int64_t group, int splits)
+{
+    return splits > 1 ? (size_t)(prefill_grid(q_tokens, seqs, kv_heads, group) * splits * kRows) : 0;
+}
+
+template <int D>
+static fp4_status launch_d(const PrefillArgs &a, int64_t grid, hipStream_t st)
+{
+    hipLaunchKernelGGL(k_attn_prefill<D>, dim3((unsigned)(grid * a.splits)), dim3(256), 0, st, a);
+    if (a.splits > 1)
+        hipLaunchKernelGGL(k_attn_prefill_join<D>, dim3((unsigned)(grid * (kRows * D / 1024))), dim3(256), 0, st, a);
+    return hipGetLastError() == hipSuccess ? FP4_OK : FP4_ERR_HIP;
 }
 
 fp4_status launch_attn_prefill(const PrefillArgs &a, hipStream_t st)

@@ -531,6 +531,11 @@ fp4_status attn_decode_paged(const void *q, int64_t seqs, int64_t heads, int64_t
                              int64_t window, void *out, fp4_dtype ot, int64_t o_seq_stride,
                              int64_t o_head_stride, float *lse, void *ws, size_t ws_bytes, hipStream_t stream);
 
+/* Workspace bytes of attn_prefill on the current device: for a few rows against a long
+ * context, whose keys are split among workgroups; 0 otherwise (ws may be null then). */
+size_t attn_prefill_workspace(int64_t q_tokens, int64_t heads, int64_t k_tokens, int64_t kv_heads, int64_t head_dim,
+                              int64_t seqs);
+
 /* Attention of whole prompts, packed one behind the other.
  *  q      [q_tokens][heads][head_dim], k, v [k_tokens][kv_heads][head_dim], bf16, any
  *         strides as above (token strides of k and v below 2^24 elements: FP4_ERR_LAYOUT);
@@ -544,6 +549,7 @@ fp4_status attn_decode_paged(const void *q, int64_t seqs, int64_t heads, int64_t
  *         j > position - window.
  *  scale, out (fp32 or bf16), lse (fp32 [q_tokens][heads]): as attn_decode_paged.  A
  *         query that sees no key gives a zero row and lse = -inf.
+ *  ws     attn_prefill_workspace() bytes, 16-byte aligned.
  * k and v must be finite within a sequence's range.  q_tokens == 0 returns FP4_OK once
  * the other arguments check out; k_tokens == 0 gives zero rows.
  * q_tokens * heads / kv_heads and k_tokens < 2^31 (FP4_ERR_SHAPE). */
@@ -552,8 +558,8 @@ fp4_status attn_prefill(const void *q, int64_t q_tokens, int64_t heads, int64_t 
                         int64_t kv_heads, int64_t head_dim, int64_t k_token_stride, int64_t k_head_stride,
                         int64_t v_token_stride, int64_t v_head_stride, const int32_t *cu_q,
                         const int32_t *cu_k, int64_t seqs, float scale, int causal, int64_t window, void *out,
-                        fp4_dtype ot, int64_t o_token_stride, int64_t o_head_stride, float *lse,
-                        hipStream_t stream);
+                        fp4_dtype ot, int64_t o_token_stride, int64_t o_head_stride, float *lse, void *ws,
+                        size_t ws_bytes, hipStream_t stream);
 
 /* ---------------------------------------------------------- measurement --
  * fp4blk_read_ceiling: reads `bytes` bytes at `buf` once, with `grid`

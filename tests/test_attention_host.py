@@ -63,7 +63,7 @@ def _decode(fp4, cache=None, **kw):
 def _prefill(fp4, **kw):
     a = dict(q=FAKE, qn=50, heads=4, qt=256, qh=64, k=FAKE, v=FAKE, kn=60, kv=2, dim=64, kt=128, kh=64, vt=128, vh=64,
              cuq=FAKE, cuk=FAKE, seqs=2, scale=0.125, causal=1, window=0, out=FAKE, ot=1, ott=256, oh=64, lse=None,
-             stream=None)
+             ws=None, wsb=0, stream=None)
     a.update(kw)
     return fp4.lib().attn_prefill(*a.values())
 
@@ -134,6 +134,11 @@ def test_prefill(fp4):
     for bad in (dict(q=FAKE + 2), dict(kt=100), dict(vh=-64), dict(ott=32), dict(out=FAKE + 8)):
         assert _prefill(fp4, **bad) == LAYOUT, bad
     assert _prefill(fp4, qn=0, q=None, k=None, v=None, out=None) == OK
+    L = fp4.lib()
+    assert L.attn_prefill_workspace(8192, 8, 8192, 2, 64, 1) == 0          # the rows alone fill the chip
+    assert L.attn_prefill_workspace(5, 8, 100, 2, 64, 1) == 0              # few keys
+    assert L.attn_prefill_workspace(5, 8, 100000, 2, 64, 1) > 0
+    assert L.attn_prefill_workspace(5, 9, 100000, 2, 64, 1) == 0
     if not GPU:
         assert _prefill(fp4) == NO_DEVICE and _prefill(fp4, kn=0, k=None, v=None) == NO_DEVICE
 

@@ -314,6 +314,16 @@ def test_prompt_long_rows(dim):
     ref.check(out[rows], lse[rows], want, dim, 2.0 ** -8, f"long {dim}")
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_prompt_few_rows_long_context(dim):
+    """A few queries behind long contexts: the keys are split among workgroups and joined.  Contexts
+    shorter than a part beside them, a window that leaves parts empty, and one that cuts."""
+    for lq, lk, window in (([1], [9000], 0), ([3, 1, 0, 2], [5000, 7, 0, 2049], 0), ([33], [6000], 0),
+                           ([5, 4], [4100, 100], 700), ([2], [5000], 1)):
+        _prompt(lq, lk, 4, 2, dim, window=window, seed=lk[0])
+    _prompt([4], [5000], 4, 2, dim, causal=False, seed=1)
+
+
 def test_prompt_others_are_not_read():
     """Keys and values of other sequences hold NaN and infinities; keys that are masked may too."""
     fp4 = _fp4()
