@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 
 import torch
@@ -1154,9 +1155,29 @@ def kv_cache_read(cache: KVCache, block_table: torch.Tensor, cu_seqlens: torch.T
     return k_out, v_out
 
 
+@functools.lru_cache(maxsize=4096)
+def _decode_need(seqs, heads, kv_heads, page_size, head_dim, table_width) -> int:
+    """Workspace bytes, by the sizes alone."""
+    sizes = _KvCacheArg(KV_BF16, 1, kv_heads, page_size, head_dim)
+    return lib().attn_decode_paged_workspace(seqs, heads, ctypes.byref(sizes), table_width)
+
+
+@functools.lru_cache(maxsize=4096)
+def _prefill_need(q_tokens, heads, k_tokens, kv_heads, head_dim, seqs) -> int:
+    return lib().attn_prefill_workspace(q_tokens, heads, k_tokens, kv_heads, head_dim, seqs)
+
+
 def attn_decode_paged_workspace(cache: KVCache, seqs: int, heads: int, table_width: int) -> torch.Tensor:
-    return torch.empty(lib().attn_decode_paged_workspace(seqs, heads, cache._ref, table_width), dtype=torch.uint8,
-                       device=cache.device)
+    """A workspace for attn_decode_paged calls of these sizes."""
+    return torch.empty(_decode_need(seqs, heads, cache.kv_heads, cache.page_size, cache.head_dim, table_width),
+                       dtype=torch.uint8, device=cache.device)
+
+
+def attn_prefill_workspace(q_tokens: int, heads: int, k_tokens: int, kv_heads: int, head_dim: int, seqs: int,
+                           device="cuda") -> torch.Tensor:
+    """A workspace for attn_prefill calls of these sizes."""
+    return torch.empty(_prefill_need(q_tokens, heads, k_tokens, kv_heads, head_dim, seqs), dtype=torch.uint8,
+                       device=device)
 
 
 def attn_decode_paged(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -1178,12 +1199,11 @@ def attn_decode_paged(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor
     out, ot, oh = _out_heads(out, n, h, d, dtype, q)
     if lse is not None:
         _lse(lse, n, h)
-    L = lib()
-    need = L.attn_decode_paged_workspace(n, h, cache._ref, width)
+    need = _decode_need(n, h, cache.kv_heads, cache.page_size, d, width)
     if need or workspace is not None:
         workspace = _workspace(workspace, need, q)
     _need_cuda(cache.k_codes, q, block_table, seq_lens, out, lse, workspace)
-    _run(L.attn_decode_paged, _ptr(q), n, h, qt, qh, _kv(cache), _ptr(block_table), width, stride, _ptr(seq_lens),
+    _run(lib().attn_decode_paged, _ptr(q), n, h, qt, qh, _kv(cache), _ptr(block_table), width, stride, _ptr(seq_lens),
          d ** -0.5 if scale is None else scale, window, _ptr(out), _dt(out), ot, oh, _ptr(lse), _ptr(workspace),
          need, _stream())
     return out
@@ -1212,12 +1232,11 @@ def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q
     out, ot, oh = _out_heads(out, n, h, d, dtype, q)
     if lse is not None:
         _lse(lse, n, h)
-    L = lib()
-    need = L.attn_prefill_workspace(n, h, nk, hk, d, seqs)
+    need = _prefill_need(n, h, nk, hk, d, seqs)
     if need or workspace is not None:
         workspace = _workspace(workspace, need, q)
     _need_cuda(q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse, workspace)
-    _run(L.attn_prefill, _ptr(q), n, h, qt, qh, _ptr(k), _ptr(v), nk, hk, d, kt, kh, vt, vh, _ptr(cu_seqlens_q),
+    _run(lib().attn_prefill, _ptr(q), n, h, qt, qh, _ptr(k), _ptr(v), nk, hk, d, kt, kh, vt, vh, _ptr(cu_seqlens_q),
          _ptr(cu_seqlens_k), seqs, d ** -0.5 if scale is None else scale, int(bool(causal)), window, _ptr(out),
          _dt(out), ot, oh, _ptr(lse), _ptr(workspace), need, _stream())
     return out

@@ -46,7 +46,7 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 namespace {
 
 constexpr int kTile = 128;          // keys of one work unit
-constexpr int kOver = 2;            // what a row costs beside its tiles, in units
+constexpr int kOver = 1;            // what a row costs beside its tiles, in units
 constexpr float kLazy = 8.0f;       // log2 headroom before the running maximum moves
 
 constexpr int kv_bits(int fmt) { return fmt == FP4_KV_BF16 ? 16 : fmt == FP4_KV_MXFP8 ? 8 : 4; }
@@ -89,46 +89,54 @@ __device__ __forceinline__ int wave_inclusive_sum(int v)
     return v;
 }
 
-// Total tiles of all sequences (of one row each).
-__device__ __forceinline__ int total_cost(const DecodeArgs &a)
-{
-    const int lane = threadIdx.x & 63;
-    int sum = 0;
-    for (int b0 = 0; b0 < a.seqs; b0 += 64) sum += b0 + lane < a.seqs ? seq_span(a, b0 + lane).cost() : 0;
-    sum = wave_inclusive_sum(sum);
-    return __builtin_amdgcn_readlane(sum, 63);
-}
+// What one row of every sequence costs, added up along the sequences.  A lane keeps the
+// cost of sequence `lane` and the sum up to it; sequences past 64 are gone through again
+// when one is looked for.
+struct Plan {
+    int cost, sum;    // of sequence `lane`, and of sequences 0 .. lane
+    int head, total;  // of the first 64 sequences, and of all
+};
 
-// The sequence that holds tile x of the concatenated sequences (0 <= x < total),
-// and the number of tiles before it.
-__device__ __forceinline__ void find_seq(const DecodeArgs &a, int x, int &b, int &before)
+__device__ __forceinline__ Plan make_plan(const DecodeArgs &a)
 {
     const int lane = threadIdx.x & 63;
-    int base = 0;
-    for (int b0 = 0;; b0 += 64) {
-        const int t = b0 + lane < a.seqs ? seq_span(a, b0 + lane).cost() : 0;
-        const int inc = wave_inclusive_sum(t);
-        const int sum = __builtin_amdgcn_readlane(inc, 63);
-        if (x < base + sum || b0 + 64 >= a.seqs) {
-            const uint64_t past = __ballot(base + inc <= x);  // sequences that end at or before x
-            int i = __builtin_popcountll(past);
-            i = i > 63 ? 63 : i;
-            b = b0 + i;
-            before = base + __builtin_amdgcn_readlane(inc - t, i);
-            return;
-        }
-        base += sum;
+    Plan p;
+    p.cost = lane < a.seqs ? seq_span(a, lane).cost() : 0;
+    p.sum = wave_inclusive_sum(p.cost);
+    p.head = p.total = __builtin_amdgcn_readlane(p.sum, 63);
+    if (a.seqs > 64) {
+        int more = 0;
+        for (int b0 = 64; b0 < a.seqs; b0 += 64) more += b0 + lane < a.seqs ? seq_span(a, b0 + lane).cost() : 0;
+        p.total += __builtin_amdgcn_readlane(wave_inclusive_sum(more), 63);
     }
+    return p;
 }
 
-// Tiles before sequence b.
-__device__ __forceinline__ int cost_before(const DecodeArgs &a, int b)
+// The sequence at x (0 <= x < total) along the sum, and the sum before it.
+__device__ __forceinline__ void find_seq(const DecodeArgs &a, const Plan &p, int x, int &b, int &before)
 {
     const int lane = threadIdx.x & 63;
-    int sum = 0;
-    for (int b0 = 0; b0 < b; b0 += 64) sum += b0 + lane < b ? seq_span(a, b0 + lane).cost() : 0;
-    sum = wave_inclusive_sum(sum);
-    return __builtin_amdgcn_readlane(sum, 63);
+    int cost = p.cost, sum = p.sum, base = 0, b0 = 0;
+    while (x >= base + __builtin_amdgcn_readlane(sum, 63) && b0 + 64 < a.seqs) {
+        base += __builtin_amdgcn_readlane(sum, 63);
+        b0 += 64;
+        cost = b0 + lane < a.seqs ? seq_span(a, b0 + lane).cost() : 0;
+        sum = wave_inclusive_sum(cost);
+    }
+    int i = __builtin_popcountll(__ballot(base + sum <= x));  // sequences that end at or before x
+    i = i > 63 ? 63 : i;
+    b = b0 + i;
+    before = base + __builtin_amdgcn_readlane(sum - cost, i);
+}
+
+// The sum before sequence b.
+__device__ __forceinline__ int cost_before(const DecodeArgs &a, const Plan &p, int b)
+{
+    if (b < 64) return __builtin_amdgcn_readlane(p.sum - p.cost, b);
+    const int lane = threadIdx.x & 63;
+    int more = 0;
+    for (int b0 = 64; b0 < b; b0 += 64) more += b0 + lane < b ? seq_span(a, b0 + lane).cost() : 0;
+    return p.head + __builtin_amdgcn_readlane(wave_inclusive_sum(more), 63);
 }
 
 // Workgroup w of `grid` takes units [start(w), start(w + 1)): the first `extra` of
@@ -297,21 +305,29 @@ __device__ __forceinline__ float xor16_sum(float v)
 
 // Waves of a workgroup, and waves a SIMD is to hold (which bounds the registers).
 // FIXME measured table
-template <int FMT, int D>
+template <int FMT, int D, bool SPLIT>
 struct Shape {
     static constexpr int kHold = D < 256 ? (D * kv_bits(FMT) <= 512 ? 4 : 3) : (FMT == FP4_KV_BF16 ? 1 : 2);
-    static constexpr int kWaves = 4;
+    static constexpr int kWaves = SPLIT || kHold == 1 ? 4 : 8;
     static constexpr int kPerCu = kHold * 4 / kWaves;  // workgroups a CU holds
 };
 
+// Orders LDS accesses of the workgroup; loads from memory stay in flight across it.
+__device__ __forceinline__ void lds_barrier()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // SPLIT: the workgroups share all units; else one workgroup per row.
 template <int FMT, int D, bool SPLIT>
-__global__ __launch_bounds__((64 * Shape<FMT, D>::kWaves), (Shape<FMT, D>::kHold)) void k_attn_decode(DecodeArgs a)
+__global__ __launch_bounds__((64 * Shape<FMT, D, SPLIT>::kWaves), (SPLIT ? Shape<FMT, D, SPLIT>::kHold : 1)) void k_attn_decode(DecodeArgs a)
 {
     using C = Cfg<FMT, D>;
-    constexpr int kWaves = Shape<FMT, D>::kWaves;
+    constexpr int kWaves = Shape<FMT, D, SPLIT>::kWaves;
     constexpr int kStride = 32 * kWaves;  // keys the workgroup takes at a time
-    static_assert(kTile % kStride == 0, "a unit is a whole number of passes");
+    static_assert(!SPLIT || kTile % kStride == 0, "a unit is a whole number of passes");
     __shared__ f32x4 sm_o[kWaves / 2][C::kDT][64];
     __shared__ float sm_m[kWaves][16], sm_l[kWaves][16];
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
@@ -322,146 +338,163 @@ __global__ __launch_bounds__((64 * Shape<FMT, D>::kWaves), (Shape<FMT, D>::kHold
     int u = wg, u_end = wg + 1, b = 0, base = 0;
     SeqSpan sp;
     if constexpr (SPLIT) {
-        const int units = total_cost(a) * rows;
+        const Plan plan = make_plan(a);
+        const int units = plan.total * rows;
         const int grid = (int)gridDim.x < units ? (int)gridDim.x : units;
         if (wg >= grid) return;
         const Share sh = share_of(units, grid);
         u = share_start(sh, wg);
         u_end = share_start(sh, wg + 1);
         int before;
-        find_seq(a, u / rows, b, before);
+        find_seq(a, plan, u / rows, b, before);
         base = before * rows;  // first unit of sequence b
-        sp = seq_span(a, b);
     } else {
         b = wg / rows;
-        sp = seq_span(a, b);
     }
+    sp = seq_span(a, b);
     // the lane's offsets from a sub-tile's first key
     const uint32_t k_lane = n * C::kRow + g * C::kKB, v_lane = 4 * g * C::kRow + n * C::kVB;
     const uint32_t ks_lane = ((g * C::kKV / C::kBlk) << a.page_shift) + n;
     const uint32_t vs_lane = ((n * C::kVV / C::kBlk) << a.page_shift) + 4 * g;
-    while (u < u_end) {
-        int r, t0, t1;
+    // the next segment (a range of one row's tiles) of this workgroup's units; false when they are used up
+    int r = 0, t0 = 0, t1 = 0;
+    auto advance = [&]() -> bool {
         if constexpr (SPLIT) {
-            while (u >= base + sp.cost() * rows) {
-                base += sp.cost() * rows;
-                sp = seq_span(a, ++b);
+            while (u < u_end) {
+                while (u >= base + sp.cost() * rows) {
+                    base += sp.cost() * rows;
+                    sp = seq_span(a, ++b);
+                }
+                // a row's units: kOver that stand for its fixed cost, then its tiles
+                r = (u - base) / sp.cost();
+                const int row_u = base + r * sp.cost(), first = u - row_u, left = u_end - row_u;
+                t0 = first > kOver ? first - kOver : 0;
+                t1 = left >= sp.cost() ? sp.tiles : left - kOver;
+                u = row_u + sp.cost();
+                if (t1 > t0) return true;  // else only (a part of) the fixed cost
             }
-            // a row's units: kOver that stand for its fixed cost, then its tiles
-            r = (u - base) / sp.cost();
-            const int row_u = base + r * sp.cost(), first = u - row_u;
-            const int left = u_end - row_u;
-            t0 = first > kOver ? first - kOver : 0;
-            t1 = left >= sp.cost() ? sp.tiles : left - kOver;
-            u = row_u + sp.cost();
-            if (t1 <= t0) continue;  // only (a part of) the fixed cost
+            return false;
         } else {
+            const bool first = u < u_end;
             r = wg - b * rows;
             t0 = 0;
             t1 = sp.tiles;
+            u = u_end;
+            return first;
         }
-        const int hkv = r / a.head_tiles, h0 = (r - hkv * a.head_tiles) * 16;
-        const int nh = a.group - h0 < 16 ? a.group - h0 : 16;  // query heads of this tile
-        const int head0 = hkv * a.group + h0;
+    };
 
-        // ---- raw bytes of 32 keys and of their values, fetched ahead of their use
-        uint32_t kr[2][C::kKW], ksr[2][C::kScaled ? C::kKL * C::kKS : 1];
-        uint32_t vr[8][C::kVL][C::kVW], vsr[2][C::kVL];
+    // ---- raw bytes of 32 keys and of their values, fetched ahead of their use
+    uint32_t kr[2][C::kKW], ksr[2][C::kScaled ? C::kKL * C::kKS : 1];
+    uint32_t vr[8][C::kVL][C::kVW], vsr[2][C::kVL];
+    uint4 q[C::kSteps];
+    int hkv = 0, head0 = 0, nh = 0, key0 = 0, seg_end = 0;
+    const int page_mask = (1 << a.page_shift) - 1;
+    // pages of the two sub-tiles that are fetched next, looked up a pass ahead of their use; a
+    // sub-tile past the sequence's end reads its last page (its keys are masked)
+    int page_id[2];
+    auto look_up = [&](int key0) {
         const const_i32 table = as_const(a.table + b * a.table_stride);
-        const int page_mask = (1 << a.page_shift) - 1, top_page = (sp.len - 1) >> a.page_shift;
-        // first row of a sub-tile within its pool, counted in tokens of one head; a sub-tile
-        // past the sequence's end reads its last page (its keys are masked)
-        auto block_of = [&](int key, int64_t &block, int &off) {
-            int page = key >> a.page_shift;
-            page = page < top_page ? page : top_page;
-            int id = table[page];
-            id = id < 0 ? 0 : (id >= a.pages ? a.pages - 1 : id);
-            block = ((int64_t)id * a.kv_heads + hkv) << a.page_shift;
-            off = key & page_mask;
-        };
-        auto fetch_k = [&](int key0) {
+        const int top_page = (sp.len - 1) >> a.page_shift;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                int64_t block;
-                int off;
-                block_of(key0 + 16 * j, block, off);
-                const uint8_t *kp = a.k_codes + (block + off) * C::kRow;
+        for (int j = 0; j < 2; ++j) {
+            const int page = (key0 + 16 * j) >> a.page_shift;
+            page_id[j] = table[page < top_page ? page : top_page];
+        }
+    };
+    // first row of a sub-tile's page within its pool, counted in tokens of one head
+    auto block_of = [&](int j) -> int64_t {
+        int id = page_id[j];
+        id = id < 0 ? 0 : (id >= a.pages ? a.pages - 1 : id);
+        return ((int64_t)id * a.kv_heads + hkv) << a.page_shift;
+    };
+    auto fetch_k = [&](int key0) {
 #pragma unroll
-                for (int i = 0; i < C::kKL; ++i) load_dwords<C::kKB>(kp + i * 4 * C::kKB + k_lane, &kr[j][i * (C::kKB / 4)]);
-                if constexpr (C::kScaled) {
-                    const uint8_t *ksp = a.k_scales + block * (D / C::kBlk) + off;
+        for (int j = 0; j < 2; ++j) {
+            const int64_t block = block_of(j);
+            const int off = (key0 + 16 * j) & page_mask;
+            const uint8_t *kp = a.k_codes + (block + off) * C::kRow;
 #pragma unroll
-                    for (int i = 0; i < C::kKL; ++i)
+            for (int i = 0; i < C::kKL; ++i) load_dwords<C::kKB>(kp + i * 4 * C::kKB + k_lane, &kr[j][i * (C::kKB / 4)]);
+            if constexpr (C::kScaled) {
+                const uint8_t *ksp = a.k_scales + block * (D / C::kBlk) + off;
 #pragma unroll
-                        for (int e = 0; e < C::kKS; ++e)
-                            ksr[j][i * C::kKS + e] = (ksp + ((i * 4 * C::kKV / C::kBlk + e) << a.page_shift))[ks_lane];
-                }
+                for (int i = 0; i < C::kKL; ++i)
+#pragma unroll
+                    for (int e = 0; e < C::kKS; ++e)
+                        ksr[j][i * C::kKS + e] = (ksp + ((i * 4 * C::kKV / C::kBlk + e) << a.page_shift))[ks_lane];
             }
-        };
-        auto fetch_v = [&](int key0) {
+        }
+    };
+    auto fetch_v = [&](int key0) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                int64_t block;
-                int off;
-                block_of(key0 + 16 * j, block, off);
-                const uint8_t *vp = a.v_codes + (block + off) * C::kRow;
+        for (int j = 0; j < 2; ++j) {
+            const int64_t block = block_of(j);
+            const int off = (key0 + 16 * j) & page_mask;
+            const uint8_t *vp = a.v_codes + (block + off) * C::kRow;
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-                    for (int h = 0; h < C::kVL; ++h) load_dwords<C::kVB>(vp + t * C::kRow + h * 16 * C::kVB + v_lane, vr[4 * j + t][h]);
-                if constexpr (C::kScaled) {
-                    const uint8_t *vsp = a.v_scales + block * (D / C::kBlk) + off;
+                for (int h = 0; h < C::kVL; ++h) load_dwords<C::kVB>(vp + t * C::kRow + h * 16 * C::kVB + v_lane, vr[4 * j + t][h]);
+            if constexpr (C::kScaled) {
+                const uint8_t *vsp = a.v_scales + block * (D / C::kBlk) + off;
 #pragma unroll
-                    for (int h = 0; h < C::kVL; ++h)
-                        vsr[j][h] = *reinterpret_cast<const uint32_t *>(vsp + ((h * 16 * C::kVV / C::kBlk) << a.page_shift) + vs_lane);
-                }
+                for (int h = 0; h < C::kVL; ++h)
+                    vsr[j][h] = *reinterpret_cast<const uint32_t *>(vsp + ((h * 16 * C::kVV / C::kBlk) << a.page_shift) + vs_lane);
             }
-        };
-
-        int key0 = sp.a0 + t0 * kTile + wave * 32;
-        const int seg_end = sp.a0 + t1 * kTile < sp.len ? sp.a0 + t1 * kTile : sp.len;
-        const bool any = key0 < seg_end;
-        if (any) {
+        }
+    };
+    // a segment's query heads (the B operand: lane n = head, the same order of d as K's
+    // loads), first keys and first values, requested before the segment before it is joined
+    auto begin = [&]() {
+        hkv = r / a.head_tiles;
+        const int h0 = (r - hkv * a.head_tiles) * 16;
+        nh = a.group - h0 < 16 ? a.group - h0 : 16;
+        head0 = hkv * a.group + h0;
+        key0 = sp.a0 + t0 * kTile + wave * 32;
+        if (sp.len > 0) look_up(key0);
+        seg_end = sp.a0 + t1 * kTile < sp.len ? sp.a0 + t1 * kTile : sp.len;
+        const uint16_t *qp = a.q + b * a.q_seq + (int64_t)(head0 + n) * a.q_head;
+#pragma unroll
+        for (int s = 0; s < C::kSteps; ++s) {
+            const int i = 8 * s / C::kKV, e = 8 * s % C::kKV;
+            q[s] = make_uint4(0, 0, 0, 0);
+            if (n < nh) q[s] = *reinterpret_cast<const uint4 *>(qp + i * 4 * C::kKV + g * C::kKV + e);
+        }
+        if (key0 < seg_end) {
             fetch_k(key0);
             fetch_v(key0);
+            look_up(key0 + kStride);
         }
+    };
 
-        // ---- q: the B operand, lane n = head, the same order of d as K's loads
-        uint4 q[C::kSteps];
+    bool more = advance();
+    if (more) begin();
+    while (more) {
         float c = a.scale_log2;
-        {
-            const uint16_t *qp = a.q + b * a.q_seq + (int64_t)(head0 + n) * a.q_head;
+        if constexpr (C::kF16) {
+            float m = 0.0f;
 #pragma unroll
             for (int s = 0; s < C::kSteps; ++s) {
-                const int i = 8 * s / C::kKV, e = 8 * s % C::kKV;
-                q[s] = make_uint4(0, 0, 0, 0);
-                if (n < nh) q[s] = *reinterpret_cast<const uint4 *>(qp + i * 4 * C::kKV + g * C::kKV + e);
+                const uint32_t w[4] = {q[s].x, q[s].y, q[s].z, q[s].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    m = fmaxf(m, fmaxf(__builtin_fabsf(__uint_as_float(w[i] << 16)),
+                                       __builtin_fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
             }
-            if constexpr (C::kF16) {
-                float m = 0.0f;
+            m = xor16_max(m);
+            const int e = m > 0.0f && m < INFINITY ? 15 - __builtin_amdgcn_frexp_expf(m) : 0;
 #pragma unroll
-                for (int s = 0; s < C::kSteps; ++s) {
-                    const uint32_t w[4] = {q[s].x, q[s].y, q[s].z, q[s].w};
+            for (int s = 0; s < C::kSteps; ++s) {
+                uint32_t w[4] = {q[s].x, q[s].y, q[s].z, q[s].w};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        m = fmaxf(m, fmaxf(__builtin_fabsf(__uint_as_float(w[i] << 16)),
-                                           __builtin_fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
-                }
-                m = xor16_max(m);
-                const int e = m > 0.0f && m < INFINITY ? 15 - __builtin_amdgcn_frexp_expf(m) : 0;
-#pragma unroll
-                for (int s = 0; s < C::kSteps; ++s) {
-                    uint32_t w[4] = {q[s].x, q[s].y, q[s].z, q[s].w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        w[i] = pack2<true>(__builtin_amdgcn_ldexpf(__uint_as_float(w[i] << 16), e),
-                                           __builtin_amdgcn_ldexpf(__uint_as_float(w[i] & 0xFFFF0000u), e));
-                    q[s] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-                c = __builtin_amdgcn_ldexpf(c * a.k_tscale[hkv], -e);
+                for (int i = 0; i < 4; ++i)
+                    w[i] = pack2<true>(__builtin_amdgcn_ldexpf(__uint_as_float(w[i] << 16), e),
+                                       __builtin_amdgcn_ldexpf(__uint_as_float(w[i] & 0xFFFF0000u), e));
+                q[s] = make_uint4(w[0], w[1], w[2], w[3]);
             }
+            c = __builtin_amdgcn_ldexpf(c * a.k_tscale[hkv], -e);
         }
-
         c = fmaxf(c, 0x1p-140f);  // a scale of 0: -inf of a masked key stays -inf, every other score becomes 0
 
         f32x4 o[C::kDT];
@@ -549,7 +582,7 @@ __global__ __launch_bounds__((64 * Shape<FMT, D>::kWaves), (Shape<FMT, D>::kHold
                 }
         };
 
-        if (any) {
+        if (key0 < seg_end) {
             f32x4 s[2];
             // the next keys are requested as soon as this pass's keys are used up, the next
             // values as soon as its values are: one set of registers, loads always in flight
@@ -563,6 +596,7 @@ __global__ __launch_bounds__((64 * Shape<FMT, D>::kWaves), (Shape<FMT, D>::kHold
                 if (cut) mask_values(key0);
                 values(pf);
                 fetch_v(key0 + kStride);
+                look_up(key0 + 2 * kStride);
                 __builtin_amdgcn_sched_barrier(0);
             }
             scores(s);
@@ -573,13 +607,18 @@ __global__ __launch_bounds__((64 * Shape<FMT, D>::kWaves), (Shape<FMT, D>::kHold
             values(pf);
         }
 
-        // ---- the waves' results become one
+        // ---- the waves' results become one, while the next segment's first loads are in flight
+        const int e_b = b, e_head0 = head0, e_nh = nh, e_hkv = hkv, slot = 2 * wg + (t0 == 0);
+        const bool whole = t0 == 0 && t1 == sp.tiles;
+        more = advance();
+        if (more) begin();
+        __builtin_amdgcn_sched_barrier(0);
         l = xor16_sum(l);
         if (lane < 16) {
             sm_m[wave][n] = m;
             sm_l[wave][n] = l;
         }
-        __syncthreads();
+        lds_barrier();
         float M = -INFINITY, L = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) M = fmaxf(M, sm_m[w][n]);
@@ -595,22 +634,20 @@ __global__ __launch_bounds__((64 * Shape<FMT, D>::kWaves), (Shape<FMT, D>::kHold
 #pragma unroll
                 for (int i = 0; i < C::kDT; ++i) sm_o[wave - half][i][lane] = o[i];
             }
-            __syncthreads();
+            lds_barrier();
             if (wave < half) {
 #pragma unroll
                 for (int i = 0; i < C::kDT; ++i) o[i] += sm_o[wave][i][lane];
             }
-            if (half > 1) __syncthreads();
+            if (half > 1) lds_barrier();
         }
-        if (wave == 0 && n < nh) {
-            const bool whole = t0 == 0 && t1 == sp.tiles;
-            const int slot = 2 * wg + (t0 == 0);  // a range begins within at most one row and ends within one
+        if (wave == 0 && n < e_nh) {
             float *po = nullptr;
             float f = 1.0f;
             if (whole) {
                 f = L == 0.0f ? 0.0f : 1.0f / L;
-                if constexpr (C::kF16) f *= a.v_tscale[hkv];
-                if (a.lse && g == 0) a.lse[(int64_t)b * a.heads + head0 + n] = (M + __builtin_amdgcn_logf(L)) * 0.69314718f;
+                if constexpr (C::kF16) f *= a.v_tscale[e_hkv];
+                if (a.lse && g == 0) a.lse[(int64_t)e_b * a.heads + e_head0 + n] = (M + __builtin_amdgcn_logf(L)) * 0.69314718f;
             } else {
                 po = a.part_o + ((int64_t)slot * a.part_heads + n) * D;
                 if (g == 0) {
@@ -630,17 +667,16 @@ __global__ __launch_bounds__((64 * Shape<FMT, D>::kWaves), (Shape<FMT, D>::kHold
                         if (!whole) {
                             *reinterpret_cast<float4 *>(po + d + i) = v;
                         } else if (a.out_bf16) {
-                            uint16_t *p = reinterpret_cast<uint16_t *>(a.out) + b * a.o_seq + (head0 + n) * a.o_head + d + i;
+                            uint16_t *p = reinterpret_cast<uint16_t *>(a.out) + e_b * a.o_seq + (e_head0 + n) * a.o_head + d + i;
                             *reinterpret_cast<uint2 *>(p) = make_uint2(pack2<false>(v.x, v.y), pack2<false>(v.z, v.w));
                         } else {
-                            float *p = reinterpret_cast<float *>(a.out) + b * a.o_seq + (head0 + n) * a.o_head + d + i;
+                            float *p = reinterpret_cast<float *>(a.out) + e_b * a.o_seq + (e_head0 + n) * a.o_head + d + i;
                             *reinterpret_cast<float4 *>(p) = v;
                         }
                     }
                 }
         }
-        if (SPLIT && u < u_end) __syncthreads();  // the next segment writes sm_m, sm_l and sm_o again
-        if constexpr (!SPLIT) break;
+        if (more) lds_barrier();  // the next segment writes sm_m, sm_l and sm_o again
     }
 }
 
@@ -652,33 +688,41 @@ __global__ __launch_bounds__(256) void k_attn_decode_join(DecodeArgs a, int grid
 {
     constexpr int kLanes = D / 4, kParts = 256 / kLanes;
     __shared__ f32x4 sm[kParts][kLanes];
-    __shared__ float sm_l[kParts];
+    __shared__ float sm_m[kParts], sm_l[kParts];
     const int b = blockIdx.x / a.heads, head = blockIdx.x - b * a.heads;
     const int hkv = head / a.group, hg = head - hkv * a.group, n = hg & 15;
     const int rows = a.kv_heads * a.head_tiles;
-    const int units = total_cost(a) * rows;
+    const Plan plan = make_plan(a);
+    const int units = plan.total * rows;
     const int grid = grid_full < units ? grid_full : units;
     const Share sh = share_of(units, grid);
     const SeqSpan sp = seq_span(a, b);
     const int r = hkv * a.head_tiles + (hg >> 4);
-    const int u0 = cost_before(a, b) * rows + r * sp.cost() + kOver;  // its first tile
+    const int u0 = cost_before(a, plan, b) * rows + r * sp.cost() + kOver;  // its first tile
     const int w0 = share_owner(sh, u0), w1 = share_owner(sh, u0 + sp.tiles - 1);
     if (w0 == w1) return;
-    auto at = [&](int w) -> int64_t { return (int64_t)(2 * w + (w == w0)) * a.part_heads + n; };
-    float M = -INFINITY;
-    for (int w = w0 + (threadIdx.x & 63); w <= w1; w += 64) M = fmaxf(M, a.part_ml[at(w) * 2]);
-    M = wave_max(M);
-    const float Ms = M == -INFINITY ? 0.0f : M;
     const int d = threadIdx.x % kLanes, part = threadIdx.x / kLanes;
     f32x4 acc = {0, 0, 0, 0};
-    float L = 0.0f;
+    float m = -INFINITY, L = 0.0f;
 #pragma unroll 4
     for (int w = w0 + part; w <= w1; w += kParts) {
-        const int64_t i = at(w);
-        const float f = __builtin_amdgcn_exp2f(a.part_ml[i * 2] - Ms);
-        L += f * a.part_ml[i * 2 + 1];
-        acc += f * *reinterpret_cast<const f32x4 *>(a.part_o + i * D + 4 * d);
+        const int64_t i = (int64_t)(2 * w + (w == w0)) * a.part_heads + n;
+        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + i * 2);
+        const f32x4 o = *reinterpret_cast<const f32x4 *>(a.part_o + i * D + 4 * d);
+        const float mn = fmaxf(m, ml.x), ms = mn == -INFINITY ? 0.0f : mn;
+        const float fa = __builtin_amdgcn_exp2f(m - ms), fb = __builtin_amdgcn_exp2f(ml.x - ms);
+        L = L * fa + ml.y * fb;
+        acc = acc * fa + o * fb;
+        m = mn;
     }
+    if (d == 0) sm_m[part] = m;
+    __syncthreads();
+    float M = sm_m[0];
+#pragma unroll
+    for (int i = 1; i < kParts; ++i) M = fmaxf(M, sm_m[i]);
+    const float f0 = __builtin_amdgcn_exp2f(m - (M == -INFINITY ? 0.0f : M));
+    acc *= f0;
+    L *= f0;
     sm[part][d] = acc;
     if (d == 0) sm_l[part] = L;
     __syncthreads();
@@ -721,10 +765,11 @@ int decode_grid(int64_t seqs, int64_t kv_heads, int64_t head_tiles, int64_t max_
 template <int FMT, int D>
 static void launch_decode(const DecodeArgs &a, hipStream_t st)
 {
-    using S = Shape<FMT, D>;
+    using S = Shape<FMT, D, true>;
     const int rows = a.kv_heads * a.head_tiles;
     if (!decode_splits(a.max_len)) {
-        hipLaunchKernelGGL((k_attn_decode<FMT, D, false>), dim3((unsigned)(a.seqs * rows)), dim3(64 * S::kWaves), 0, st, a);
+        hipLaunchKernelGGL((k_attn_decode<FMT, D, false>), dim3((unsigned)(a.seqs * rows)),
+                           dim3(64 * Shape<FMT, D, false>::kWaves), 0, st, a);
         return;
     }
     const int64_t units = decode_units_bound(a.seqs, a.kv_heads, a.head_tiles, a.max_len);
