@@ -49,7 +49,9 @@ __device__ __forceinline__ int clamp_offset(int v, int64_t top) { return v < 0 ?
 
 // Row tile x of the concatenated sequences, a sequence's last tiles first: they see the most
 // keys.  (The longest sequence first as well gained nothing measurable and costs a pass
-// over the lanes.)
+// over the lanes.)  Where the chip holds all workgroups at once, two a CU, the second half
+// comes in reverse: the CUs that got the longest tiles first get the shortest ones as
+// their second (2048 tokens, 32/8 heads of 128: 46.5 -> 45.3 us; two prompts of 1000: 33.6 -> 27.7 us).
 __device__ __forceinline__ QTile find_tile(const PrefillArgs &a, int x)
 {
     const int lane = threadIdx.x & 63;
@@ -66,6 +68,7 @@ __device__ __forceinline__ QTile find_tile(const PrefillArgs &a, int x)
             if (lane >= off) inc += o;
         }
         const int sum = __builtin_amdgcn_readlane(inc, 63);
+        if (a.seqs <= 64 && x >= a.fold_at && x < sum && sum * a.kv_heads <= a.fold_most) x = sum - 1 - (x - a.fold_at);
         if (x < base + sum) {
             int i = __builtin_popcountll(__ballot(base + inc <= x));
             i = i > 63 ? 63 : i;
@@ -429,9 +432,13 @@ static fp4_status launch_d(const PrefillArgs &a, int64_t grid, hipStream_t st)
 fp4_status launch_attn_prefill(const PrefillArgs &a, hipStream_t st)
 {
     const int64_t grid = prefill_grid(a.q_tokens, a.seqs, a.kv_heads, a.group);
-    if (a.head_dim == 64) return launch_d<64>(a, grid, st);
-    if (a.head_dim == 128) return launch_d<128>(a, grid, st);
-    return launch_d<256>(a, grid, st);
+    PrefillArgs f = a;
+    const int cus = device_cu_count();
+    f.fold_at = (cus + a.kv_heads - 1) / a.kv_heads;  // row tiles that come one to a CU
+    f.fold_most = a.splits == 1 && a.head_dim < 256 ? 2 * cus : 0;
+    if (a.head_dim == 64) return launch_d<64>(f, grid, st);
+    if (a.head_dim == 128) return launch_d<128>(f, grid, st);
+    return launch_d<256>(f, grid, st);
 }
 
 }  // namespace fp4k

@@ -212,6 +212,7 @@ struct PrefillArgs {
     int out_bf16;
     int64_t o_tok, o_head;
     float *lse;
+    int fold_at, fold_most;  // order of the row tiles (set by the launcher)
     int splits;      // parts of every row tile's keys; 1: no partial results
     float *part_o;   // [row tile, key head][split][row][head_dim]
     float *part_ml;  // [row tile, key head][split][row][2]
