@@ -685,8 +685,8 @@ __device__ __forceinline__ uint32_t bf16x2_rne(float lo, float hi)
     return r;
 }
 
-// The (k or v, head) and the first token of this workgroup: U passes of 2048 / head_dim
-// tokens of one head.
+// The (k or v, head) and the first token of this workgroup, which takes passes of 2048 /
+// head_dim tokens of one head.
 struct KvTile {
     int side, head;
     uint32_t t0;
@@ -701,55 +701,51 @@ __device__ __forceinline__ KvTile kv_tile(const KvArgs &a, uint32_t tile_tokens)
     return k;
 }
 
-template <int FMT, typename T, int U>
+// One row a lane group: with two or four in flight the call got slower (11829 tokens of 8 heads
+// of 128, one / two / four: bf16 16.7 / 26.7 / 28.0 us, NVFP4 14.0 / 15.6 / 16.9 us; 62 to 97 MB,
+// 4.4 to 5.8 TB/s), as the chip is full of waves either way and the writes then come in
+// longer strides.
+template <int FMT, typename T>
 __global__ __launch_bounds__(256) void k_kv_append(KvArgs a, int lane_shift)
 {
-    const uint32_t pass = 256u >> lane_shift;  // tokens of a pass
-    const KvTile tile = kv_tile(a, pass * U);
-    const uint32_t c8 = threadIdx.x & ((1u << lane_shift) - 1u), row = threadIdx.x >> lane_shift;
-    const T *xp = reinterpret_cast<const T *>(tile.side ? a.x[1] : a.x[0]) + tile.head * (tile.side ? a.head[1] : a.head[0]) + c8 * 8;
-    const int64_t tok = tile.side ? a.tok[1] : a.tok[0];
+    const uint32_t pass = 256u >> lane_shift;  // tokens of the workgroup
+    const KvTile tile = kv_tile(a, pass);
+    const uint32_t c8 = threadIdx.x & ((1u << lane_shift) - 1u), t = tile.t0 + (threadIdx.x >> lane_shift);
+    const T *xp = reinterpret_cast<const T *>(tile.side ? a.x[1] : a.x[0]) + t * (tile.side ? a.tok[1] : a.tok[0]) +
+                  tile.head * (tile.side ? a.head[1] : a.head[0]) + c8 * 8;
     uint8_t *codes = tile.side ? a.codes[1] : a.codes[0], *scales = tile.side ? a.scales[1] : a.scales[0];
-    int64_t slot[U];
-    float v[U][8];
-    uint4 raw[U];
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-        const uint32_t t = tile.t0 + i * pass + row;
-        slot[i] = -1;
-        if (t < a.tokens) {  // whole rows, so whole blocks, of lanes
-            slot[i] = a.slots[t];
-            if constexpr (FMT == FP4_KV_BF16 && sizeof(T) == 2) raw[i] = *reinterpret_cast<const uint4 *>(xp + t * tok);
-            else Vec8<T>::load(xp + t * tok, v[i]);
-        }
+    // the row is requested together with its slot, not after it (a return between the two let the
+    // compiler wait for the slot first: 60000 MXFP8 tokens 70 -> 88 us)
+    int64_t slot = -1;
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    if (t < a.tokens) {  // whole rows, so whole blocks, of lanes
+        slot = a.slots[t];
+        if constexpr (FMT == FP4_KV_BF16 && sizeof(T) == 2) raw = *reinterpret_cast<const uint4 *>(xp);
+        else Vec8<T>::load(xp, v);
     }
-    int bad_any = 0;
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-        const bool stored = slot[i] >= 0 && slot[i] < (a.pages << a.page_shift);
-        if (!stored) continue;
-        const int64_t page = slot[i] >> a.page_shift;
-        const uint32_t off = (uint32_t)slot[i] & ((1u << a.page_shift) - 1u);
-        const int64_t block = (page * a.kv_heads + tile.head) << a.page_shift;
-        if constexpr (FMT == FP4_KV_BF16) {
-            if constexpr (sizeof(T) == 4)
-                raw[i] = make_uint4(bf16x2_rne(v[i][0], v[i][1]), bf16x2_rne(v[i][2], v[i][3]), bf16x2_rne(v[i][4], v[i][5]),
-                                    bf16x2_rne(v[i][6], v[i][7]));
-            *reinterpret_cast<uint4 *>(codes + ((((block + off) << lane_shift) + c8) << 4)) = raw[i];
-        } else {
-            constexpr int kBlkShift = FMT == FP4_KV_NVFP4 ? 1 : 2;  // lanes of a block
-            constexpr int kUnitB = FMT == FP4_KV_MXFP8 ? 8 : 4;     // code bytes of a unit
-            uint32_t byte;
-            const float s = FMT == FP4_KV_NVFP4 ? (tile.side ? a.tscale[1] : a.tscale[0])[tile.head] : 0.0f;
-            const uint2 w = kv_encode8<FMT>(v[i], s, a.rule, byte, bad_any);
-            uint8_t *cp = codes + (((block + off) << lane_shift) + c8) * kUnitB;
-            if constexpr (kUnitB == 8) *reinterpret_cast<uint2 *>(cp) = w;
-            else *reinterpret_cast<uint32_t *>(cp) = w.x;
-            if ((c8 & ((1u << kBlkShift) - 1u)) == 0u)
-                scales[(block << (lane_shift - kBlkShift)) + ((c8 >> kBlkShift) << a.page_shift) + off] = (uint8_t)byte;
-        }
+    if (slot < 0 || slot >= (a.pages << a.page_shift)) return;
+    const int64_t page = slot >> a.page_shift;
+    const uint32_t off = (uint32_t)slot & ((1u << a.page_shift) - 1u);
+    const int64_t block = (page * a.kv_heads + tile.head) << a.page_shift;
+    if constexpr (FMT == FP4_KV_BF16) {
+        if constexpr (sizeof(T) == 4)
+            raw = make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
+        *reinterpret_cast<uint4 *>(codes + ((((block + off) << lane_shift) + c8) << 4)) = raw;
+    } else {
+        constexpr int kBlkShift = FMT == FP4_KV_NVFP4 ? 1 : 2;  // lanes of a block
+        constexpr int kUnitB = FMT == FP4_KV_MXFP8 ? 8 : 4;     // code bytes of a unit
+        uint32_t byte;
+        int bad = 0;
+        const float s = FMT == FP4_KV_NVFP4 ? (tile.side ? a.tscale[1] : a.tscale[0])[tile.head] : 0.0f;
+        const uint2 w = kv_encode8<FMT>(v, s, a.rule, byte, bad);
+        uint8_t *cp = codes + (((block + off) << lane_shift) + c8) * kUnitB;
+        if constexpr (kUnitB == 8) *reinterpret_cast<uint2 *>(cp) = w;
+        else *reinterpret_cast<uint32_t *>(cp) = w.x;
+        if ((c8 & ((1u << kBlkShift) - 1u)) == 0u)
+            scales[(block << (lane_shift - kBlkShift)) + ((c8 >> kBlkShift) << a.page_shift) + off] = (uint8_t)byte;
+        if (bad && a.nonfinite) *a.nonfinite = 1;
     }
-    if (bad_any && a.nonfinite) *a.nonfinite = 1;
 }
 
 // The last sequence b with cu[b] <= t (0 when there is none): 64 offsets at a time.
@@ -1048,27 +1044,13 @@ fp4_status launch_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, 
 
 static int kv_lane_shift(const KvArgs &a) { return a.head_dim == 64 ? 3 : a.head_dim == 128 ? 4 : 5; }
 
-// Passes of a workgroup: four (their loads in flight together) when that still leaves
-// two workgroups a CU, else one, so that a small call spreads over the chip.
-static bool kv_four(const KvArgs &a)
-{
-    const int64_t pass = 256 >> kv_lane_shift(a);
-    return (a.tokens + 4 * pass - 1) / (4 * pass) * 2 * a.kv_heads >= 2 * device_cu_count();
-}
-
-template <int FMT, typename T, int U>
-static void launch_append_u(const KvArgs &a, hipStream_t st)
-{
-    const uint32_t tile = (256u >> kv_lane_shift(a)) * U, tiles = (uint32_t)((a.tokens + tile - 1) / tile);
-    hipLaunchKernelGGL((k_kv_append<FMT, T, U>), dim3(tiles * 2 * a.kv_heads), dim3(256), 0, st, a, kv_lane_shift(a));
-}
-
 template <int FMT>
 static void launch_append_fmt(const KvArgs &a, fp4_dtype xt, hipStream_t st)
 {
-    const bool four = kv_four(a);
-    if (xt == FP4_BF16) four ? launch_append_u<FMT, uint16_t, 4>(a, st) : launch_append_u<FMT, uint16_t, 1>(a, st);
-    else four ? launch_append_u<FMT, float, 4>(a, st) : launch_append_u<FMT, float, 1>(a, st);
+    const uint32_t pass = 256u >> kv_lane_shift(a), tiles = (uint32_t)((a.tokens + pass - 1) / pass);
+    const dim3 grid(tiles * 2 * a.kv_heads);
+    if (xt == FP4_BF16) hipLaunchKernelGGL((k_kv_append<FMT, uint16_t>), grid, dim3(256), 0, st, a, kv_lane_shift(a));
+    else hipLaunchKernelGGL((k_kv_append<FMT, float>), grid, dim3(256), 0, st, a, kv_lane_shift(a));
 }
 
 fp4_status launch_kv_append(const KvArgs &a, fp4_kv_format fmt, fp4_dtype xt, hipStream_t st)
@@ -1090,7 +1072,11 @@ static void launch_read_u(const KvArgs &a, hipStream_t st)
 template <int FMT>
 static void launch_read_fmt(const KvArgs &a, fp4_dtype yt, hipStream_t st)
 {
-    const bool four = kv_four(a);
+    // four passes a workgroup (their loads in flight together: 59833 NVFP4 tokens of 8 heads of 128 in
+    // 79 us, two passes 95 us) when that still leaves two workgroups a CU, else one, so that a small
+    // call spreads over the chip
+    const int64_t pass = 256 >> kv_lane_shift(a);
+    const bool four = (a.tokens + 4 * pass - 1) / (4 * pass) * 2 * a.kv_heads >= 2 * device_cu_count();
     if (yt == FP4_BF16) four ? launch_read_u<FMT, true, 4>(a, st) : launch_read_u<FMT, true, 1>(a, st);
     else four ? launch_read_u<FMT, false, 4>(a, st) : launch_read_u<FMT, false, 1>(a, st);
 }
