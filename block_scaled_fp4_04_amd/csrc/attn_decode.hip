@@ -682,11 +682,11 @@ __global__ __launch_bounds__((64 * Shape<FMT, D, SPLIT>::kWaves), (SPLIT ? Shape
 
 // One workgroup per (sequence, query head): adds up the partial results of a row
 // that several workgroups of k_attn_decode share.  Four d a thread, the partial
-// results dealt to 1024 / D groups of threads.
-template <int D>
-__global__ __launch_bounds__(256) void k_attn_decode_join(DecodeArgs a, int grid_full)
+// results dealt to 4 THREADS / D groups of threads.
+template <int D, int THREADS>
+__global__ __launch_bounds__(THREADS) void k_attn_decode_join(DecodeArgs a, int grid_full)
 {
-    constexpr int kLanes = D / 4, kParts = 256 / kLanes;
+    constexpr int kLanes = D / 4, kParts = THREADS / kLanes;
     __shared__ f32x4 sm[kParts][kLanes];
     __shared__ float sm_m[kParts], sm_l[kParts];
     const int b = blockIdx.x / a.heads, head = blockIdx.x - b * a.heads;
@@ -776,7 +776,10 @@ static void launch_decode(const DecodeArgs &a, hipStream_t st)
     const int64_t most = S::kPerCu * (int64_t)device_cu_count();
     const int grid = (int)(units < most ? units : most);
     hipLaunchKernelGGL((k_attn_decode<FMT, D, true>), dim3(grid), dim3(64 * S::kWaves), 0, st, a);
-    hipLaunchKernelGGL(k_attn_decode_join<D>, dim3((unsigned)(a.seqs * a.heads)), dim3(256), 0, st, a, grid);
+    // a wave a row where there are many (their parts are few), else four (2560 rows 6.6 -> 5.3 us)
+    const dim3 jg((unsigned)(a.seqs * a.heads));
+    if (a.seqs * a.heads > 1024) hipLaunchKernelGGL((k_attn_decode_join<D, 64>), jg, dim3(64), 0, st, a, grid);
+    else hipLaunchKernelGGL((k_attn_decode_join<D, 256>), jg, dim3(256), 0, st, a, grid);
 }
 
 template <int FMT>
