@@ -177,39 +177,36 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_prefill(PrefillA
         for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
     float m = -INFINITY, l = 0.0f;
 
-    // K and V tiles go to LDS through a descriptor that ends with the tile's last row: rows
-    // past the sequence arrive as zeros.  A wave's copies are kStep rows apart, which
-    // leaves their swizzle alone (D = 256: alternates it).
+    // K and V tiles go to LDS through a descriptor that ends with the sequence's last row: rows
+    // past it arrive as zeros.  The whole offset of a row is the lane's: the range check then
+    // compares it with the descriptor's size alone.  (A row in the scalar offset is taken off the
+    // size first, which a copy wholly past the end would bring below zero.)  A wave's copies are
+    // kStep rows apart, which leaves their swizzle alone (D = 256: alternates it).
     constexpr int kStep = 4096 / kRowB;
     constexpr int kOfs = D == 256 ? 2 : 1;
     uint32_t k_ofs[kOfs], v_ofs[kOfs];
 #pragma unroll
     for (int i = 0; i < kOfs; ++i) {
-        const int r = i * kStep + (wave * 1024 + lane * 16) / kRowB, slot = (lane * 16 % kRowB) / 16;
-        k_ofs[i] = (uint32_t)(r * (int)a.k_tok + (slot ^ swz_k<D>(r)) * 8) * 2 - i * kStep * (uint32_t)a.k_tok * 2;
-        v_ofs[i] = (uint32_t)(r * (int)a.v_tok + (slot ^ swz_v<D>(r)) * 8) * 2 - i * kStep * (uint32_t)a.v_tok * 2;
+        const int r = (wave * 1024 + lane * 16) / kRowB, slot = (lane * 16 % kRowB) / 16;  // row of a copy, chunk
+        k_ofs[i] = (uint32_t)(r * (int)a.k_tok + (slot ^ swz_k<D>(i * kStep + r)) * 8) * 2;
+        v_ofs[i] = (uint32_t)(r * (int)a.v_tok + (slot ^ swz_v<D>(i * kStep + r)) * 8) * 2;
     }
     const uint16_t *kb = a.k + k0 * a.k_tok + hkv * a.k_head;
     const uint16_t *vb = a.v + k0 * a.v_tok + hkv * a.v_head;
-    auto rsrc = [&](const uint16_t *p, int64_t tok, int key0) {
+    auto stage = [&](const uint16_t *base, int tok, const uint32_t (&ofs)[kOfs], int key0, uint8_t *dst)
+                     __attribute__((always_inline)) {
         const int n = lk - key0 < kKeys ? lk - key0 : kKeys;
-        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(p + key0 * tok), (short)0, ((n - 1) * (int)tok + D) * 2,
-                                                 0x00020000);
-    };
-    auto stage_k = [&](int key0, uint8_t *dst) __attribute__((always_inline)) {
-        const __amdgpu_buffer_rsrc_t r = rsrc(kb, a.k_tok, key0);
+        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(base + key0 * (int64_t)tok),
+                                                                           (short)0, ((n - 1) * tok + D) * 2, 0x00020000);
+        int step = kStep * tok * 2;
+        if constexpr (D == 256) asm volatile("" : "+s"(step));  // the sums are formed here, not kept in registers (which spill)
 #pragma unroll
         for (int j = 0; j < kCopies; ++j)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(dst + wave * 1024 + j * 4096), 16, (int)k_ofs[j % kOfs],
-                                                     j * kStep * (int)a.k_tok * 2, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(dst + wave * 1024 + j * 4096), 16,
+                                                     (int)(ofs[j % kOfs] + (uint32_t)(j * step)), 0, 0, 0);
     };
-    auto stage_v = [&](int key0, uint8_t *dst) __attribute__((always_inline)) {
-        const __amdgpu_buffer_rsrc_t r = rsrc(vb, a.v_tok, key0);
-#pragma unroll
-        for (int j = 0; j < kCopies; ++j)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(dst + wave * 1024 + j * 4096), 16, (int)v_ofs[j % kOfs],
-                                                     j * kStep * (int)a.v_tok * 2, 0, 0);
-    };
+    auto stage_k = [&](int key0, uint8_t *dst) __attribute__((always_inline)) { stage(kb, (int)a.k_tok, k_ofs, key0, dst); };
+    auto stage_v = [&](int key0, uint8_t *dst) __attribute__((always_inline)) { stage(vb, (int)a.v_tok, v_ofs, key0, dst); };
 
     const float c = fmaxf(a.scale_log2, 0x1p-140f);  // a scale of 0: a masked key's -inf stays
     const int c16 = lane & 15, dgrp = (lane >> 4) & 1;
