@@ -1057,7 +1057,7 @@ def _kv(cache: KVCache):
 def _heads(t: torch.Tensor, dtypes, what: str):
     """(tokens, heads, dim, token stride, head stride) of [tokens, heads, dim] with unit stride along dim.
     The stride of a dimension of size 1 is never followed, and torch may report any value for it: it
-    is given as that of a contiguous tensor then."""
+    is given as `dim` then, which passes every check of strides."""
     if t.dtype not in dtypes:
         raise TypeError(f"{what} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
     if t.dim() != 3:
@@ -1069,7 +1069,7 @@ def _heads(t: torch.Tensor, dtypes, what: str):
     if h <= 1:
         sh = d
     if n <= 1:
-        sn = h * sh if h * sh > d else d
+        sn = d
     return n, h, d, sn, sh
 
 

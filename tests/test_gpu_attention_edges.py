@@ -47,3 +47,19 @@ def test_prompt_ends_before_nan(dim, causal):
         last = [i + 1 if causal else m for i in range(m)]
         want = ref.attention(q[at].double(), k[at].double(), v[at].double(), dim ** -0.5, [0] * m, last)
         ref.check(out[at], lse[at], want, dim, 2.0 ** -8, f"{m} keys before NaN, head_dim {dim}")
+
+
+def test_one_token_of_head_major_buffers():
+    """A single query and key as views of large head-major buffers (their token stride is never followed)."""
+    fp4 = _fp4()
+    heads, dim = 8, 128
+    q, k, v = (torch.randn(heads, 32768, dim, device="cuda").to(torch.bfloat16)[:, 5:6].transpose(0, 1) for _ in range(3))
+    hold = torch.zeros(heads, 32768, dim, device="cuda", dtype=torch.bfloat16)
+    out = hold[:, 7:8].transpose(0, 1)
+    fp4.attn_prefill(q, k, v, _cu([1]), _cu([1]), out=out)
+    assert torch.equal(out, v) and int((hold != 0).any(-1).sum()) == heads
+    c = fp4.KVCache.alloc("bf16", 2, heads, 16, dim)
+    fp4.kv_cache_append(c, k, v, torch.tensor([19], dtype=torch.int64, device="cuda"))
+    table, one = torch.tensor([[1]], dtype=torch.int32, device="cuda"), torch.tensor([4], dtype=torch.int32, device="cuda")
+    c.k_codes[1, :, :3], c.v_codes[1, :, :3] = c.k_codes[1, :, 3:4], c.v_codes[1, :, 3:4]
+    assert torch.equal(fp4.attn_decode_paged(q, c, table, one), v)
