@@ -1155,29 +1155,34 @@ def kv_cache_read(cache: KVCache, block_table: torch.Tensor, cu_seqlens: torch.T
     return k_out, v_out
 
 
+def _device() -> int:
+    """The current device, which the workspace sizes depend on (-1 where no device is in use)."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+
+
 @functools.lru_cache(maxsize=4096)
-def _decode_need(seqs, heads, kv_heads, page_size, head_dim, table_width) -> int:
-    """Workspace bytes, by the sizes alone."""
+def _decode_need(device, seqs, heads, kv_heads, page_size, head_dim, table_width) -> int:
+    """Workspace bytes, by the current device and the sizes."""
     sizes = _KvCacheArg(KV_BF16, 1, kv_heads, page_size, head_dim)
     return lib().attn_decode_paged_workspace(seqs, heads, ctypes.byref(sizes), table_width)
 
 
 @functools.lru_cache(maxsize=4096)
-def _prefill_need(q_tokens, heads, k_tokens, kv_heads, head_dim, seqs) -> int:
+def _prefill_need(device, q_tokens, heads, k_tokens, kv_heads, head_dim, seqs) -> int:
     return lib().attn_prefill_workspace(q_tokens, heads, k_tokens, kv_heads, head_dim, seqs)
 
 
 def attn_decode_paged_workspace(cache: KVCache, seqs: int, heads: int, table_width: int) -> torch.Tensor:
     """A workspace for attn_decode_paged calls of these sizes."""
-    return torch.empty(_decode_need(seqs, heads, cache.kv_heads, cache.page_size, cache.head_dim, table_width),
-                       dtype=torch.uint8, device=cache.device)
+    need = _decode_need(_device(), seqs, heads, cache.kv_heads, cache.page_size, cache.head_dim, table_width)
+    return torch.empty(need, dtype=torch.uint8, device=cache.device)
 
 
 def attn_prefill_workspace(q_tokens: int, heads: int, k_tokens: int, kv_heads: int, head_dim: int, seqs: int,
                            device="cuda") -> torch.Tensor:
     """A workspace for attn_prefill calls of these sizes."""
-    return torch.empty(_prefill_need(q_tokens, heads, k_tokens, kv_heads, head_dim, seqs), dtype=torch.uint8,
-                       device=device)
+    need = _prefill_need(_device(), q_tokens, heads, k_tokens, kv_heads, head_dim, seqs)
+    return torch.empty(need, dtype=torch.uint8, device=device)
 
 
 def attn_decode_paged(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -1199,7 +1204,7 @@ def attn_decode_paged(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor
     out, ot, oh = _out_heads(out, n, h, d, dtype, q)
     if lse is not None:
         _lse(lse, n, h)
-    need = _decode_need(n, h, cache.kv_heads, cache.page_size, d, width)
+    need = _decode_need(_device(), n, h, cache.kv_heads, cache.page_size, d, width)
     if need or workspace is not None:
         workspace = _workspace(workspace, need, q)
     _need_cuda(cache.k_codes, q, block_table, seq_lens, out, lse, workspace)
@@ -1232,7 +1237,7 @@ def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q
     out, ot, oh = _out_heads(out, n, h, d, dtype, q)
     if lse is not None:
         _lse(lse, n, h)
-    need = _prefill_need(n, h, nk, hk, d, seqs)
+    need = _prefill_need(_device(), n, h, nk, hk, d, seqs)
     if need or workspace is not None:
         workspace = _workspace(workspace, need, q)
     _need_cuda(q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse, workspace)

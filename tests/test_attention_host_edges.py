@@ -19,3 +19,21 @@ def test_one_token_of_a_head_major_buffer(fp4, room):  # noqa: F811
             got = host._prefill(fp4, kn=n, heads=8, kv=8, dim=128, kt=tok, kh=head, vt=tok, vh=head, qn=n, qt=tok, qh=head,
                                 ott=tok, oh=head)
             assert got == NO_DEVICE, n
+
+
+def test_workspace_sizes_are_kept_by_device(fp4, monkeypatch):  # noqa: F811
+    """The library sizes a workspace by the current device's CUs: what one device needs says nothing of another."""
+    class Lib:  # the two queries on devices of 256 and 304 CUs
+        attn_prefill_workspace = staticmethod(lambda *a: cus[now] * 16)
+        attn_decode_paged_workspace = staticmethod(lambda *a: cus[now] * 32)
+
+    cus, now = {0: 256, 1: 304}, 0
+    monkeypatch.setattr(fp4, "lib", lambda: Lib)
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now)
+    cache = type("Sizes", (), dict(kv_heads=2, page_size=16, head_dim=64, device="cpu"))
+    fp4._decode_need.cache_clear(), fp4._prefill_need.cache_clear()
+    for now in (0, 1, 0):
+        assert fp4.attn_prefill_workspace(5, 8, 90001, 2, 64, 1, device="cpu").numel() == cus[now] * 16
+        assert fp4.attn_decode_paged_workspace(cache, 3, 8, 12345).numel() == cus[now] * 32
+    fp4._decode_need.cache_clear(), fp4._prefill_need.cache_clear()
