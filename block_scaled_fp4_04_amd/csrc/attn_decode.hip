@@ -21,8 +21,8 @@
 //                the widened pairs), so V needs no LDS either.
 // The running maximum is common to the four lane groups and moves only when a new
 // score exceeds it by more than 2^8 (log2 units: 8), so the exchange between lanes
-// and the rescaling are rare; P stays below 2^8, which neither its 16-bit form nor the
-// fp32 sums mind.  P is rounded to 16 bits (bf16, or f16 for NVFP4) because the matrix
+// and the rescaling are rare; P stays below 2^8 (NVFP4: 2^15), which neither its 16-bit
+// form nor the fp32 sums mind.  P is rounded to 16 bits (bf16, or f16 for NVFP4) because the matrix
 // core takes 16-bit operands; sums, maxima and outputs stay fp32 until the store.
 //
 // Widening: E2M1 / E4M3 times a power of two is exact in bf16 (MXFP4, MXFP8); E2M1
@@ -48,6 +48,10 @@ namespace {
 constexpr int kTile = 128;          // keys of one work unit
 constexpr int kOver = 1;            // what a row costs beside its tiles, in units
 constexpr float kLazy = 8.0f;       // log2 headroom before the running maximum moves
+// log2 by which the softmax weights of the f16 form (NVFP4) stand above 1 where the running maximum
+// was taken: they stay below 2^15, and the smallest f16 is then 2^-31 of the largest weight rather
+// than 2^-24, below which a weight would count in the softmax sum and be lost from the output
+constexpr float kRaise = 7.0f;
 
 constexpr int kv_bits(int fmt) { return fmt == FP4_KV_BF16 ? 16 : fmt == FP4_KV_MXFP8 ? 8 : 4; }
 constexpr int kv_block(int fmt) { return fmt == FP4_KV_NVFP4 ? 16 : 32; }
@@ -499,7 +503,8 @@ __global__ __launch_bounds__((64 * Shape<FMT, D, SPLIT>::kWaves), (SPLIT ? Shape
         f32x4 o[C::kDT];
 #pragma unroll
         for (int i = 0; i < C::kDT; ++i) o[i] = f32x4{0, 0, 0, 0};
-        float m = -INFINITY, l = 0.0f;
+        constexpr float kUp = C::kF16 ? kRaise : 0.0f;
+        float m = -INFINITY, l = 0.0f;  // m: the running maximum less kUp
 
         // scores of the 32 keys in kr: s[j] holds keys 16 j + 4 g .. + 3 of head n
         auto scores = [&](f32x4 (&s)[2]) {
@@ -540,8 +545,8 @@ __global__ __launch_bounds__((64 * Shape<FMT, D, SPLIT>::kWaves), (SPLIT ? Shape
         auto weights = [&](f32x4 (&s)[2]) -> uint4 {
             const float tm = c * fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
                                        fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
-            if (__ballot(tm > m + kLazy)) {
-                const float mn = fmaxf(m, xor16_max(tm));
+            if (__ballot(tm > m + (kUp + kLazy))) {
+                const float mn = fmaxf(m, xor16_max(tm) - kUp);
                 const float alpha = mn == m ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
                 m = mn;
                 l *= alpha;

@@ -63,3 +63,34 @@ def test_one_token_of_head_major_buffers():
     table, one = torch.tensor([[1]], dtype=torch.int32, device="cuda"), torch.tensor([4], dtype=torch.int32, device="cuda")
     c.k_codes[1, :, :3], c.v_codes[1, :, :3] = c.k_codes[1, :, 3:4], c.v_codes[1, :, 3:4]
     assert torch.equal(fp4.attn_decode_paged(q, c, table, one), v)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("n", [1000, 20000])
+def test_decode_weights_far_below_the_largest(fmt, n):
+    """Every eighth key takes nearly all of the weight and has zeros as its values; the others, about 2^-26 of
+    it each, make the whole output.  f16 weights stand 2^7 above 1, so one below 2^-14 is off by at most 2^-25,
+    which is 2^-32 of the largest weight; the sum of the weights is n / 8 largest ones.  bf16 ones keep their range."""
+    fp4 = _fp4()
+    g = torch.Generator().manual_seed(n)
+    dim, page = 64, 64
+    k, v = torch.zeros(n, 1, dim), torch.rand(n, 1, dim, generator=g) + 0.5
+    k[:, 0, 0] = 1.2 + 0.6 * torch.rand(n, generator=g)
+    k[::8, 0, 0], v[::8] = 6.0, 0.0
+    ts = torch.tensor([1.0 / 64]) if fmt == "nvfp4" else None
+    pages = (n + page - 1) // page
+    c = fp4.KVCache.alloc(fmt, pages, 1, page, dim, "cuda", *([None] * 2 if ts is None else [ts.cuda()] * 2))
+    fp4.kv_cache_append(c, k.cuda(), v.cuda(), torch.arange(n, device="cuda"))
+    t = None if ts is None else ts.numpy()
+    kk, vv = (torch.from_numpy(ref.decode_rows(fmt, *ref.encode_rows(fmt, x.numpy(), t), t)) for x in (k, v))
+    q = torch.zeros(1, 2, dim)
+    q[0, :, 0] = torch.tensor([4.0, 4.125])
+    q = q.to(torch.bfloat16)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    lse = torch.empty(1, 2, device="cuda")
+    out = fp4.attn_decode_paged(q.cuda(), c, table, torch.tensor([n], dtype=torch.int32, device="cuda"), scale=1.0,
+                                dtype=torch.float32, lse=lse)
+    want = ref.attention(q.double(), kk, vv, 1.0, [0], [n])
+    half = fmt == "nvfp4"
+    small = 2.0 ** -8 * vv.abs().sum(0)[None] / (n / 8)  # (the check takes 2^-24 of it)
+    ref.check(out, lse, want, dim, 2.0 ** -11 if half else 2.0 ** -8, f"{fmt} {n}", small if half else None)
