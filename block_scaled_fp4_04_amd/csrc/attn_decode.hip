@@ -52,6 +52,10 @@ constexpr float kLazy = 8.0f;       // log2 headroom before the running maximum 
 // was taken: they stay below 2^15, and the smallest f16 is then 2^-31 of the largest weight rather
 // than 2^-24, below which a weight would count in the softmax sum and be lost from the output
 constexpr float kRaise = 7.0f;
+// Past this running maximum the rounding of scale * score and of the maximum differ by enough to matter
+// in exp2(fma(score, scale, -maximum)) (by a factor 2^(2^-4) here, by any factor beyond): the two are
+// then rounded alike before they are subtracted.
+constexpr float kFar = 0x1p20f;
 
 constexpr int kv_bits(int fmt) { return fmt == FP4_KV_BF16 ? 16 : fmt == FP4_KV_MXFP8 ? 8 : 4; }
 constexpr int kv_block(int fmt) { return fmt == FP4_KV_NVFP4 ? 16 : 32; }
@@ -505,6 +509,7 @@ __global__ __launch_bounds__((64 * Shape<FMT, D, SPLIT>::kWaves), (SPLIT ? Shape
         for (int i = 0; i < C::kDT; ++i) o[i] = f32x4{0, 0, 0, 0};
         constexpr float kUp = C::kF16 ? kRaise : 0.0f;
         float m = -INFINITY, l = 0.0f;  // m: the running maximum less kUp
+        bool far = false;               // of any head of the wave
 
         // scores of the 32 keys in kr: s[j] holds keys 16 j + 4 g .. + 3 of head n
         auto scores = [&](f32x4 (&s)[2]) {
@@ -552,11 +557,22 @@ __global__ __launch_bounds__((64 * Shape<FMT, D, SPLIT>::kWaves), (SPLIT ? Shape
                 l *= alpha;
 #pragma unroll
                 for (int i = 0; i < C::kDT; ++i) o[i] *= alpha;
+                far = __ballot(m > -INFINITY && __builtin_fabsf(m) > kFar) != 0;
             }
-            const float mm = m == -INFINITY ? 0.0f : -m;
+            float mm = m == -INFINITY ? 0.0f : -m, cs = c;
+            if (far) {
+#pragma clang fp contract(off)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float t = s[i >> 2][i & 3] * c;
+                    s[i >> 2][i & 3] = t + mm;
+                }
+                cs = 1.0f;
+                mm = 0.0f;
+            }
             float p[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][i & 3], c, mm));
+            for (int i = 0; i < 8; ++i) p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][i & 3], cs, mm));
             l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
             return make_uint4(pack2<C::kF16>(p[0], p[1]), pack2<C::kF16>(p[2], p[3]), pack2<C::kF16>(p[4], p[5]),
                               pack2<C::kF16>(p[6], p[7]));

@@ -37,6 +37,10 @@ namespace {
 
 constexpr int kRows = 128;     // rows of a workgroup: four waves of 32
 constexpr float kLazy = 8.0f;  // log2 headroom before the running maximum moves
+// Past this running maximum the rounding of scale * score and of the maximum differ by enough to matter
+// in exp2(fma(score, scale, -maximum)) (by a factor 2^(2^-4) here, by any factor beyond): the two are
+// then rounded alike before they are subtracted.
+constexpr float kFar = 0x1p20f;
 
 // A row tile: its sequence (-1: past the last), its number there, and the sequence's rows,
 // clamped into the buffers.
@@ -212,6 +216,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_prefill(PrefillA
     const int c16 = lane & 15, dgrp = (lane >> 4) & 1;
     auto scores = [&](const uint8_t *kt, f32x16 (&s)[kSub]) __attribute__((always_inline)) {
         const uint8_t *kr = kt + col * kRowB;
+        int first = half ^ swz_k<D>(col);  // this lane's chunk of step 0
+        if constexpr (D == 256) asm volatile("" : "+v"(first));  // the other steps' are formed here, not kept (which spills)
 #pragma unroll
         for (int e = 0; e < 16 * kSub; ++e) s[e >> 4][e & 15] = 0.0f;
 #pragma unroll
@@ -219,10 +225,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_prefill(PrefillA
 #pragma unroll
             for (int j = 0; j < kSub; ++j) {
                 // (the swizzle acts on the low four bits of a chunk's number: beyond, a constant offset)
-                const uint4 f = *reinterpret_cast<const uint4 *>(kr + 32 * j * kRowB + (st >> 3) * 256 + ((((2 * st & 15) + half) ^ swz_k<D>(col)) * 16));
+                const uint4 f = *reinterpret_cast<const uint4 *>(kr + 32 * j * kRowB + (st >> 3) * 256 + ((first ^ (2 * st & 15)) * 16));
                 s[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(f), as_bf16x8(q[st]), s[j], 0, 0, 0);
             }
     };
+    uint64_t far = 0;  // lanes whose |m| is past kFar: with any, settle() scales the scores and takes m off
     // masks the scores of tile key0 and moves the running maximum
     auto settle = [&](int key0, f32x16 (&s)[kSub]) __attribute__((always_inline)) {
         if (key0 < w_full_lo || key0 + kKeys > w_full_hi) {
@@ -240,7 +247,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_prefill(PrefillA
 #pragma unroll
         for (int e = 1; e < 16 * kSub; ++e) tm = fmaxf(tm, s[e >> 4][e & 15]);
         tm *= c;
-        if (__ballot(tm > m + kLazy)) {
+        if (__ballot(tm > m + kLazy) | far) {
             const float mn = fmaxf(m, fmaxf(tm, other_half(tm)));
             const float alpha = mn == m ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
             m = mn;
@@ -249,16 +256,26 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_prefill(PrefillA
             for (int i = 0; i < kDT; ++i)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) o[i][e] *= alpha;
+            far = __ballot(m > -INFINITY && __builtin_fabsf(m) > kFar);
+            if (far) {
+#pragma clang fp contract(off)
+                const float less = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+                for (int e = 0; e < 16 * kSub; ++e) {
+                    const float t = s[e >> 4][e & 15] * c;
+                    s[e >> 4][e & 15] = t - less;
+                }
+            }
         }
     };
     // P of step st: keys 16 st + 8 (j >> 2) + 4 half + (j & 3), registers 8 (st & 1) .. + 7 of s[st >> 1]
     auto weights = [&](const f32x16 (&s)[kSub], uint4 (&p)[2 * kSub]) __attribute__((always_inline)) {
-        const float mm = m == -INFINITY ? 0.0f : -m;
+        const float cs = far ? 1.0f : c, mm = far || m == -INFINITY ? 0.0f : -m;
 #pragma unroll
         for (int st = 0; st < 2 * kSub; ++st) {
             float e[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[st >> 1][8 * (st & 1) + i], c, mm));
+            for (int i = 0; i < 8; ++i) e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[st >> 1][8 * (st & 1) + i], cs, mm));
             l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
             p[st] = make_uint4(pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7]));
         }

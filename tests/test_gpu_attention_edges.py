@@ -94,3 +94,76 @@ def test_decode_weights_far_below_the_largest(fmt, n):
     half = fmt == "nvfp4"
     small = 2.0 ** -8 * vv.abs().sum(0)[None] / (n / 8)  # (the check takes 2^-24 of it)
     ref.check(out, lse, want, dim, 2.0 ** -11 if half else 2.0 ** -8, f"{fmt} {n}", small if half else None)
+
+
+FAR = [3e5, 2e6, 1e9, 1e15, 1e30]
+
+
+def _far_data(n, seed):
+    """Keys of small whole scores with q = 1 or -1, so that every score is exact and the largest ones share all the weight."""
+    g = torch.Generator().manual_seed(seed)
+    k, v = torch.zeros(n, 1, 64), torch.randn(n, 1, 64, generator=g)
+    k[:, 0, 0] = torch.tensor([-3.0, -2.0, -1.0, 0.5, 1.0, 2.0, 3.0, 4.0])[torch.randint(0, 8, (n,), generator=g)]
+    k[torch.randperm(n, generator=g)[:3], 0, 0] = 6.0
+    return k, v
+
+
+def _far_want(q, k, v, scale, last):
+    """The mean of the values whose scores are the largest, and the logarithm.  (Scores are compared before they are
+    scaled: at 1e15 even 64 bits would round the logarithm of a weight.)"""
+    out, lse = torch.zeros(q.shape, dtype=torch.float64), torch.zeros(q.shape[:2], dtype=torch.float64)
+    for i in range(q.shape[0]):
+        for h in range(q.shape[1]):
+            z = k[:last[i], 0] @ q[i, h]
+            top = z == z.max()
+            out[i, h], lse[i, h] = v[:last[i], 0][top].mean(0), z.max() * scale + float(top.sum().double().log())
+    return out, lse
+
+
+def _check_far(out, lse, want, v, what):
+    """The largest scores' weights are equal, so they round alike; the rest is fp32 sums of at most 2^13 terms."""
+    d = (out.cpu().double() - want[0]).abs()
+    assert float(d.max()) <= (2.0 ** -8 + 2.0 ** -11) * float(v.abs().max()), f"{what}: {float(d.max())}"
+    assert bool(((lse.cpu().double() - want[1]).abs() <= 2.0 ** -20 * want[1].abs()).all()), what
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8", "nvfp4", "mxfp4"])
+@pytest.mark.parametrize("n", [700, 5000])
+def test_decode_scores_far_out(fmt, n):
+    """Scores up to the documented scale of 1e30: the largest take all of the weight, however they are rounded."""
+    fp4 = _fp4()
+    k, v = _far_data(n, n)
+    ts = torch.tensor([1.0 / 64]) if fmt == "nvfp4" else None
+    pages = (n + 63) // 64
+    c = fp4.KVCache.alloc(fmt, pages, 1, 64, 64, "cuda", *([None] * 2 if ts is None else [ts.cuda()] * 2))
+    fp4.kv_cache_append(c, k.cuda(), v.cuda(), torch.arange(n, device="cuda"))
+    if fmt == "bf16":
+        kk, vv = (x.to(torch.bfloat16).double() for x in (k, v))
+    else:
+        t = None if ts is None else ts.numpy()
+        kk, vv = (torch.from_numpy(ref.decode_rows(fmt, *ref.encode_rows(fmt, x.numpy(), t), t)) for x in (k, v))
+    q = torch.zeros(1, 2, 64)
+    q[0, :, 0] = torch.tensor([1.0, -1.0])
+    q = q.to(torch.bfloat16)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    for scale in FAR:
+        lse = torch.empty(1, 2, device="cuda")
+        out = fp4.attn_decode_paged(q.cuda(), c, table, torch.tensor([n], dtype=torch.int32, device="cuda"), scale=scale,
+                                    dtype=torch.float32, lse=lse)
+        _check_far(out, lse, _far_want(q.double(), kk, vv, float(np.float32(scale)), [n]), vv, f"{fmt} {n} {scale}")
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_prompt_scores_far_out(dim):
+    """The same for prompts: one of a few rows (keys split among workgroups) and one of many."""
+    fp4 = _fp4()
+    for lq, n in ((3, 5000), (300, 300)):
+        k, v = (torch.nn.functional.pad(x, (0, dim - 64)).to(torch.bfloat16) for x in _far_data(n, n + dim))
+        q = torch.zeros(lq, 2, dim)
+        q[:, :, 0] = torch.tensor([1.0, -1.0])
+        q = q.to(torch.bfloat16)
+        for scale in FAR:
+            lse = torch.empty(lq, 2, device="cuda")
+            out = fp4.attn_prefill(q.cuda(), k.cuda(), v.cuda(), _cu([lq]), _cu([n]), scale=scale, dtype=torch.float32, lse=lse)
+            want = _far_want(q.double(), k.double(), v.double(), float(np.float32(scale)), [i + 1 + n - lq for i in range(lq)])
+            _check_far(out, lse, want, v.double(), f"{dim} {lq} {n} {scale}")
