@@ -31,6 +31,7 @@
 namespace fp4k {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) void lds_void;
 
 namespace {
@@ -130,6 +131,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_prefill(PrefillA
     // Two buffers each for K and V, as objects of their own: the compiler then knows that a
     // copy into one does not touch the others, and does not wait for it at every LDS read.
     __shared__ __align__(16) uint8_t sm_k0[kTileB], sm_k1[kTileB], sm_v0[kTileB], sm_v1[kTileB];
+    __shared__ uint32_t sm_found[2][4];  // by buffer of V and wave: infinities or NaN in what the wave has copied
     const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // blocks: (row tile, split, key head), the key head fastest
@@ -152,12 +154,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_prefill(PrefillA
     const int pos = tok + lk - lq;
     const int ub = a.causal ? pos + 1 : lk;                                  // keys [lb, ub)
     const int lb = a.window > 0 && pos - a.window + 1 > 0 ? pos - a.window + 1 : 0;
-    // the range of keys of the wave and of the workgroup
+    // the range of keys of the workgroup
     auto tok_of = [&](int64_t r) { return (int)((uint32_t)(r < rows ? r : rows - 1) / (uint32_t)a.group); };
     auto ub_of = [&](int t) { return a.causal ? t + lk - lq + 1 : lk; };
     auto lb_of = [&](int t) { const int p = t + lk - lq; return a.window > 0 && p - a.window + 1 > 0 ? p - a.window + 1 : 0; };
-    const int w_t0 = tok_of(row0 + wave * 32), w_t1 = tok_of(row0 + wave * 32 + 31);
-    const int w_full_hi = ub_of(w_t0), w_full_lo = lb_of(w_t1);    // every row of the wave sees [w_full_lo, w_full_hi)
+    const int g_full_hi = ub_of(tok_of(row0)), g_full_lo = lb_of(tok_of(row0 + kRows - 1));  // every row of the workgroup
     int lo = lb_of(tok_of(row0)) & ~(kKeys - 1);
     int hi = ub_of(tok_of(row0 + kRows - 1));
     if (a.splits > 1 && lo < hi) {
@@ -230,9 +231,34 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_prefill(PrefillA
             }
     };
     uint64_t far = 0;  // lanes whose |m| is past kFar: with any, settle() scales the scores and takes m off
-    // masks the scores of tile key0 and moves the running maximum
-    auto settle = [&](int key0, f32x16 (&s)[kSub]) __attribute__((always_inline)) {
-        if (key0 < w_full_lo || key0 + kKeys > w_full_hi) {
+    // A tile that some row of the workgroup does not see whole may hold infinities and NaN in keys that are masked
+    // there, and the product would carry them into every row (0 times them is NaN).  Each wave therefore searches
+    // what it has copied of such a tile before the barrier that hands it over; what is found is cleared in LDS,
+    // and added to the rows that see it at the end, from memory.  (8192 tokens 652 -> 656 us, a windowed chunk
+    // 312 -> 317 us, packed prompts 56.0 -> 55.9 us on one card; searched after the barrier, by every wave, in a
+    // branch of its own 658, 319 and 56.9 us; a loop of its own for the whole tiles 681, 383 and 56.9 us.)
+    auto clean = [&](int key0) { return __builtin_expect(key0 >= g_full_lo && key0 + kKeys <= g_full_hi, 1); };
+    auto search = [&](const uint8_t *vt, uint32_t (&found)[4]) __attribute__((always_inline)) {
+        __builtin_amdgcn_s_waitcnt((0x7 << 4) | (0xF << 8));  // vmcnt(0): the wave's own copies have arrived
+        u16x2 top = {0, 0};
+#pragma unroll
+        for (int j = 0; j < kCopies; ++j) {
+            const u32x4 w = *reinterpret_cast<const u32x4 *>(vt + wave * 1024 + j * 4096 + lane * 16);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t x = w[e] & 0x7FFF7FFFu;
+                u16x2 h;
+                __builtin_memcpy(&h, &x, 4);
+                top = __builtin_elementwise_max(top, h);
+            }
+        }
+        const uint64_t any = __ballot(top[0] >= 0x7F80 || top[1] >= 0x7F80);
+        if (lane == 0) found[wave] = any != 0;
+    };
+    // masks the scores of tile key0, whose values are in vt, and moves the running maximum
+    auto settle = [&](int key0, f32x16 (&s)[kSub], const uint8_t *vt, uint32_t (&found)[4]) __attribute__((always_inline)) {
+        if (!clean(key0)) {
+            search(vt, found);
             // of the lane's keys 8 x + 4 half + i, those in [lb, ub)
             const int first = lb - key0 - 4 * half, last = ub - key0 - 4 * half;
 #pragma unroll
@@ -298,6 +324,24 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_prefill(PrefillA
                 o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(f), as_bf16x8(p[st]), o[i], 0, 0, 0);
             }
     };
+    int spoiled_lo = lk, spoiled_hi = 0;  // keys of the tiles with a find
+    auto clear_masked = [&](int key0, uint8_t *vt, const uint32_t (&found)[4]) __attribute__((always_inline)) {
+        if (clean(key0)) return;
+        if (__builtin_expect(__builtin_amdgcn_readfirstlane(found[0] | found[1] | found[2] | found[3]) == 0, 1)) return;
+        spoiled_lo = key0 < spoiled_lo ? key0 : spoiled_lo;
+        spoiled_hi = key0 + kKeys < lk ? key0 + kKeys : lk;
+#pragma unroll 1
+        for (int at = threadIdx.x * 16; at < kTileB; at += 4096) {
+            u32x4 w = *reinterpret_cast<const u32x4 *>(vt + at);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u;
+                if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu;
+            }
+            *reinterpret_cast<u32x4 *>(vt + at) = w;
+        }
+        __syncthreads();
+    };
 
     // The next tile's scores are formed while this tile's weights are: the matrix core and
     // the vector units then work at once within a wave, not only between the two waves of a SIMD.
@@ -310,34 +354,55 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_prefill(PrefillA
         if (lo + kKeys < hi) stage_k(lo + kKeys, sm_k1);
         stage_v(lo, sm_v0);
         scores(sm_k0, s0);
-        settle(lo, s0);
+        settle(lo, s0, sm_v0, sm_found[0]);
         int key0 = lo;
         // `now`: scores of tile key0; k_next, v_now: the buffers that hold what this pass reads
-        auto pass = [&](f32x16 (&now)[kSub], f32x16 (&next)[kSub], uint8_t *k_now, const uint8_t *k_next, const uint8_t *v_now,
-                        uint8_t *v_next) __attribute__((always_inline)) {
+        auto pass = [&](f32x16 (&now)[kSub], f32x16 (&next)[kSub], uint8_t *k_now, const uint8_t *k_next, uint8_t *v_now,
+                        uint8_t *v_next, const uint32_t (&found)[4], uint32_t (&found_next)[4]) __attribute__((always_inline)) {
             __syncthreads();  // K of the next tile and V of this one have arrived; the other buffers are free
+            clear_masked(key0, v_now, found);
             if (key0 + 2 * kKeys < hi) stage_k(key0 + 2 * kKeys, k_now);
             stage_v(key0 + kKeys, v_next);
             scores(k_next, next);
             weights(now, p);
             values(v_now, p);
-            settle(key0 + kKeys, next);
+            settle(key0 + kKeys, next, v_next, found_next);
             key0 += kKeys;
         };
         while (key0 + 2 * kKeys < hi) {
-            pass(s0, s1, sm_k0, sm_k1, sm_v0, sm_v1);
-            pass(s1, s0, sm_k1, sm_k0, sm_v1, sm_v0);
+            pass(s0, s1, sm_k0, sm_k1, sm_v0, sm_v1, sm_found[0], sm_found[1]);
+            pass(s1, s0, sm_k1, sm_k0, sm_v1, sm_v0, sm_found[1], sm_found[0]);
         }
         if (key0 + kKeys < hi) {
-            pass(s0, s1, sm_k0, sm_k1, sm_v0, sm_v1);
+            pass(s0, s1, sm_k0, sm_k1, sm_v0, sm_v1, sm_found[0], sm_found[1]);
             __syncthreads();
+            clear_masked(key0, sm_v1, sm_found[1]);
             weights(s1, p);
             values(sm_v1, p);
         } else {
             __syncthreads();
+            clear_masked(key0, sm_v0, sm_found[0]);
             weights(s0, p);
             values(sm_v0, p);
         }
+    }
+
+    // a weight times an infinity or NaN is that again, whatever the weight of a key that is seen
+#pragma unroll 1
+    for (int key = spoiled_lo; key < spoiled_hi; ++key) {
+        if (key < lb || key >= ub) continue;
+        const uint16_t *vp = vb + key * a.v_tok + 4 * half;
+#pragma unroll
+        for (int i = 0; i < kDT; ++i)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const u32x2 w = *reinterpret_cast<const u32x2 *>(vp + 32 * i + 8 * x);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float v = __uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
+                    o[i][4 * x + e] += __builtin_fabsf(v) < INFINITY ? 0.0f : v;
+                }
+            }
     }
 
     l += other_half(l);

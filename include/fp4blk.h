@@ -550,8 +550,9 @@ size_t attn_prefill_workspace(int64_t q_tokens, int64_t heads, int64_t k_tokens,
  *  scale, out (fp32 or bf16), lse (fp32 [q_tokens][heads]): as attn_decode_paged.  A
  *         query that sees no key gives a zero row and lse = -inf.
  *  ws     attn_prefill_workspace() bytes, 16-byte aligned.
- * k and v must be finite within a sequence's range.  q_tokens == 0 returns FP4_OK once
- * the other arguments check out; k_tokens == 0 gives zero rows.
+ * An infinity or NaN in k or v reaches only the queries that see its key (in v: only its
+ * column of them).  q_tokens == 0 returns FP4_OK once the other arguments check out;
+ * k_tokens == 0 gives zero rows.
  * q_tokens * heads / kv_heads and k_tokens < 2^31 (FP4_ERR_SHAPE). */
 fp4_status attn_prefill(const void *q, int64_t q_tokens, int64_t heads, int64_t q_token_stride,
                         int64_t q_head_stride, const void *k, const void *v, int64_t k_tokens,

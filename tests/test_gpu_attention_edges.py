@@ -167,3 +167,40 @@ def test_prompt_scores_far_out(dim):
             out = fp4.attn_prefill(q.cuda(), k.cuda(), v.cuda(), _cu([lq]), _cu([n]), scale=scale, dtype=torch.float32, lse=lse)
             want = _far_want(q.double(), k.double(), v.double(), float(np.float32(scale)), [i + 1 + n - lq for i in range(lq)])
             _check_far(out, lse, want, v.double(), f"{dim} {lq} {n} {scale}")
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("lq,lk,window", [(130, 130, 0), (200, 200, 70), (5, 6000, 0), (3, 5000, 900), (600, 1000, 333), (20, 9, 0)])
+def test_prompt_values_that_are_not_numbers_where_masked(dim, lq, lk, window):
+    """Infinities and NaN in V reach exactly the rows and columns that see them: later tokens' and those behind the window
+    leave a row's bits as they are."""
+    fp4 = _fp4()
+    g = torch.Generator().manual_seed(dim + lk)
+    heads, kv = 4, 2
+    q, k, v = _randn(g, lq, heads, dim), _randn(g, lk, kv, dim), _randn(g, lk, kv, dim)
+    pos = torch.arange(lq) + lk - lq
+    at = sorted({lk - 1, lk - 2, lk - lq // 2 - 1, max(0, lk - lq), max(0, lk - lq - window), lk // 2 if window else lk - 1, 0})
+    bad = v.clone()
+    for i, key in enumerate(at):
+        bad[key, i % kv, 7 * i % dim] = (float("inf"), float("-inf"), float("nan"))[i % 3]
+        bad[key, (i + 1) % kv, (7 * i + 1) % dim] = (float("nan"), float("inf"), float("-inf"))[i % 3]
+    run = lambda v: fp4.attn_prefill(q.cuda(), k.cuda(), v.cuda(), _cu([lq]), _cu([lk]), window=window, dtype=torch.float32,  # noqa: E731
+                                     lse=lse).cpu()
+    lse = torch.empty(lq, heads, device="cuda")
+    clean = run(v)
+    lse_clean = lse.clone()
+    got = run(bad)
+    assert torch.equal(lse, lse_clean)
+    # what a row sees of them, by column: sums of infinities and NaN alone
+    keys = torch.arange(lk)
+    seen = keys <= pos[:, None]
+    if window:
+        seen &= keys > pos[:, None] - window
+    hit = torch.where(torch.isfinite(bad), 0.0, bad.float())
+    want = torch.zeros(lq, kv, dim)
+    for key in at:
+        want[seen[:, key]] += hit[key]
+    want = want.repeat_interleave(heads // kv, 1)
+    fine = want == 0
+    assert torch.equal(got[fine], clean[fine])
+    assert torch.equal(torch.nan_to_num(got[~fine], nan=1.0, posinf=2.0, neginf=3.0), torch.nan_to_num(want[~fine], nan=1.0, posinf=2.0, neginf=3.0))
