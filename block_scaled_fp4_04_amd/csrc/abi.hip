@@ -1146,7 +1146,7 @@ size_t attn_prefill_workspace(int64_t q_tokens, int64_t heads, int64_t k_tokens,
 {
     if (q_tokens <= 0 || heads <= 0 || kv_heads <= 0 || heads % kv_heads != 0 || head_dim <= 0 || seqs <= 0) return 0;
     const int64_t group = heads / kv_heads;
-    const int splits = prefill_splits(q_tokens, k_tokens, seqs, kv_heads, group, head_dim);
+    const int splits = prefill_splits(q_tokens, k_tokens, seqs, kv_heads, group, head_dim, 0);  // (a window only lowers it)
     return align256(prefill_part_rows(q_tokens, seqs, kv_heads, group, splits) * (size_t)(head_dim + 2) * 4);
 }
 
@@ -1178,7 +1178,7 @@ fp4_status attn_prefill(const void *q, int64_t q_tokens, int64_t heads, int64_t 
     const size_t need = attn_prefill_workspace(q_tokens, heads, k_tokens, kv_heads, head_dim, seqs);
     if (need > 0 && (!ws || !aligned16(ws) || ws_bytes < need)) return FP4_ERR_WORKSPACE;
     PrefillArgs a = {};
-    a.splits = prefill_splits(q_tokens, k_tokens, seqs, kv_heads, group, head_dim);
+    a.splits = prefill_splits(q_tokens, k_tokens, seqs, kv_heads, group, head_dim, window);
     a.part_o = reinterpret_cast<float *>(ws);
     a.part_ml = a.part_o + prefill_part_rows(q_tokens, seqs, kv_heads, group, a.splits) * head_dim;
     a.q = reinterpret_cast<const uint16_t *>(q);

@@ -91,6 +91,29 @@ __device__ __forceinline__ QTile find_tile(const PrefillArgs &a, int x)
     return {-1, 0, 0, 0, 0, 0};
 }
 
+// The keys [lo, hi) that the rows of a tile see, `lo` rounded down to a tile of keys, and the parts they
+// are cut into, of a.splits at most: as many as parts of kPartKeys make, so that a row tile with few keys
+// among longer ones (or behind a window) has one part, which writes the output itself.  (Four chunks of
+// 33 tokens behind 6000 keys: parts of 256 keys 36.9 us, 448 33.4, 512 32.0, all 32 splits 41.8; sixteen of up
+// to 300 behind 2000: 30.1, 30.1, 31.5, 29.6.)
+constexpr int kPartKeys = 448;
+struct KeyRange {
+    int lo, hi, parts;
+};
+template <int KEYS>
+__device__ __forceinline__ KeyRange key_range(const PrefillArgs &a, const QTile &qt)
+{
+    const uint32_t rows = (uint32_t)qt.lq * (uint32_t)a.group, row0 = (uint32_t)qt.tile * kRows;
+    const int first = (int)(row0 / (uint32_t)a.group) + qt.lk - qt.lq;  // position of the first row
+    const int last = (int)((row0 + kRows < rows ? row0 + kRows - 1 : rows - 1) / (uint32_t)a.group) + qt.lk - qt.lq;
+    KeyRange k;
+    k.lo = (a.window > 0 && first - a.window + 1 > 0 ? first - a.window + 1 : 0) & ~(KEYS - 1);
+    k.hi = a.causal ? last + 1 : qt.lk;
+    const int most = (k.hi - k.lo + kPartKeys - 1) / kPartKeys;
+    k.parts = most < a.splits ? (most < 1 ? 1 : most) : a.splits;
+    return k;
+}
+
 // swizzle of the 16-byte chunks of an LDS row
 template <int D>
 __device__ __forceinline__ int swz_k(int row)
@@ -134,7 +157,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_prefill(PrefillA
     __shared__ uint32_t sm_found[2][4];  // by buffer of V and wave: infinities or NaN in what the wave has copied
     const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // blocks: (row tile, split, key head), the key head fastest
+    // blocks: (row tile, part, key head), the key head fastest
     const int xs = blockIdx.x / a.kv_heads, hkv = blockIdx.x - xs * a.kv_heads;
     const int x = xs / a.splits, split = xs - x * a.splits;
     const QTile qt = find_tile(a, x);
@@ -159,13 +182,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_prefill(PrefillA
     auto ub_of = [&](int t) { return a.causal ? t + lk - lq + 1 : lk; };
     auto lb_of = [&](int t) { const int p = t + lk - lq; return a.window > 0 && p - a.window + 1 > 0 ? p - a.window + 1 : 0; };
     const int g_full_hi = ub_of(tok_of(row0)), g_full_lo = lb_of(tok_of(row0 + kRows - 1));  // every row of the workgroup
-    int lo = lb_of(tok_of(row0)) & ~(kKeys - 1);
-    int hi = ub_of(tok_of(row0 + kRows - 1));
-    if (a.splits > 1 && lo < hi) {
-        const int share = ((hi - lo + kKeys - 1) / kKeys + a.splits - 1) / a.splits * kKeys;
+    const KeyRange range = key_range<kKeys>(a, qt);
+    int lo = range.lo, hi = range.hi;
+    if (range.parts > 1) {
+        const int share = ((hi - lo + kKeys - 1) / kKeys + range.parts - 1) / range.parts * kKeys;
         lo += split * share;
         hi = lo + share < hi ? lo + share : hi;
     }
+    if (split >= range.parts) return;
 
     // ---- Q: the B operand, held for the whole tile
     uint4 q[kSteps];
@@ -407,7 +431,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_prefill(PrefillA
 
     l += other_half(l);
     if (!live) return;
-    if (a.splits > 1) {
+    if (range.parts > 1) {
         // unnormalised sums of this part of the keys; k_attn_prefill_join adds the parts
         const int64_t at = ((int64_t)(x * a.kv_heads + hkv) * a.splits + split) * kRows + wave * 32 + col;
         if (half == 0) *reinterpret_cast<float2 *>(a.part_ml + 2 * at) = make_float2(m, l);
@@ -450,15 +474,17 @@ __global__ __launch_bounds__(256) void k_attn_prefill_join(PrefillArgs a)
     const int64_t q0 = qt.q0, row = (int64_t)qt.tile * kRows + r;
     if (row >= (int64_t)qt.lq * a.group) return;
     const int tok = (int)((uint32_t)row / (uint32_t)a.group), head = hkv * a.group + (int)row - tok * a.group;
+    const int parts = key_range<(D == 256 ? 32 : 64)>(a, qt).parts;
+    if (parts == 1) return;  // written by its workgroup
     const int64_t first = (int64_t)xh * a.splits * kRows + r;
     float M = -INFINITY;
-    for (int s = 0; s < a.splits; ++s) M = fmaxf(M, a.part_ml[2 * (first + s * kRows)]);
+    for (int s = 0; s < parts; ++s) M = fmaxf(M, a.part_ml[2 * (first + s * kRows)]);
     const float Ms = M == -INFINITY ? 0.0f : M;
     const int d = threadIdx.x % kLanes * 4;
     f32x4 acc = {0, 0, 0, 0};
     float L = 0.0f;
 #pragma unroll 4
-    for (int s = 0; s < a.splits; ++s) {
+    for (int s = 0; s < parts; ++s) {
         const int64_t at = first + s * kRows;
         const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + 2 * at);
         if (ml.y == 0.0f) continue;  // saw no key; its sums may not have been written
@@ -483,13 +509,20 @@ int64_t prefill_grid(int64_t q_tokens, int64_t seqs, int64_t kv_heads, int64_t g
     return (q_tokens * group / kRows + more) * kv_heads;
 }
 
-// Parts of every row tile's keys: where the row tiles do not fill half of the workgroups the
-// chip holds (two a CU, one at head_dim 256), as many as do, of at least 512 keys.
-int prefill_splits(int64_t q_tokens, int64_t k_tokens, int64_t seqs, int64_t kv_heads, int64_t group, int64_t head_dim)
+// The most parts of a row tile's keys: where the row tiles do not fill half of the workgroups the
+// chip holds (two a CU, one at head_dim 256), as many as do, but no more than a row tile has work for
+// (key_range).  How long the longest sequence is only the device knows: four times the mean here, which
+// keeps a batch of short prompts in one launch (16 of 64 tokens 16.6 -> 12.4 us, 16 of 200 22.3 -> 12.3) and
+// a long one among short ones split (3000 tokens beside seven of 2 to 600: 43.5 us, by twice the mean 54.1).
+int prefill_splits(int64_t q_tokens, int64_t k_tokens, int64_t seqs, int64_t kv_heads, int64_t group, int64_t head_dim,
+                   int64_t window)
 {
     const int64_t grid = prefill_grid(q_tokens, seqs, kv_heads, group);
     const int64_t room = device_cu_count() * (head_dim == 256 ? 1 : 2) / (grid > 0 ? grid : 1);
-    const int64_t most = k_tokens / 512;
+    const int64_t mean = (k_tokens + seqs - 1) / seqs;
+    int64_t keys = 4 * mean < k_tokens ? 4 * mean : k_tokens;
+    if (window > 0 && window < keys - 2 * kRows) keys = window + 2 * kRows;  // a row tile's tokens, to whole tiles of keys
+    const int64_t most = keys / kPartKeys;
     const int64_t s = room < most ? room : most;
     return s < 1 ? 1 : (s > 64 ? 64 : (int)s);
 }

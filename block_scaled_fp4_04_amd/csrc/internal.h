@@ -213,13 +213,14 @@ struct PrefillArgs {
     int64_t o_tok, o_head;
     float *lse;
     int fold_at, fold_most;  // order of the row tiles (set by the launcher)
-    int splits;      // parts of every row tile's keys; 1: no partial results
+    int splits;      // most parts of a row tile's keys; 1: no partial results
     float *part_o;   // [row tile, key head][split][row][head_dim]
     float *part_ml;  // [row tile, key head][split][row][2]
 };
 
 int64_t prefill_grid(int64_t q_tokens, int64_t seqs, int64_t kv_heads, int64_t group);
-int prefill_splits(int64_t q_tokens, int64_t k_tokens, int64_t seqs, int64_t kv_heads, int64_t group, int64_t head_dim);
+int prefill_splits(int64_t q_tokens, int64_t k_tokens, int64_t seqs, int64_t kv_heads, int64_t group, int64_t head_dim,
+                   int64_t window);
 // rows of partial results (0 without splits)
 size_t prefill_part_rows(int64_t q_tokens, int64_t seqs, int64_t kv_heads, int64_t group, int splits);
 fp4_status launch_attn_prefill(const PrefillArgs &a, hipStream_t st);

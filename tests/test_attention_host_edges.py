@@ -37,3 +37,12 @@ def test_workspace_sizes_are_kept_by_device(fp4, monkeypatch):  # noqa: F811
         assert fp4.attn_prefill_workspace(5, 8, 90001, 2, 64, 1, device="cpu").numel() == cus[now] * 16
         assert fp4.attn_decode_paged_workspace(cache, 3, 8, 12345).numel() == cus[now] * 32
     fp4._decode_need.cache_clear(), fp4._prefill_need.cache_clear()
+
+
+def test_short_prompts_are_not_split(fp4):  # noqa: F811
+    """The keys of a row are its sequence's, not the batch's: many short prompts need no partial results."""
+    need = fp4.lib().attn_prefill_workspace
+    assert need(1024, 8, 1024, 2, 128, 16) == 0      # 16 prompts of 64 tokens
+    assert need(3200, 4, 3200, 1, 128, 16) == 0      # 16 of 200
+    assert need(16, 8, 16 * 40000, 2, 128, 16) > 0   # 16 queries, each behind 39999 keys
+    assert need(16, 8, 60000, 2, 128, 16) > 0        # one of them may have nearly all the keys

@@ -204,3 +204,66 @@ def test_prompt_values_that_are_not_numbers_where_masked(dim, lq, lk, window):
     fine = want == 0
     assert torch.equal(got[fine], clean[fine])
     assert torch.equal(torch.nan_to_num(got[~fine], nan=1.0, posinf=2.0, neginf=3.0), torch.nan_to_num(want[~fine], nan=1.0, posinf=2.0, neginf=3.0))
+
+
+def _attention_on_gpu(q, k, v, scale, first, last):
+    """attention_ref.attention for long sequences: the same terms, a head at a time in float64 on the device."""
+    n, heads, dim = q.shape
+    group = heads // k.shape[1]
+    at = torch.arange(k.shape[0], device="cuda")
+    hidden = (at < first[:, None]) | (at >= last[:, None])
+    out, lse, mass, size = [], [], [], []
+    for h in range(heads):
+        kk, vv = k[:, h // group].double().contiguous(), v[:, h // group].double().contiguous()
+        qq = q[:, h].double().contiguous()
+        z = (qq @ kk.t().contiguous() * scale).masked_fill_(hidden, -float("inf"))
+        lse.append(torch.logsumexp(z, 1))
+        p = torch.exp(z - torch.where(torch.isinf(lse[-1]), 0.0, lse[-1])[:, None])
+        out.append(p @ vv)
+        mass.append(p @ vv.abs())
+        size.append((qq.abs() @ kk.abs().t().contiguous() * scale).masked_fill_(hidden, 0.0).amax(1))
+    return [torch.stack(x, 1).cpu() for x in (out, lse, mass, size)]
+
+
+def _check_prompt(lq, lk, heads, kv, dim, window=0, causal=True, seed=0):
+    fp4 = _fp4()
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    q, k, v = (torch.randn(n, h, dim, device="cuda", generator=g).to(torch.bfloat16) for n, h in ((sum(lq), heads), (sum(lk), kv), (sum(lk), kv)))
+    lse = torch.full((sum(lq), heads), 7.0, device="cuda")
+    out = fp4.attn_prefill(q, k, v, _cu(lq), _cu(lk), causal=causal, window=window, dtype=torch.float32, lse=lse)
+    a = b = 0
+    for n, m in zip(lq, lk):
+        if n:
+            pos = torch.arange(n, device="cuda") + m - n
+            last = (pos + 1 if causal else torch.full_like(pos, m)).clamp(min=0)
+            first = (pos - window + 1).clamp(min=0) if window else torch.zeros_like(pos)
+            want = _attention_on_gpu(q[a:a + n], k[b:b + m], v[b:b + m], dim ** -0.5, first, last) if m else \
+                [torch.zeros(n, heads, dim, dtype=torch.float64), torch.full((n, heads), -float("inf"), dtype=torch.float64),
+                 torch.zeros(n, heads, dim, dtype=torch.float64), torch.zeros(n, heads, dtype=torch.float64)]
+            ref.check(out[a:a + n], lse[a:a + n], want, dim, 2.0 ** -8, f"{n} of {m}, {heads}/{kv}x{dim} window {window} causal {causal}")
+        a, b = a + n, b + m
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_prompt_parts_by_row_tile(dim):
+    """Row tiles of one call with different numbers of parts: none, one, as many as the call has; lengths
+    around a part; windows that leave one part of many keys."""
+    need = _fp4().lib().attn_prefill_workspace
+    for lq, lk, window, heads, kv in (([3, 40, 1, 7, 2], [3000, 40, 447, 448, 449], 0, 4, 2), ([5, 5], [9000, 895], 0, 8, 2),
+                                      ([300, 5, 0, 1], [3000, 60, 0, 897], 0, 4, 1), ([64, 9], [5000, 4000], 600, 4, 2),
+                                      ([64, 9], [5000, 4000], 2000, 4, 2), ([20, 1], [9, 4000], 0, 2, 1)):
+        assert need(sum(lq), heads, sum(lk), kv, dim, len(lq)) > 0
+        _check_prompt(lq, lk, heads, kv, dim, window, seed=dim + sum(lk))
+    _check_prompt([3, 40, 2], [3000, 40, 449], 4, 2, dim, causal=False, seed=dim)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lens,heads,kv", [([7001], 6, 2), ([2500, 1, 0, 2300, 33, 1900], 6, 2), ([3100, 2700], 8, 8), ([8400], 8, 8)])
+def test_prompt_tile_order(dim, lens, heads, kv):
+    """Row tiles that fill the chip once and part of a second time: the second half comes in reverse (every row is checked).
+    [8400] has more than that, so they come in order."""
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    tiles = sum(-(-n * heads // kv // 128) for n in lens)
+    assert -(-cus // kv) < tiles and (tiles * kv <= 2 * cus or lens == [8400])
+    assert _fp4().lib().attn_prefill_workspace(sum(lens), heads, sum(lens), kv, dim, len(lens)) == 0
+    _check_prompt(lens, lens, heads, kv, dim, seed=len(lens))
