@@ -341,7 +341,7 @@ __global__ __launch_bounds__((64 * Shape<FMT, D, SPLIT>::kWaves), (SPLIT ? Shape
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
     const int rows = a.kv_heads * a.head_tiles;
-    const int wg = blockIdx.x;
+    const int wg = blockIdx.x + (SPLIT ? 0 : a.first);
     int u = wg, u_end = wg + 1, b = 0, base = 0;
     SeqSpan sp;
     if constexpr (SPLIT) {
@@ -709,7 +709,7 @@ __global__ __launch_bounds__(THREADS) void k_attn_decode_join(DecodeArgs a, int 
     constexpr int kLanes = D / 4, kParts = THREADS / kLanes;
     __shared__ f32x4 sm[kParts][kLanes];
     __shared__ float sm_m[kParts], sm_l[kParts];
-    const int b = blockIdx.x / a.heads, head = blockIdx.x - b * a.heads;
+    const int row = blockIdx.x + a.first, b = row / a.heads, head = row - b * a.heads;
     const int hkv = head / a.group, hg = head - hkv * a.group, n = hg & 15;
     const int rows = a.kv_heads * a.head_tiles;
     const Plan plan = make_plan(a);
@@ -782,6 +782,18 @@ int decode_grid(int64_t seqs, int64_t kv_heads, int64_t head_tiles, int64_t max_
     return (int)(units < most ? units : most);
 }
 
+// Launches `kernel` over `blocks` workgroups, as several launches where one would pass the 2^32 threads of
+// a launch; a.first is then the first workgroup of each.
+template <typename Kernel>
+static void launch_rows(Kernel kernel, DecodeArgs a, int64_t blocks, int threads, hipStream_t st, int arg = 0)
+{
+    const int64_t most = (int64_t(1) << 31) / threads;
+    for (int64_t first = 0; first < blocks; first += most) {
+        a.first = (int)first;
+        kernel(a, dim3((unsigned)(blocks - first < most ? blocks - first : most)), dim3(threads), st, arg);
+    }
+}
+
 template <int FMT, int D>
 static void launch_decode(const DecodeArgs &a, hipStream_t st)
 {
@@ -790,9 +802,14 @@ static void launch_decode(const DecodeArgs &a, hipStream_t st)
     // a window bounds every row alike: where the rows fill the chip, one launch serves it as well
     // (129 sequences, window 1024, head_dim 256: 28.0 -> 21.5 us; window 4096 loses on ragged batches)
     const int64_t reach = a.window > 0 && a.window + 31 < a.max_len ? a.window + 31 : a.max_len;
-    if (!decode_splits(reach) || (a.window > 0 && reach <= 2100 && a.seqs * rows >= device_cu_count())) {
-        hipLaunchKernelGGL((k_attn_decode<FMT, D, false>), dim3((unsigned)(a.seqs * rows)),
-                           dim3(64 * Shape<FMT, D, false>::kWaves), 0, st, a);
+    // every workgroup of the two launches adds up all lengths, which with this many sequences costs more than
+    // the longest row can gain (sequences, keys of the table: 512, 2048: 48.4 -> 43.8 us; 4096, 2048: 381 -> 242;
+    // 8192, 2048: 357 -> 84; one long row among short ones breaks even at 256, 2048 and 512, 4096)
+    const bool many = 4 * (int64_t)a.seqs >= a.max_len;
+    if (!decode_splits(reach) || many || (a.window > 0 && reach <= 2100 && a.seqs * rows >= device_cu_count())) {
+        launch_rows([](const DecodeArgs &x, dim3 g, dim3 t, hipStream_t s, int) {
+            hipLaunchKernelGGL((k_attn_decode<FMT, D, false>), g, t, 0, s, x);
+        }, a, (int64_t)a.seqs * rows, 64 * Shape<FMT, D, false>::kWaves, st);
         return;
     }
     const int64_t units = decode_units_bound(a.seqs, a.kv_heads, a.head_tiles, a.max_len);
@@ -800,9 +817,12 @@ static void launch_decode(const DecodeArgs &a, hipStream_t st)
     const int grid = (int)(units < most ? units : most);
     hipLaunchKernelGGL((k_attn_decode<FMT, D, true>), dim3(grid), dim3(64 * S::kWaves), 0, st, a);
     // a wave a row where there are many (their parts are few), else four (2560 rows 6.6 -> 5.3 us)
-    const dim3 jg((unsigned)(a.seqs * a.heads));
-    if (a.seqs * a.heads > 1024) hipLaunchKernelGGL((k_attn_decode_join<D, 64>), jg, dim3(64), 0, st, a, grid);
-    else hipLaunchKernelGGL((k_attn_decode_join<D, 256>), jg, dim3(256), 0, st, a, grid);
+    const int64_t jrows = (int64_t)a.seqs * a.heads;
+    if (jrows > 1024)
+        launch_rows([](const DecodeArgs &x, dim3 g, dim3 t, hipStream_t s, int grid) {
+            hipLaunchKernelGGL((k_attn_decode_join<D, 64>), g, t, 0, s, x, grid);
+        }, a, jrows, 64, st, grid);
+    else hipLaunchKernelGGL((k_attn_decode_join<D, 256>), dim3((unsigned)jrows), dim3(256), 0, st, a, grid);
 }
 
 template <int FMT>

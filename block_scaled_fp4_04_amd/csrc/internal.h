@@ -193,6 +193,7 @@ struct DecodeArgs {
     float *part_o;   // [slot][part_heads][head_dim]
     float *part_ml;  // [slot][part_heads][2]
     int part_heads;
+    int first;       // first workgroup of this launch (set by the launcher)
 };
 
 // workgroups of the decode kernel, and an upper bound of its work units

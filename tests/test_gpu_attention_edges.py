@@ -267,3 +267,29 @@ def test_prompt_tile_order(dim, lens, heads, kv):
     assert -(-cus // kv) < tiles and (tiles * kv <= 2 * cus or lens == [8400])
     assert _fp4().lib().attn_prefill_workspace(sum(lens), heads, sum(lens), kv, dim, len(lens)) == 0
     _check_prompt(lens, lens, heads, kv, dim, seed=len(lens))
+
+
+def test_decode_more_rows_than_a_launch_holds():
+    """2^20 + 3 sequences of 8 heads: more workgroups of 512 threads than one launch may have."""
+    fp4 = _fp4()
+    n, heads, dim = (1 << 20) + 3, 8, 64
+    g = torch.Generator().manual_seed(0)
+    c = fp4.KVCache.alloc("bf16", 1, heads, 16, dim)
+    k, v = (_randn(g, 16, heads, dim).cuda() for _ in range(2))
+    fp4.kv_cache_append(c, k, v, torch.arange(16, device="cuda"))
+    q = _randn(g, 1, heads, dim).cuda()
+    some = torch.arange(17, dtype=torch.int32, device="cuda")
+    small = fp4.attn_decode_paged(q.expand(17, -1, -1), c, torch.zeros(17, 1, dtype=torch.int32, device="cuda"), some)
+    lens = torch.randint(0, 17, (n,), generator=g, dtype=torch.int32).cuda()
+    out = fp4.attn_decode_paged(q.expand(n, -1, -1), c, torch.zeros(n, 1, dtype=torch.int32, device="cuda"), lens)
+    assert torch.equal(out.view(n, -1), small.view(17, -1)[lens.long()])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "nvfp4"])
+def test_decode_many_sequences_of_wide_tables(fmt):
+    """A batch with more sequences than a quarter of its table's keys takes a workgroup a row, at any length."""
+    from test_gpu_attention import _check_decode
+
+    rng = np.random.default_rng(4)
+    lens = [int(x) for x in rng.integers(0, 30, 530)] + [1300, 0, 2047]
+    _check_decode(fmt, lens, 2, 1, 64, 16, seed=21)
