@@ -214,6 +214,7 @@ struct PrefillArgs {
     int64_t o_tok, o_head;
     float *lse;
     int fold_at, fold_most;  // order of the row tiles (set by the launcher)
+    int first;               // first workgroup of this launch (set by the launcher)
     int splits;      // most parts of a row tile's keys; 1: no partial results
     float *part_o;   // [row tile, key head][split][row][head_dim]
     float *part_ml;  // [row tile, key head][split][row][2]

@@ -293,3 +293,40 @@ def test_decode_many_sequences_of_wide_tables(fmt):
     rng = np.random.default_rng(4)
     lens = [int(x) for x in rng.integers(0, 30, 530)] + [1300, 0, 2047]
     _check_decode(fmt, lens, 2, 1, 64, 16, seed=21)
+
+
+@pytest.mark.parametrize("count", [256, 257, 4500])
+def test_prompt_sequences_by_search(count):
+    """Batches of many sequences find their row tiles by search: empty ones between, some of several tiles, at the end too."""
+    rng = np.random.default_rng(count)
+    lq = [int(x) for x in rng.integers(0, 4, count)]
+    for i in (0, 7, count // 2, count - 1):
+        lq[i] = 200 + i % 50
+    lk = [n + int(x) if n else 0 for n, x in zip(lq, rng.integers(0, 3, count))]
+    fp4 = _fp4()
+    g = torch.Generator(device="cuda").manual_seed(count)
+    heads, kv, dim = 6, 2, 64
+    q, k, v = (torch.randn(n, h, dim, device="cuda", generator=g).to(torch.bfloat16) for n, h in ((sum(lq), heads), (sum(lk), kv), (sum(lk), kv)))
+    lse = torch.empty(sum(lq), heads, device="cuda")
+    out = fp4.attn_prefill(q, k, v, _cu(lq), _cu(lk), dtype=torch.float32, lse=lse)
+    # the same sequences, 100 a call
+    oq, ok = np.cumsum([0] + lq), np.cumsum([0] + lk)
+    for b in range(0, count, 100):
+        e = min(b + 100, count)
+        some = torch.empty(int(oq[e] - oq[b]), heads, device="cuda")
+        part = fp4.attn_prefill(q[oq[b]:oq[e]], k[ok[b]:ok[e]], v[ok[b]:ok[e]], _cu(lq[b:e]), _cu(lk[b:e]), dtype=torch.float32, lse=some)
+        assert torch.equal(out[oq[b]:oq[e]], part) and torch.equal(lse[oq[b]:oq[e]], some), b
+    b = count // 2
+    _check_prompt(lq[b - 5:b + 5], lk[b - 5:b + 5], heads, kv, dim)
+
+
+def test_prompt_more_rows_than_a_launch_holds():
+    """2^20 + 5 sequences of 8 heads: more workgroups of 256 threads than one launch of this kernel takes."""
+    fp4 = _fp4()
+    n, heads, dim = (1 << 20) + 5, 8, 64
+    g = torch.Generator().manual_seed(1)
+    q, k, v = (_randn(g, 1, heads, dim).cuda().expand(n, -1, -1) for _ in range(3))
+    out = torch.full((n, heads, dim), 7.0, dtype=torch.bfloat16, device="cuda")
+    cu = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    fp4.attn_prefill(q, k, v, cu, cu, out=out)
+    assert torch.equal(out, v)
