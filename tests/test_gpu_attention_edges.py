@@ -330,3 +330,174 @@ def test_prompt_more_rows_than_a_launch_holds():
     cu = torch.arange(n + 1, dtype=torch.int32, device="cuda")
     fp4.attn_prefill(q, k, v, cu, cu, out=out)
     assert torch.equal(out, v)
+
+
+# ---- the split form of decode: rows shared by workgroups, and the launch that joins them
+
+def _split(lens, heads, kv, page, dim, slack=1):
+    """The workspace of a call as _check_decode makes it: rows are split only where it is not empty."""
+    fp4 = _fp4()
+    width = max(1, max((n + page - 1) // page for n in lens)) + slack
+    sizes = fp4._KvCacheArg(0, 1, kv, page, dim)
+    import ctypes
+
+    assert 4 * len(lens) < width * page  # (more sequences take a workgroup a row)
+    return fp4.lib().attn_decode_paged_workspace(len(lens), heads, ctypes.byref(sizes), width)
+
+
+def _check_split(fmt, lens, heads, kv, dim, page, **kw):
+    from test_gpu_attention import _check_decode
+
+    assert _split(lens, heads, kv, page, dim) > 0
+    return _check_decode(fmt, lens, heads, kv, dim, page, **kw)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8", "nvfp4", "mxfp4"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_decode_split_head_dims(fmt, dim):
+    _check_split(fmt, [1500, 0, 1, 2333], 4, 2, dim, 64, seed=dim)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "nvfp4"])
+@pytest.mark.parametrize("count,longest", [(65, 1100), (129, 1500), (200, 1300), (257, 2000)])
+def test_decode_split_many_sequences(fmt, count, longest):
+    """More sequences than lanes of a wave, ragged, empty ones among them, the longest first, last and in the middle."""
+    rng = np.random.default_rng(count)
+    lens = [int(x) for x in rng.integers(0, 90, count)]
+    for i in (0, 63, 64, count // 2, count - 1):
+        lens[i] = longest - i
+    _check_split(fmt, lens, 2, 1, 64, 16, seed=count)
+
+
+@pytest.mark.parametrize("count,heads,kv", [(3, 17, 1), (2, 40, 1), (66, 40, 2), (130, 16, 1), (70, 20, 4)])
+def test_decode_split_head_tiles(count, heads, kv):
+    """Several tiles of 16 heads on a key head; more than 1024 rows to join, and fewer."""
+    rng = np.random.default_rng(heads)
+    lens = [int(x) for x in rng.integers(0, 60, count)]
+    lens[count // 2], lens[-1] = 1777, 1025
+    _check_split("mxfp4", lens, heads, kv, 64, 32, seed=count)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8", "nvfp4", "mxfp4"])
+@pytest.mark.parametrize("window", [1000, 1100, 2999, 3001])
+def test_decode_split_window(fmt, window):
+    """Windows that start inside a tile of a row that several workgroups share (and one just under the split form)."""
+    _check_split(fmt, [5003, 1100, 0, 2, 3000], 2, 1, 64 if window < 2000 else 128, 64, window=window, seed=window)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "nvfp4"])
+@pytest.mark.parametrize("dim,window", [(64, 1024), (256, 1001), (128, 2069)])
+def test_decode_window_fills_the_chip(fmt, dim, window):
+    """Enough windowed rows take one workgroup each, though the table is wide."""
+    count = -(-torch.cuda.get_device_properties(0).multi_processor_count // 8)
+    rng = np.random.default_rng(dim)
+    lens = [int(x) for x in rng.integers(0, 200, count)]
+    lens[1], lens[2], lens[-1] = 2600, window + 1, window
+    _check_split(fmt, lens, 8, 8, dim, 64, window=window, seed=window)
+
+
+def test_decode_split_repeats_streams_graph():
+    """The split form gives the same bits on every call, on another stream, with a caller's workspace of any contents, and
+    from a captured graph whose lengths and queries change between replays."""
+    fp4 = _fp4()
+    from test_gpu_attention import _filled
+
+    lens = [2900, 5, 0, 1333]
+    c, table, _, _ = _filled(fp4, "nvfp4", lens, 2, 128, 16, 13)
+    for t in (c.k_codes, c.v_codes, c.k_scales, c.v_scales):  # unused bytes: numbers
+        t[t == 255] = 0x31
+    q = torch.randn(4, 8, 128, device="cuda").to(torch.bfloat16)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ws = fp4.attn_decode_paged_workspace(c, 4, 8, table.shape[1])
+    assert ws.numel() > 0
+    first = fp4.attn_decode_paged(q, c, table, n)
+    assert torch.equal(first, fp4.attn_decode_paged(q, c, table, n))
+    for fill in (0, 255):
+        ws.fill_(fill)
+        assert torch.equal(first, fp4.attn_decode_paged(q, c, table, n, workspace=ws))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = fp4.attn_decode_paged(q, c, table, n)
+    side.synchronize()
+    assert torch.equal(first, other)
+    out, lse = torch.empty_like(q), torch.empty(4, 8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fp4.attn_decode_paged(q, c, table, n, out=out, lse=lse, workspace=ws)
+    for step in range(4):
+        q.copy_(torch.randn(4, 8, 128, device="cuda").to(torch.bfloat16))
+        n.copy_(torch.tensor([2900 - 650 * step, 5 + step, step, 1333], dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        again = torch.empty_like(lse)
+        assert torch.equal(out, fp4.attn_decode_paged(q, c, table, n, lse=again)), step
+        assert torch.equal(lse, again), step
+
+
+def test_decode_split_parts_join_by_lse():
+    """Windowed and whole results of split rows agree through the logarithms of their sums."""
+    fp4 = _fp4()
+    from test_gpu_attention import _filled
+
+    c, table, k, v = _filled(fp4, "bf16", [3500], 1, 64, 16, 14)
+    assert fp4.attn_decode_paged_workspace(c, 1, 4, table.shape[1]).numel() > 0
+    q = torch.randn(1, 4, 64, device="cuda").to(torch.bfloat16)
+    lse = [torch.empty(1, 4, device="cuda") for _ in range(3)]
+    n = lambda x: torch.tensor([x], dtype=torch.int32, device="cuda")  # noqa: E731
+    whole = fp4.attn_decode_paged(q, c, table, n(3500), lse=lse[0], dtype=torch.float32)
+    head = fp4.attn_decode_paged(q, c, table, n(1377), lse=lse[1], dtype=torch.float32)
+    tail = fp4.attn_decode_paged(q, c, table, n(3500), window=3500 - 1377, lse=lse[2], dtype=torch.float32)
+    assert torch.allclose(torch.logaddexp(lse[1], lse[2]), lse[0], atol=2e-6)
+    w = [torch.exp(x - lse[0])[..., None] for x in lse[1:]]
+    assert float((w[0] * head + w[1] * tail - whole).abs().max()) < 3 * 2.0 ** -8 * float(v.abs().max())
+
+
+def test_decode_split_bad_ids_and_lengths_stay_inside():
+    """As the one-launch form: page ids outside the cache and lengths outside the table are clamped."""
+    fp4 = _fp4()
+    c = fp4.KVCache.alloc("bf16", 5, 1, 64, 64)
+    for t in (c.k_codes, c.v_codes):
+        t.fill_(1.0)
+    table = torch.randint(-(2 ** 31), 2 ** 31 - 1, (2, 40), dtype=torch.int64, device="cuda").to(torch.int32)
+    n = torch.tensor([10 ** 9, -3], dtype=torch.int32, device="cuda")
+    q = torch.ones(2, 1, 64, device="cuda", dtype=torch.bfloat16)
+    assert fp4.attn_decode_paged_workspace(c, 2, 1, 40).numel() > 0
+    out = fp4.attn_decode_paged(q, c, table, n)
+    assert bool((out[0] == 1).all()) and bool((out[1] == 0).all())
+
+
+def test_decode_split_values_that_are_not_numbers_where_masked():
+    """Keys and values behind the window and past the end may hold anything."""
+    fp4 = _fp4()
+    n, window, dim = 3001, 1203, 128
+    g = torch.Generator().manual_seed(3)
+    k, v = _randn(g, 3072, 1, dim), _randn(g, 3072, 1, dim)
+    c = fp4.KVCache.alloc("bf16", 48, 1, 64, dim)
+    table = torch.arange(48, dtype=torch.int32, device="cuda")[None]
+    assert fp4.attn_decode_paged_workspace(c, 1, 3, 48).numel() > 0
+    q = _randn(g, 1, 3, dim).cuda()
+    outs = []
+    for spoil in (False, True):
+        if spoil:
+            k[:n - window], v[:n - window] = float("nan"), float("inf")
+            k[n:], v[n:] = float("inf"), float("nan")
+        fp4.kv_cache_append(c, k.cuda(), v.cuda(), torch.arange(3072, device="cuda"))
+        outs.append(fp4.attn_decode_paged(q, c, table, torch.tensor([n], dtype=torch.int32, device="cuda"), window=window))
+    assert torch.equal(outs[0], outs[1]) and bool(outs[0].isfinite().all())
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "nvfp4"])
+def test_layer_with_long_context(fmt):
+    """The example layer with contexts whose decode step is split and captured with its workspace."""
+    import importlib.util
+    import os
+
+    import test_gpu_attention_layer as layer
+
+    spec = importlib.util.spec_from_file_location("attention_layer", os.path.join(layer.ROOT, "examples", "attention_layer.py"))
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    worst, _, y = m.run(fmt, prompts=(1300, 17), steps=4)
+    assert y.shape == (2, 1024) and bool(y.isfinite().all())
+    assert worst < layer.BOUND[fmt], (fmt, worst)
