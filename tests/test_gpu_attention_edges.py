@@ -501,3 +501,45 @@ def test_layer_with_long_context(fmt):
     worst, _, y = m.run(fmt, prompts=(1300, 17), steps=4)
     assert y.shape == (2, 1024) and bool(y.isfinite().all())
     assert worst < layer.BOUND[fmt], (fmt, worst)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4", "nvfp4"])
+def test_decode_every_scale_byte(fmt):
+    """One key a sequence and a query of zeros, so that its value is the output, bit for bit: every finite block scale, as
+    the cache is read back (below 2^-126 the 16-bit operands of the products may lose bits)."""
+    fp4 = _fp4()
+    dim, page = 64, 16
+    top = 0x7E if fmt == "nvfp4" else 254 if fmt == "mxfp4" else 245  # the largest with finite values
+    pages = -(-(top + 1) // page)
+    ts = [torch.tensor([0.75], device="cuda")] * 2 if fmt == "nvfp4" else [None] * 2
+    c = fp4.KVCache.alloc(fmt, pages, 1, page, dim, "cuda", *ts)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for t in (c.k_codes, c.v_codes):
+        t.copy_(torch.randint(0, 256, t.shape, device="cuda", generator=g, dtype=torch.uint8))
+        if fmt == "mxfp8":
+            t[(t & 127) == 127] = 0x7E
+    c.k_scales.fill_(0x38 if fmt == "nvfp4" else 120)
+    c.v_scales.copy_(torch.arange(pages * page, device="cuda").clamp(max=top).view(pages, 1, 1, page).expand_as(c.v_scales).to(torch.uint8))
+    n = top + 1
+    # every key is the last of a sequence of its own, behind a window of one
+    at = torch.arange(n, device="cuda")
+    table = torch.full((n, 1), -1, dtype=torch.int32, device="cuda")
+    table[:, 0] = (at // page).int()
+    q = torch.zeros(n, 1, dim, device="cuda", dtype=torch.bfloat16)
+    out = fp4.attn_decode_paged(q, c, table, (at % page + 1).int(), window=1, dtype=torch.float32)
+    _, v = fp4.kv_cache_read(c, torch.arange(pages, dtype=torch.int32, device="cuda")[None], _cu([n]), n, dtype=torch.float32)
+    wrong = (out[:, 0].double() - v[:, 0].double()).abs() > 2.0 ** -126
+    assert not bool(wrong.any()), (fmt, wrong.nonzero()[:4].tolist())
+
+
+def test_prompt_strides_past_4_gib():
+    """Keys and values whose rows lie 16 MiB apart: offsets within the buffer pass 2^32 bytes."""
+    fp4 = _fp4()
+    n, dim, step = 300, 64, 1 << 23
+    hold = torch.zeros(n * step, dtype=torch.bfloat16, device="cuda")
+    k = hold.as_strided((n, 2, dim), (step, dim, 1))
+    v = hold.as_strided((n, 2, dim), (step, dim, 1), 4 * dim)
+    q, a, b = (torch.randn(n, h, dim, device="cuda").to(torch.bfloat16) for h in (4, 2, 2))
+    k.copy_(a)
+    v.copy_(b)
+    assert torch.equal(fp4.attn_prefill(q, k, v, _cu([n]), _cu([n])), fp4.attn_prefill(q, a, b, _cu([n]), _cu([n])))
