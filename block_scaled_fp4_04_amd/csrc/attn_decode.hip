@@ -770,7 +770,9 @@ int64_t decode_units_bound(int64_t seqs, int64_t kv_heads, int64_t head_tiles, i
 }
 
 // Whether rows are split among workgroups: not when a row's longest context is a few
-// passes of one workgroup, whose latency is below that of a second launch.
+// passes of one workgroup, whose latency is below that of a second launch (one launch / split: 8 bf16 rows of
+// 600 keys 9.8 / 13.6 us, 1000 13.2 / 13.5, 1900 20.8 / 13.3; 128 NVFP4 rows of 600 9.5 / 13.5, 1000 10.9 / 15.3,
+// 1900 14.9 / 17.4).
 static bool decode_splits(int64_t max_len) { return max_len > 1024; }
 
 // Workgroups of a split launch: as many as the device holds at once.
@@ -800,7 +802,8 @@ static void launch_decode(const DecodeArgs &a, hipStream_t st)
     using S = Shape<FMT, D, true>;
     const int rows = a.kv_heads * a.head_tiles;
     // a window bounds every row alike: where the rows fill the chip, one launch serves it as well
-    // (129 sequences, window 1024, head_dim 256: 28.0 -> 21.5 us; window 4096 loses on ragged batches)
+    // (129 sequences, window 1024, head_dim 256: 28.0 -> 21.5 us; 64 of 8000 keys, window 2000: 33.5 -> 26.3 us;
+    // window 4096: 57.7 -> 50.7 us, but on a ragged batch of 128 46.5 -> 57.0 us)
     const int64_t reach = a.window > 0 && a.window + 31 < a.max_len ? a.window + 31 : a.max_len;
     // every workgroup of the two launches adds up all lengths, which with this many sequences costs more than
     // the longest row can gain (sequences, keys of the table: 512, 2048: 48.4 -> 43.8 us; 4096, 2048: 381 -> 242;
@@ -816,7 +819,8 @@ static void launch_decode(const DecodeArgs &a, hipStream_t st)
     const int64_t most = S::kPerCu * (int64_t)device_cu_count();
     const int grid = (int)(units < most ? units : most);
     hipLaunchKernelGGL((k_attn_decode<FMT, D, true>), dim3(grid), dim3(64 * S::kWaves), 0, st, a);
-    // a wave a row where there are many (their parts are few), else four (2560 rows 6.6 -> 5.3 us)
+    // a wave a row where there are many (their parts are few), else four (whole calls, four waves / one: 2560 rows
+    // 47.7 / 45.6 us, 2048 25.8 / 23.4, 1280 45.4 / 45.6, 256 16.3 / 17.2, 96 long ones 45.8 / 49.0)
     const int64_t jrows = (int64_t)a.seqs * a.heads;
     if (jrows > 1024)
         launch_rows([](const DecodeArgs &x, dim3 g, dim3 t, hipStream_t s, int grid) {

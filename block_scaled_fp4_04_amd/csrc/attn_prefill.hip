@@ -85,7 +85,7 @@ __device__ __forceinline__ QTile find_slot(const PrefillArgs &a, int x)
 // keys.  (The longest sequence first as well gained nothing measurable and costs a pass
 // over the lanes.)  Where the chip holds all workgroups at once, two a CU, the second half
 // comes in reverse: the CUs that got the longest tiles first get the shortest ones as
-// their second (2048 tokens, 32/8 heads of 128: 46.5 -> 45.3 us; two prompts of 1000: 33.6 -> 27.7 us).
+// their second (2048 tokens, 32/8 heads of 128: 48.4 -> 47.5 us; two prompts of 1000: 34.3 -> 28.9 us).
 __device__ __forceinline__ QTile find_tile(const PrefillArgs &a, int x)
 {
     if (a.seqs > kManySeqs) return find_slot(a, x);

@@ -701,10 +701,10 @@ __device__ __forceinline__ KvTile kv_tile(const KvArgs &a, uint32_t tile_tokens)
     return k;
 }
 
-// One row a lane group: with two or four in flight the call got slower (11829 tokens of 8 heads
-// of 128, one / two / four: bf16 16.7 / 26.7 / 28.0 us, NVFP4 14.0 / 15.6 / 16.9 us; 62 to 97 MB,
-// 4.4 to 5.8 TB/s), as the chip is full of waves either way and the writes then come in
-// longer strides.
+// One row a lane group: with four in flight most calls got slower (8 heads of 128, one / four: 11829 tokens
+// bf16 15.1 / 23.9 us, MXFP8 15.2 / 17.7, NVFP4 16.2 / 17.4, MXFP4 12.6 / 14.5; 60000 tokens 81.8 / 96.1,
+// 72.5 / 76.0, 72.0 / 68.1, 59.9 / 61.3: 5 to 6 TB/s), as the chip is full of waves either way and the
+// writes then come in longer strides.
 template <int FMT, typename T>
 __global__ __launch_bounds__(256) void k_kv_append(KvArgs a, int lane_shift)
 {
@@ -714,8 +714,8 @@ __global__ __launch_bounds__(256) void k_kv_append(KvArgs a, int lane_shift)
     const T *xp = reinterpret_cast<const T *>(tile.side ? a.x[1] : a.x[0]) + t * (tile.side ? a.tok[1] : a.tok[0]) +
                   tile.head * (tile.side ? a.head[1] : a.head[0]) + c8 * 8;
     uint8_t *codes = tile.side ? a.codes[1] : a.codes[0], *scales = tile.side ? a.scales[1] : a.scales[0];
-    // the row is requested together with its slot, not after it (a return between the two let the
-    // compiler wait for the slot first: 60000 MXFP8 tokens 70 -> 88 us)
+    // the row is requested together with its slot, not after it (a return between the two lets the
+    // compiler wait for the slot first: 60000 MXFP8 tokens 72 -> 88 us)
     int64_t slot = -1;
     float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     uint4 raw = make_uint4(0, 0, 0, 0);
@@ -868,9 +868,10 @@ __global__ __launch_bounds__(256) void k_kv_read(KvArgs a, int lane_shift)
         if constexpr (OUT_BF16) {
             if constexpr (FMT != FP4_KV_BF16)
                 raw[i] = make_uint4(bf16x2_rne(o[0], o[1]), bf16x2_rne(o[2], o[3]), bf16x2_rne(o[4], o[5]), bf16x2_rne(o[6], o[7]));
-            // ordinary stores: streaming ones made this kernel 10% faster alone, and the attention that reads
-            // its output next up to 25% slower (16384 tokens: read 17.5 -> 16.0 us, with the attention of 128
-            // queries 433 -> 530 us), because the rows then come from HBM
+            // ordinary stores: streaming ones make this kernel up to 30% faster alone, and the attention that reads
+            // its output next up to 20% slower, because the rows then come from HBM (MXFP8, this kernel and with
+            // the attention of 1024 queries: 16384 tokens 16.7 -> 15.7 us, 283 -> 339 us; 60000 tokens 73.7 ->
+            // 54.0 us, 1172 -> 1231 us; with 128 queries 71.7 -> 71.3 and 210 -> 205 us)
             *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(out) + at) = raw[i];
         } else {
             float *yp = reinterpret_cast<float *>(out) + at;
@@ -1072,8 +1073,8 @@ static void launch_read_u(const KvArgs &a, hipStream_t st)
 template <int FMT>
 static void launch_read_fmt(const KvArgs &a, fp4_dtype yt, hipStream_t st)
 {
-    // four passes a workgroup (their loads in flight together: 59833 NVFP4 tokens of 8 heads of 128 in
-    // 79 us, two passes 95 us) when that still leaves two workgroups a CU, else one, so that a small
+    // four passes a workgroup (their loads in flight together: 59833 NVFP4 tokens of 8 heads of 128, with
+    // an append of 4, in 85 us, two passes 104 us) when that still leaves two workgroups a CU, else one, so that a small
     // call spreads over the chip
     const int64_t pass = 256 >> kv_lane_shift(a);
     const bool four = (a.tokens + 4 * pass - 1) / (4 * pass) * 2 * a.kv_heads >= 2 * device_cu_count();

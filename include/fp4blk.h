@@ -516,13 +516,14 @@ size_t attn_decode_paged_workspace(int64_t seqs, int64_t heads, const fp4_kv_cac
  *         to [0, table_width * page_size].  Length 0 gives a zero row and lse = -inf.
  *         Page ids are clamped into the cache: a bad id gives wrong values, no access
  *         outside the buffers.
- *  scale  in [0, 1e30] (FP4_ERR_SHAPE otherwise).
+ *  scale  in [0, 1e30] (FP4_ERR_SHAPE otherwise); scores past the fp32 range give
+ *         unspecified results.
  *  out    [seqs][heads][head_dim] fp32 or bf16 (ot).
  *  lse    optional fp32 [seqs][heads]: log sum_j exp(scale q.k_j), natural logarithm,
  *         with which results over parts of a context can be joined.
  *  ws     attn_decode_paged_workspace() bytes, 16-byte aligned.
  * Scores, softmax sums and output sums are fp32; the softmax weights are rounded to 16
- * bits (bf16; f16 for NVFP4) as operands of the matrix core.  Nothing outside a
+ * bits (bf16; f16, raised by 2^7, for NVFP4) as operands of the matrix core.  Nothing outside a
  * sequence's range is ever used, whatever it holds.  The same inputs give the same
  * bits.  seqs * kv_heads * (table_width * page_size / 128) < 2^31 (FP4_ERR_SHAPE). */
 fp4_status attn_decode_paged(const void *q, int64_t seqs, int64_t heads, int64_t q_seq_stride,
