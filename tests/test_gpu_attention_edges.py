@@ -543,3 +543,24 @@ def test_prompt_strides_past_4_gib():
     k.copy_(a)
     v.copy_(b)
     assert torch.equal(fp4.attn_prefill(q, k, v, _cu([n]), _cu([n])), fp4.attn_prefill(q, a, b, _cu([n]), _cu([n])))
+
+
+@pytest.mark.parametrize("empty", [3, 8, 9, 70, 30000])
+def test_read_between_empty_sequences(empty):
+    """Runs of empty sequences between the tokens of one tile, before the first and after the last."""
+    fp4 = _fp4()
+    lens = [0] * empty + [5] + [0] * empty + [1, 2] + [0] * empty + [40] + [0] * empty
+    used = [i for i, n in enumerate(lens) if n]
+    c = fp4.KVCache.alloc("bf16", 6, 2, 16, 64)
+    table = torch.full((len(lens), 3), -1, dtype=torch.int32)
+    pages, slots = iter(range(6)), []
+    for i in used:
+        for j in range((lens[i] + 15) // 16):
+            table[i, j] = next(pages)
+        slots += [int(table[i, p // 16]) * 16 + p % 16 for p in range(lens[i])]
+    n = sum(lens)
+    k, v = (torch.randn(n, 2, 64, device="cuda").to(torch.bfloat16) for _ in range(2))
+    fp4.kv_cache_append(c, k, v, torch.tensor(slots, dtype=torch.int64, device="cuda"))
+    kr, vr = fp4.kv_cache_read(c, table.cuda(), _cu(lens), n + 3)
+    assert torch.equal(kr[:n], k) and torch.equal(vr[:n], v)
+    assert not bool(kr[n:].any()) and not bool(vr[n:].any())
