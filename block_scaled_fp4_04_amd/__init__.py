@@ -99,6 +99,18 @@ def _declare(L):
         "attn_prefill": (i32, [p, i64, i64, i64, i64, p, p, i64, i64, i64, i64, i64, i64, i64, p, p, i64, f32, i32,
                                i64, p, i32, i64, i64, p, p, sz, p]),
         "attn_prefill_workspace": (sz, [i64, i64, i64, i64, i64, i64]),
+        "qk_norm_rope": (i32, [p, p, i32, i64, i64, i64, i64, i64, i64, i64, i64, p, p, i64, i64, f32, p, p, i64, i32, p,
+                               p, i32, i64, i64, i64, i64, p]),
+        "qk_norm_rope_append": (i32, [p, p, p, p, i32, i64, i64, i64, i64, i64, i64, i64, i64, p, p, i64, i64, f32, p, p,
+                                      i64, i32, p, i32, p, p, i32, i64, i64, p]),
+        "kv_pages_extend_workspace": (sz, [i64, i64]),
+        "kv_pages_extend": (i32, [p, p, i64, i64, i64, p, p, i64, p, p, p, p, p, p, p, sz, p]),
+        "kv_pages_collect_workspace": (sz, [i64, i64, i64]),
+        "kv_pages_collect": (i32, [p, p, i64, i64, i64, p, p, sz, p]),
+        "kv_pages_reorder": (i32, [p, i64, i64, i64, i64, p, p, i64, p, i64, p, p]),
+        "kv_cache_copy": (i32, [p, p, i64, p]),
+        "beam_select_workspace": (sz, [i64, i64, i64, i64, i32]),
+        "beam_select": (i32, [p, i32, i64, i64, i64, i64, p, p, i64, i64, p, p, p, p, sz, p]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -1244,4 +1256,322 @@ def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q
     _run(lib().attn_prefill, _ptr(q), n, h, qt, qh, _ptr(k), _ptr(v), nk, hk, d, kt, kh, vt, vh, _ptr(cu_seqlens_q),
          _ptr(cu_seqlens_k), seqs, d ** -0.5 if scale is None else scale, int(bool(causal)), window, _ptr(out),
          _dt(out), ot, oh, _ptr(lse), _ptr(workspace), need, _stream())
+    return out
+
+
+# ------------------------------------------------- around the attention ---
+
+def rope_frequencies(rot: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """The usual angles per position, base ** (-2 i / rot): float64 [rot / 2], made once."""
+    return float(base) ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / max(rot, 1))
+
+
+def _head_weight(w, heads: int, dim: int, what: str) -> int:
+    """The head stride of a norm's weight: float32 [dim] (0) or [heads, dim]."""
+    if w.dtype != torch.float32:
+        raise TypeError(f"{what} must be float32, got {w.dtype}")
+    if not w.is_contiguous() or (tuple(w.shape) != (dim,) and tuple(w.shape) != (heads, dim)):
+        raise ValueError(f"{what} must be a contiguous [{dim}] or [{heads}, {dim}], got {tuple(w.shape)}")
+    return 0 if w.dim() == 1 else dim
+
+
+def _norm_args(n, q_heads, k_heads, d, positions, freqs, q_weight, k_weight, eps):
+    """(q weight's and k weight's head strides, eps, rot): the checks that both forms of the norm share."""
+    qs = ks = 0
+    if eps is None:
+        if q_weight is not None or k_weight is not None:
+            raise ValueError("weights belong to a norm: give eps")
+    else:
+        if not eps > 0:
+            raise ValueError(f"eps must be positive (None: no norm), got {eps}")
+        if q_weight is None or (k_weight is None and k_heads > 0):
+            raise ValueError("a norm needs its weights (ones for none)")
+        qs = _head_weight(q_weight, q_heads, d, "q_weight")
+        if k_heads > 0:
+            ks = _head_weight(k_weight, k_heads, d, "k_weight")
+    rot = 0
+    if freqs is not None:
+        if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
+            raise TypeError("freqs must be a contiguous float64 vector [rot / 2]")
+        rot = 2 * freqs.shape[0]
+        if rot % 16 or rot > d:
+            raise ValueError(f"freqs turn {rot} values: a multiple of 16 up to head_dim {d} is needed")
+    if rot:
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+        _i32_vec(positions, n, "positions")
+    return qs, ks, 0.0 if eps is None else eps, rot
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor | None, freqs: torch.Tensor | None,
+                 q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float | None = None,
+                 interleaved: bool = False, dtype=torch.bfloat16, q_out: torch.Tensor | None = None,
+                 k_out: torch.Tensor | None = None):
+    """Every head's row of q [tokens, heads, head_dim] and k [tokens, kv_heads, head_dim] (fp32 or
+    bf16, any token and head strides; k may be None) normed by its root mean square (eps None: not)
+    with weights float32 [head_dim] or [heads, head_dim], and its first 2 * len(freqs) values
+    rotated by positions (int32 [tokens]) times freqs (float64, `rope_frequencies`; None: not):
+    value i with i + rot / 2, or neighbours when `interleaved`.  q_out and k_out may be q and k.
+    Returns (q_out, k_out)."""
+    n, h, d, qt, qh = _heads(q, _F32_BF16, "q")
+    hk = kt = kh = kot = koh = 0
+    if k is not None:
+        nk, hk, dk, kt, kh = _heads(k, _F32_BF16, "k")
+        if nk != n or dk != d or k.dtype != q.dtype:
+            raise ValueError(f"q is {tuple(q.shape)} {q.dtype}, k {tuple(k.shape)} {k.dtype}")
+        if hk == 0:
+            raise ValueError("k has no heads (None for no k)")
+    elif k_weight is not None or k_out is not None:
+        raise ValueError("k_weight and k_out belong to a k")
+    qs, ks, eps, rot = _norm_args(n, h, hk, d, positions, freqs, q_weight, k_weight, eps)
+    q_out, qot, qoh = _out_heads(q_out, n, h, d, dtype, q, "q_out")
+    if k is not None:
+        k_out, kot, koh = _out_heads(k_out, n, hk, d, q_out.dtype, k, "k_out")
+        if k_out.dtype != q_out.dtype:
+            raise TypeError("q_out and k_out must have the same dtype")
+    _need_cuda(q, k, positions if rot else None, freqs, q_weight, k_weight, q_out, k_out)
+    _run(lib().qk_norm_rope, _ptr(q), _ptr(k), _dt(q), n, h, hk, d, qt, qh, kt, kh, _ptr(q_weight), _ptr(k_weight), qs, ks,
+         eps, _ptr(positions) if rot else None, _ptr(freqs), rot, int(bool(interleaved)), _ptr(q_out), _ptr(k_out),
+         _dt(q_out), qot, qoh, kot, koh, _stream())
+    return q_out, k_out
+
+
+def qk_norm_rope_append(cache: KVCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                        positions: torch.Tensor | None, slots: torch.Tensor, freqs: torch.Tensor | None,
+                        q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                        eps: float | None = None, interleaved: bool = False, rule="ocp",
+                        nonfinite: torch.Tensor | None = None, dtype=torch.bfloat16,
+                        q_out: torch.Tensor | None = None) -> torch.Tensor:
+    """qk_norm_rope with the keys, and v as it is, quantized into the cache at `slots` as
+    kv_cache_append does (the keys from fp32, not from rows rounded before).  Returns q_out."""
+    n, h, d, qt, qh = _heads(q, _F32_BF16, "q")
+    nk, hk, dk, kt, kh = _heads(k, _F32_BF16, "k")
+    nv, hv, dv, vt, vh = _heads(v, _F32_BF16, "v")
+    if nk != n or nv != n or dk != d or dv != d or hv != hk or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k and v must agree in tokens, head_dim and dtype, k and v in heads")
+    if hk != cache.kv_heads or d != cache.head_dim:
+        raise ValueError(f"k has {hk} heads of {d}, the cache {cache.kv_heads} of {cache.head_dim}")
+    qs, ks, eps, rot = _norm_args(n, h, hk, d, positions, freqs, q_weight, k_weight, eps)
+    if slots.dtype != torch.int64 or slots.dim() != 1 or slots.shape[0] != n or not slots.is_contiguous():
+        raise ValueError(f"slots must be a contiguous int64 tensor of {n} element(s)")
+    if nonfinite is not None and (nonfinite.dtype != torch.int32 or nonfinite.numel() < 1):
+        raise ValueError("nonfinite must be an int32 tensor of at least one element")
+    q_out, qot, qoh = _out_heads(q_out, n, h, d, dtype, q, "q_out")
+    _need_cuda(cache.k_codes, q, k, v, positions if rot else None, freqs, slots, q_weight, k_weight, nonfinite, q_out)
+    _run(lib().qk_norm_rope_append, _kv(cache), _ptr(q), _ptr(k), _ptr(v), _dt(q), n, h, qt, qh, kt, kh, vt, vh,
+         _ptr(q_weight), _ptr(k_weight), qs, ks, eps, _ptr(positions) if rot else None, _ptr(freqs), rot,
+         int(bool(interleaved)), _ptr(slots), _rule(rule), _ptr(nonfinite), _ptr(q_out), _dt(q_out), qot, qoh, _stream())
+    return q_out
+
+
+class _KvPagesArg(ctypes.Structure):
+    """fp4_kv_pages"""
+    _fields_ = [("free_list", ctypes.c_void_p), ("state", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int64)]
+
+
+class KVPages:
+    """The free pages of a cache (of all layers' caches, which share block tables).
+
+    free   int32 [pages]: the first state[0] entries are free page ids, dealt from the end
+    state  int32 [2]: the number of free pages, and of sequences refused so far
+
+    `alloc` makes a pool in which every page is free."""
+
+    def __init__(self, free: torch.Tensor, state: torch.Tensor, page_size: int):
+        if page_size < 16 or page_size > 256 or page_size & (page_size - 1):
+            raise ValueError(f"page_size must be a power of two in [16, 256], got {page_size}")
+        if free.dim() != 1 or free.shape[0] == 0:
+            raise ValueError("free must be [pages]")
+        _i32_vec(free, free.shape[0], "free")
+        _i32_vec(state, 2, "state")
+        _need_cuda(free, state)
+        self.free, self.state, self.pages, self.page_size, self.device = free, state, free.shape[0], page_size, free.device
+        self._arg = _KvPagesArg(free.data_ptr(), state.data_ptr(), self.pages, page_size)
+        self._ref = ctypes.byref(self._arg)
+
+    @classmethod
+    def alloc(cls, pages: int, page_size: int, device="cuda") -> "KVPages":
+        return cls(torch.arange(pages - 1, -1, -1, dtype=torch.int32, device=device),
+                   torch.tensor([pages, 0], dtype=torch.int32, device=device), page_size)
+
+
+def _pool(pages: KVPages):
+    if _recording is not None:
+        _recording_keep.append(pages)
+    return pages._ref
+
+
+@dataclasses.dataclass
+class KVPlan:
+    """Where the new tokens of kv_pages_extend go: slots int64 and positions int32 [tokens], the
+    offsets cu_q (new tokens) and cu_k (whole contexts) int32 [sequences + 1] (None: not asked
+    for), and the lengths and the pool's state after."""
+    slots: torch.Tensor
+    positions: torch.Tensor
+    cu_q: torch.Tensor | None
+    cu_k: torch.Tensor | None
+    seq_lens: torch.Tensor
+    state: torch.Tensor
+
+
+def kv_pages_extend_workspace(seqs: int, tokens: int, device="cuda") -> torch.Tensor:
+    return torch.empty(lib().kv_pages_extend_workspace(seqs, tokens), dtype=torch.uint8, device=device)
+
+
+def kv_pages_extend(pages: KVPages, block_table: torch.Tensor, seq_lens: torch.Tensor, new_lens: torch.Tensor,
+                    tokens: int, in_place: bool = True, offsets: bool = True, out: KVPlan | None = None,
+                    workspace: torch.Tensor | None = None) -> KVPlan:
+    """Room for new_lens[b] more tokens (int32) behind the seq_lens[b] that sequence b holds: pages are
+    dealt from the pool, block_table int32 [sequences, pages] is extended, and the slot and position of every
+    new token are listed, packed one sequence behind the other.  tokens = sum(new_lens), or more (known to the
+    caller, so that nothing waits for the device).  in_place: seq_lens and the pool's state become
+    those after the call; else the plan holds new ones.  A sequence that cannot be served whole is
+    left as it is: its slots are -1 and state[1] counts it.  `out`: a plan of the same sizes to write into."""
+    seqs, width, stride = _block_table(block_table)
+    _i32_vec(seq_lens, seqs, "seq_lens")
+    _i32_vec(new_lens, seqs, "new_lens")
+    tokens = int(tokens)
+    if out is None:
+        if tokens < 0:
+            raise ValueError(f"tokens must not be negative, got {tokens}")
+        dev = block_table.device
+        cu = torch.empty((2, seqs + 1), dtype=torch.int32, device=dev).unbind(0) if offsets else (None, None)
+        out = KVPlan(torch.empty(tokens, dtype=torch.int64, device=dev), torch.empty(tokens, dtype=torch.int32, device=dev), *cu,
+                     seq_lens if in_place else torch.empty_like(seq_lens),
+                     pages.state if in_place else torch.empty_like(pages.state))
+    else:
+        if out.slots.dtype != torch.int64 or out.slots.shape != (tokens,) or not out.slots.is_contiguous():
+            raise ValueError(f"out.slots must be a contiguous int64 tensor of {tokens} element(s)")
+        _i32_vec(out.positions, tokens, "out.positions")
+        for x, name in ((out.cu_q, "out.cu_q"), (out.cu_k, "out.cu_k")):
+            if x is not None:
+                _i32_vec(x, seqs + 1, name)
+        _i32_vec(out.seq_lens, seqs, "out.seq_lens")
+        _i32_vec(out.state, 2, "out.state")
+    need = lib().kv_pages_extend_workspace(seqs, tokens)
+    if need or workspace is not None:
+        workspace = _workspace(workspace, need, block_table)
+    _need_cuda(pages.free, block_table, seq_lens, new_lens, out.slots, out.positions, out.cu_q, out.cu_k, out.seq_lens,
+               out.state, workspace)
+    _run(lib().kv_pages_extend, _pool(pages), _ptr(block_table), seqs, width, stride, _ptr(seq_lens), _ptr(new_lens),
+         tokens, _ptr(out.seq_lens), _ptr(out.state), _ptr(out.slots), _ptr(out.positions), _ptr(out.cu_q),
+         _ptr(out.cu_k), _ptr(workspace), need, _stream())
+    return out
+
+
+def kv_pages_collect_workspace(pages: KVPages, seqs: int, table_width: int) -> torch.Tensor:
+    return torch.empty(lib().kv_pages_collect_workspace(pages.pages, seqs, table_width), dtype=torch.uint8,
+                       device=pages.device)
+
+
+def kv_pages_collect(pages: KVPages, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                     workspace: torch.Tensor | None = None) -> KVPages:
+    """The pool's free list anew: every page that no row of the block table holds within its
+    length, in ascending order.  A sequence that ended gives its pages back by a length of 0."""
+    seqs, width, stride = _block_table(block_table)
+    _i32_vec(seq_lens, seqs, "seq_lens")
+    need = lib().kv_pages_collect_workspace(pages.pages, seqs, width)
+    if need or workspace is not None:
+        workspace = _workspace(workspace, need, block_table)
+    _need_cuda(pages.free, block_table, seq_lens, workspace)
+    _run(lib().kv_pages_collect, _pool(pages), _ptr(block_table), seqs, width, stride, _ptr(seq_lens), _ptr(workspace),
+         need, _stream())
+    return pages
+
+
+def kv_pages_reorder(block_table: torch.Tensor, seq_lens: torch.Tensor, parents: torch.Tensor, page_size: int,
+                     out: torch.Tensor | None = None, copies: torch.Tensor | None = None) -> torch.Tensor:
+    """Block-table rows of beams after a selection: parents int32 [batch, beams] (beam_select's), row
+    j of a group takes the row of beam parents[j], in place or into `out`.  The rows of a group have
+    the same length.  Returns int32 [batch * beams, 3]: what kv_cache_copy has to copy in every layer's cache,
+    because a partly filled page belongs to one row only."""
+    seqs, width, stride = _block_table(block_table)
+    if parents.dtype != torch.int32:
+        raise TypeError(f"parents must be int32, got {parents.dtype}")
+    if parents.dim() != 2 or not parents.is_contiguous() or parents.numel() != seqs:
+        raise ValueError(f"parents must be a contiguous [batch, beams] of {seqs} rows, got {tuple(parents.shape)}")
+    batch, beams = parents.shape
+    _i32_vec(seq_lens, seqs, "seq_lens")
+    ostride = stride
+    if out is None:
+        out = block_table
+    elif out is not block_table:
+        oseqs, owidth, ostride = _block_table(out, "out")
+        if (oseqs, owidth) != (seqs, width):
+            raise ValueError(f"out has shape {tuple(out.shape)}, expected {(seqs, width)}")
+    if copies is None:
+        copies = torch.empty((seqs, 3), dtype=torch.int32, device=block_table.device)
+    else:
+        _copies(copies)
+        _shape(copies, (seqs, 3), "copies")
+    _need_cuda(block_table, seq_lens, parents, out, copies)
+    _run(lib().kv_pages_reorder, _ptr(block_table), batch, beams, width, stride, _ptr(seq_lens), _ptr(parents),
+         page_size, _ptr(out), ostride, _ptr(copies), _stream())
+    return copies
+
+
+def _copies(t: torch.Tensor):
+    if t.dtype != torch.int32:
+        raise TypeError(f"copies must be int32, got {t.dtype}")
+    if t.dim() != 2 or t.shape[1] != 3 or not t.is_contiguous():
+        raise ValueError(f"copies must be a contiguous [n, 3], got {tuple(t.shape)}")
+
+
+def kv_cache_copy(cache: KVCache, copies: torch.Tensor) -> KVCache:
+    """For each row (source page, destination page, tokens) of copies int32 [n, 3] the first `tokens`
+    tokens of the source page are copied into the destination page (all heads, keys and values); rows
+    with a negative page are skipped."""
+    _copies(copies)
+    _need_cuda(cache.k_codes, copies)
+    _run(lib().kv_cache_copy, _kv(cache), _ptr(copies), copies.shape[0], _stream())
+    return cache
+
+
+def beam_select_workspace(batch: int, beams: int, vocab: int, k: int, dtype=torch.bfloat16, device="cuda") -> torch.Tensor:
+    return torch.empty(lib().beam_select_workspace(batch, beams, vocab, k, _out_dt(dtype)), dtype=torch.uint8, device=device)
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: int | None = None, done: torch.Tensor | None = None,
+                end_token: int = 0, out=None, workspace: torch.Tensor | None = None):
+    """The k (default: beams) best continuations of every group of beams: logits [batch * beams, vocab] fp32 or
+    bf16, scores float32 [batch, beams] (the beams' log probabilities so far; -inf: the beam offers
+    nothing), done bool or uint8 [batch, beams] (the beam has ended and offers end_token at its own
+    score).  Returns (scores float32, parents int32, tokens int32), each [batch, k], best first, ties to the lowest
+    beam, then token.  Places that are left: -inf, min(place, beams - 1), -1."""
+    dt = _dt(logits)
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [batch * beams, vocab], got {tuple(logits.shape)}")
+    if scores.dtype != torch.float32:
+        raise TypeError(f"scores must be float32, got {scores.dtype}")
+    if scores.dim() != 2 or not scores.is_contiguous():
+        raise ValueError(f"scores must be a contiguous [batch, beams], got {tuple(scores.shape)}")
+    batch, beams = scores.shape
+    rows, vocab = logits.shape
+    if rows != batch * beams:
+        raise ValueError(f"logits have {rows} rows, scores {batch} x {beams}")
+    ld = _ld(logits)
+    if done is not None:
+        if done.dtype not in (torch.bool, torch.uint8):
+            raise TypeError(f"done must be bool or uint8, got {done.dtype}")
+        _shape(done, (batch, beams), "done")
+        if not done.is_contiguous():
+            raise ValueError("done must be contiguous")
+    k = beams if k is None else k
+    need = lib().beam_select_workspace(batch, beams, vocab, k, dt)
+    workspace = _workspace(workspace, need, logits)
+    if out is None:
+        if not 1 <= k <= 64:
+            raise ValueError(f"k must be in [1, 64], got {k}")
+        dev = logits.device
+        out = (torch.empty((batch, k), dtype=torch.float32, device=dev), torch.empty((batch, k), dtype=torch.int32, device=dev),
+               torch.empty((batch, k), dtype=torch.int32, device=dev))
+    else:
+        for t, d, name in zip(out, (torch.float32, torch.int32, torch.int32), ("scores", "parents", "tokens"), strict=True):
+            if t.dtype != d or not t.is_contiguous():
+                raise TypeError(f"out's {name} must be contiguous {d}")
+            _shape(t, (batch, k), f"out's {name}")
+    _need_cuda(logits, scores, done, workspace, *out)
+    _run(lib().beam_select, _ptr(logits), dt, batch, beams, vocab, ld, _ptr(scores), _ptr(done), end_token, k,
+         _ptr(out[0]), _ptr(out[1]), _ptr(out[2]), _ptr(workspace), need, _stream())
     return out

@@ -17,8 +17,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libfp4blk.so")
 SOURCES = ["abi.hip", "quant.hip", "gemm_nv.hip", "gemv_nv.hip", "gemm_mx.hip", "attn_decode.hip",
-           "attn_prefill.hip", "measure.hip"]
-HEADERS = ["device_common.h", "internal.h"]
+           "attn_prefill.hip", "head_norm.hip", "pages.hip", "beam.hip", "measure.hip"]
+HEADERS = ["device_common.h", "quant_device.h", "internal.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -1211,3 +1211,331 @@ fp4_status attn_prefill(const void *q, int64_t q_tokens, int64_t heads, int64_t 
 }
 
 }  // extern "C"
+
+// ------------------------------------------- around the attention --
+
+namespace {
+
+struct Strides {
+    int64_t tok, head;
+};
+
+// what qk_norm_rope and qk_norm_rope_append share: the numbers first, then the pointers
+fp4_status check_norm(fp4_dtype xt, fp4_dtype yt, int64_t tokens, int64_t heads, int64_t kv_heads, int64_t dim, float eps,
+                      int64_t rot, int interleaved)
+{
+    if (!valid_dtype(xt) || !valid_dtype(yt) || (interleaved != 0 && interleaved != 1)) return FP4_ERR_DTYPE;
+    if (tokens < 0 || tokens >= k2GiB || heads <= 0 || heads > 65535 || kv_heads < 0 || kv_heads > 65535) return FP4_ERR_SHAPE;
+    if (dim <= 0 || dim > 512 || dim % 8 != 0 || rot < 0 || rot > dim || rot % 16 != 0) return FP4_ERR_SHAPE;
+    if (!(eps == 0.0f || (eps >= 1.0e-30f && eps <= 1.0e30f))) return FP4_ERR_SHAPE;
+    return FP4_OK;
+}
+
+fp4_status check_weight(const float *w, int64_t stride)
+{
+    if (!w) return FP4_ERR_NULL;
+    if (stride < 0 || stride % 4 != 0 || !aligned16(w)) return FP4_ERR_LAYOUT;
+    return FP4_OK;
+}
+
+fp4_status check_angles(const int32_t *positions, const double *freqs, int64_t rot)
+{
+    if (rot == 0) return FP4_OK;
+    if (!positions || !freqs) return FP4_ERR_NULL;
+    return (reinterpret_cast<uintptr_t>(freqs) & 7u) == 0 ? FP4_OK : FP4_ERR_LAYOUT;
+}
+
+HeadNormArgs norm_args(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t dim, const float *qw, const float *kw,
+                       int64_t qws, int64_t kws, float eps, const int32_t *positions, const double *freqs, int64_t rot,
+                       int interleaved)
+{
+    HeadNormArgs a = {};
+    a.w[0] = qw;
+    a.w[1] = kw;
+    a.w_head[0] = qws;
+    a.w_head[1] = kws;
+    a.positions = positions;
+    a.freqs = freqs;
+    a.tokens = tokens;
+    a.heads = (int)heads;
+    a.kv_heads = (int)kv_heads;
+    a.rows = (int)(heads + kv_heads);
+    a.dim = (int)dim;
+    a.rot = (int)rot;
+    a.interleaved = interleaved;
+    a.norm = eps > 0.0f;
+    a.eps = eps;
+    a.inv_dim = 1.0f / (float)dim;
+    return a;
+}
+
+void set_rows(HeadNormArgs &a, int i, const void *x, Strides s)
+{
+    a.x[i] = x;
+    a.x_tok[i] = s.tok;
+    a.x_head[i] = s.head;
+}
+
+void set_out(HeadNormArgs &a, int i, void *y, Strides s)
+{
+    a.y[i] = y;
+    a.y_tok[i] = s.tok;
+    a.y_head[i] = s.head;
+}
+
+fp4_status check_pool(const fp4_kv_pages *p)
+{
+    if (!p) return FP4_ERR_NULL;
+    if (p->pages <= 0 || p->page_size < 16 || p->page_size > 256 || (p->page_size & (p->page_size - 1))) return FP4_ERR_SHAPE;
+    if (p->pages >= k2GiB / p->page_size) return FP4_ERR_SHAPE;
+    if (!p->free_list || !p->state) return FP4_ERR_NULL;
+    return FP4_OK;
+}
+
+fp4_status check_rows_of(const int32_t *table, int64_t seqs, int64_t width, int64_t stride, int64_t page_size)
+{
+    if (seqs <= 0 || seqs >= (1 << 24) || width <= 0 || width >= (int64_t(1) << 30) / page_size) return FP4_ERR_SHAPE;
+    if (!table) return FP4_ERR_NULL;
+    if (stride < width && seqs > 1) return FP4_ERR_LAYOUT;
+    return FP4_OK;
+}
+
+PageArgs page_args(const fp4_kv_pages *p, int32_t *table, int64_t seqs, int64_t width, int64_t stride,
+                   const int32_t *seq_lens, void *ws)
+{
+    PageArgs a = {};
+    a.free_list = p->free_list;
+    a.state_in = a.state_out = p->state;
+    a.table = table;
+    a.table_stride = stride;
+    a.seq_lens = seq_lens;
+    a.ws = reinterpret_cast<int32_t *>(ws);
+    a.pages = (int)p->pages;
+    a.page_shift = log2_of(p->page_size);
+    a.width = (int)width;
+    a.seqs = (int)seqs;
+    return a;
+}
+
+// Workspace of beam_select: sums, then maxima, values and tokens of the parts
+struct BeamSpace {
+    int64_t parts;  // of all rows
+    size_t top, value, token, bytes;
+};
+
+BeamSpace beam_space(int64_t rows, int64_t vocab, int64_t k, fp4_dtype xt)
+{
+    BeamSpace s;
+    s.parts = rows * beam_parts(rows, vocab, xt);
+    s.top = align256((size_t)s.parts * 8);
+    s.value = s.top + align256((size_t)s.parts * 4);
+    s.token = s.value + align256((size_t)(s.parts * k) * 4);
+    s.bytes = s.token + align256((size_t)(s.parts * k) * 4);
+    return s;
+}
+
+bool beam_sizes_ok(int64_t batch, int64_t beams, int64_t vocab, int64_t k)
+{
+    return batch > 0 && batch < (1 << 24) && beams > 0 && beams <= 64 && vocab > 0 && vocab <= (int64_t(1) << 30) / beams &&
+           k > 0 && k <= 64 && batch * beams < (int64_t(1) << 40) / vocab;
+}
+
+}  // namespace
+
+extern "C" {
+
+fp4_status qk_norm_rope(const void *q, const void *k, fp4_dtype xt, int64_t tokens, int64_t heads, int64_t kv_heads,
+                        int64_t head_dim, int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride,
+                        int64_t k_head_stride, const float *q_weight, const float *k_weight,
+                        int64_t q_weight_stride, int64_t k_weight_stride, float eps, const int32_t *positions,
+                        const double *freqs, int64_t rot, int interleaved, void *q_out, void *k_out, fp4_dtype yt,
+                        int64_t qo_token_stride, int64_t qo_head_stride, int64_t ko_token_stride,
+                        int64_t ko_head_stride, hipStream_t stream)
+{
+    FP4_TRY(check_norm(xt, yt, tokens, heads, kv_heads, head_dim, eps, rot, interleaved));
+    if (tokens == 0) return FP4_OK;
+    FP4_TRY(check_heads(q, q_token_stride, q_head_stride, head_dim, dsize(xt), false));
+    FP4_TRY(check_heads(q_out, qo_token_stride, qo_head_stride, head_dim, dsize(yt), true));
+    if (eps > 0.0f) FP4_TRY(check_weight(q_weight, q_weight_stride));
+    if (kv_heads > 0) {
+        FP4_TRY(check_heads(k, k_token_stride, k_head_stride, head_dim, dsize(xt), false));
+        FP4_TRY(check_heads(k_out, ko_token_stride, ko_head_stride, head_dim, dsize(yt), true));
+        if (eps > 0.0f) FP4_TRY(check_weight(k_weight, k_weight_stride));
+    }
+    FP4_TRY(check_angles(positions, freqs, rot));
+    FP4_TRY(check_device());
+    HeadNormArgs a = norm_args(tokens, heads, kv_heads, head_dim, q_weight, k_weight, q_weight_stride, k_weight_stride, eps,
+                               positions, freqs, rot, interleaved);
+    set_rows(a, 0, q, {q_token_stride, q_head_stride});
+    set_rows(a, 1, k, {k_token_stride, k_head_stride});
+    set_out(a, 0, q_out, {qo_token_stride, qo_head_stride});
+    set_out(a, 1, k_out, {ko_token_stride, ko_head_stride});
+    return launch_head_norm_rope(a, -1, xt, yt, stream);
+}
+
+fp4_status qk_norm_rope_append(const fp4_kv_cache *cache, const void *q, const void *k, const void *v, fp4_dtype xt,
+                               int64_t tokens, int64_t heads, int64_t q_token_stride, int64_t q_head_stride,
+                               int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                               int64_t v_head_stride, const float *q_weight, const float *k_weight,
+                               int64_t q_weight_stride, int64_t k_weight_stride, float eps,
+                               const int32_t *positions, const double *freqs, int64_t rot, int interleaved,
+                               const int64_t *slots, fp4_mx_rule rule, int32_t *nonfinite, void *q_out,
+                               fp4_dtype yt, int64_t qo_token_stride, int64_t qo_head_stride, hipStream_t stream)
+{
+    if (rule != FP4_MX_OCP_FLOOR && rule != FP4_MX_CEIL) return FP4_ERR_DTYPE;
+    FP4_TRY(check_cache(cache));
+    const int64_t dim = cache->head_dim;
+    FP4_TRY(check_norm(xt, yt, tokens, heads, cache->kv_heads, dim, eps, rot, interleaved));
+    if (tokens == 0) return FP4_OK;
+    FP4_TRY(check_heads(q, q_token_stride, q_head_stride, dim, dsize(xt), false));
+    FP4_TRY(check_heads(k, k_token_stride, k_head_stride, dim, dsize(xt), false));
+    FP4_TRY(check_heads(v, v_token_stride, v_head_stride, dim, dsize(xt), false));
+    FP4_TRY(check_heads(q_out, qo_token_stride, qo_head_stride, dim, dsize(yt), true));
+    if (eps > 0.0f) {
+        FP4_TRY(check_weight(q_weight, q_weight_stride));
+        FP4_TRY(check_weight(k_weight, k_weight_stride));
+    }
+    FP4_TRY(check_angles(positions, freqs, rot));
+    if (!slots) return FP4_ERR_NULL;
+    FP4_TRY(check_device());
+    HeadNormArgs a = norm_args(tokens, heads, cache->kv_heads, dim, q_weight, k_weight, q_weight_stride, k_weight_stride, eps,
+                               positions, freqs, rot, interleaved);
+    a.rows += (int)cache->kv_heads;
+    set_rows(a, 0, q, {q_token_stride, q_head_stride});
+    set_rows(a, 1, k, {k_token_stride, k_head_stride});
+    set_rows(a, 2, v, {v_token_stride, v_head_stride});
+    set_out(a, 0, q_out, {qo_token_stride, qo_head_stride});
+    a.kv = kv_args(cache);
+    a.kv.tokens = tokens;
+    a.kv.slots = slots;
+    a.kv.rule = rule;
+    a.kv.nonfinite = nonfinite;
+    return launch_head_norm_rope(a, cache->format, xt, yt, stream);
+}
+
+size_t kv_pages_extend_workspace(int64_t seqs, int64_t tokens)
+{
+    return seqs <= 0 || tokens < 0 ? 0 : pages_extend_bytes(seqs, tokens);
+}
+
+fp4_status kv_pages_extend(const fp4_kv_pages *pool, int32_t *block_table, int64_t seqs, int64_t table_width,
+                           int64_t table_stride, const int32_t *seq_lens, const int32_t *new_lens, int64_t tokens,
+                           int32_t *lens_out, int32_t *state_out, int64_t *slots, int32_t *positions,
+                           int32_t *cu_q, int32_t *cu_k, void *ws, size_t ws_bytes, hipStream_t stream)
+{
+    FP4_TRY(check_pool(pool));
+    FP4_TRY(check_rows_of(block_table, seqs, table_width, table_stride, pool->page_size));
+    if (tokens < 0 || tokens >= (int64_t(1) << 30)) return FP4_ERR_SHAPE;
+    if (!seq_lens || !new_lens || !lens_out || !state_out) return FP4_ERR_NULL;
+    if (tokens > 0 && (!slots || !positions)) return FP4_ERR_NULL;
+    const size_t need = pages_extend_bytes(seqs, tokens);
+    if (need > 0 && (!ws || !aligned16(ws) || ws_bytes < need)) return FP4_ERR_WORKSPACE;
+    FP4_TRY(check_device());
+    PageArgs a = page_args(pool, block_table, seqs, table_width, table_stride, seq_lens, ws);
+    a.new_lens = new_lens;
+    a.lens_out = lens_out;
+    a.state_out = state_out;
+    a.slots = slots;
+    a.positions = positions;
+    a.cu_q = cu_q;
+    a.cu_k = cu_k;
+    a.tokens = tokens;
+    return launch_pages_extend(a, stream);
+}
+
+size_t kv_pages_collect_workspace(int64_t pages, int64_t seqs, int64_t table_width)
+{
+    return pages <= 0 || seqs <= 0 || table_width <= 0 ? 0 : pages_collect_bytes(pages, seqs, table_width);
+}
+
+fp4_status kv_pages_collect(const fp4_kv_pages *pool, const int32_t *block_table, int64_t seqs, int64_t table_width,
+                            int64_t table_stride, const int32_t *seq_lens, void *ws, size_t ws_bytes,
+                            hipStream_t stream)
+{
+    FP4_TRY(check_pool(pool));
+    FP4_TRY(check_rows_of(block_table, seqs, table_width, table_stride, pool->page_size));
+    if (!seq_lens) return FP4_ERR_NULL;
+    const size_t need = pages_collect_bytes(pool->pages, seqs, table_width);
+    if (need > 0 && (!ws || !aligned16(ws) || ws_bytes < need)) return FP4_ERR_WORKSPACE;
+    FP4_TRY(check_device());
+    return launch_pages_collect(
+        page_args(pool, const_cast<int32_t *>(block_table), seqs, table_width, table_stride, seq_lens, ws), stream);
+}
+
+fp4_status kv_pages_reorder(const int32_t *block_table, int64_t batch, int64_t beams, int64_t table_width,
+                            int64_t table_stride, const int32_t *seq_lens, const int32_t *parents,
+                            int64_t page_size, int32_t *out, int64_t out_stride, int32_t *copies,
+                            hipStream_t stream)
+{
+    if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1))) return FP4_ERR_SHAPE;
+    if (batch <= 0 || batch >= (1 << 24) || beams <= 0 || beams > 64) return FP4_ERR_SHAPE;
+    FP4_TRY(check_rows_of(block_table, batch * beams, table_width, table_stride, page_size));
+    FP4_TRY(check_rows_of(out, batch * beams, table_width, out_stride, page_size));
+    if (pages_reorder_grid(batch, table_width) >= (1 << 24)) return FP4_ERR_SHAPE;
+    if (out == block_table && out_stride != table_stride) return FP4_ERR_LAYOUT;
+    if (!seq_lens || !parents || !copies) return FP4_ERR_NULL;
+    FP4_TRY(check_device());
+    BeamTableArgs a = {};
+    a.table = block_table;
+    a.table_stride = table_stride;
+    a.out = out;
+    a.out_stride = out_stride;
+    a.seq_lens = seq_lens;
+    a.parents = parents;
+    a.copies = copies;
+    a.batch = (int)batch;
+    a.beams = (int)beams;
+    a.width = (int)table_width;
+    a.page_shift = log2_of(page_size);
+    return launch_pages_reorder(a, stream);
+}
+
+fp4_status kv_cache_copy(const fp4_kv_cache *cache, const int32_t *copies, int64_t n, hipStream_t stream)
+{
+    FP4_TRY(check_cache(cache));
+    if (n < 0 || n >= (int64_t(1) << 23) / cache->kv_heads) return FP4_ERR_SHAPE;
+    if (n == 0) return FP4_OK;
+    if (!copies) return FP4_ERR_NULL;
+    FP4_TRY(check_device());
+    return launch_kv_copy(kv_args(cache), cache->format, copies, n, stream);
+}
+
+size_t beam_select_workspace(int64_t batch, int64_t beams, int64_t vocab, int64_t k, fp4_dtype xt)
+{
+    if (!valid_dtype(xt) || !beam_sizes_ok(batch, beams, vocab, k)) return 0;
+    return beam_space(batch * beams, vocab, k, xt).bytes;
+}
+
+fp4_status beam_select(const void *logits, fp4_dtype xt, int64_t batch, int64_t beams, int64_t vocab, int64_t ld,
+                       const float *scores, const uint8_t *done, int64_t end_token, int64_t k, float *out_scores,
+                       int32_t *out_parents, int32_t *out_tokens, void *ws, size_t ws_bytes, hipStream_t stream)
+{
+    if (!valid_dtype(xt)) return FP4_ERR_DTYPE;
+    if (!beam_sizes_ok(batch, beams, vocab, k) || end_token < 0 || end_token >= vocab) return FP4_ERR_SHAPE;
+    if (!logits || !scores || !out_scores || !out_parents || !out_tokens) return FP4_ERR_NULL;
+    if (ld < vocab || (reinterpret_cast<uintptr_t>(logits) % dsize(xt)) != 0) return FP4_ERR_LAYOUT;
+    const BeamSpace sp = beam_space(batch * beams, vocab, k, xt);
+    if (!ws || !aligned16(ws) || ws_bytes < sp.bytes) return FP4_ERR_WORKSPACE;
+    FP4_TRY(check_device());
+    uint8_t *base = reinterpret_cast<uint8_t *>(ws);
+    BeamArgs a = {};
+    a.logits = logits;
+    a.ld = ld;
+    a.scores = scores;
+    a.done = done;
+    a.batch = (int)batch;
+    a.beams = (int)beams;
+    a.vocab = (int)vocab;
+    a.k = (int)k;
+    a.end_token = (int)end_token;
+    a.part_sum = reinterpret_cast<double *>(base);
+    a.part_top = reinterpret_cast<float *>(base + sp.top);
+    a.part_value = reinterpret_cast<float *>(base + sp.value);
+    a.part_token = reinterpret_cast<int32_t *>(base + sp.token);
+    a.out_scores = out_scores;
+    a.out_parents = out_parents;
+    a.out_tokens = out_tokens;
+    return launch_beam_select(a, xt, stream);
+}
+
+}  // extern "C"

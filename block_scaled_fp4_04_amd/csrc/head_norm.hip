@@ -1,0 +1,223 @@
+// head_norm.hip -- queries and keys between their projection and the attention: every head's row is
+// normed (root mean square) and rotated by its token's position, in one pass; a second form writes
+// the keys and the values into the paged cache in its format instead of giving key rows.
+//
+// For a row x of `dim` values, y = x (mean x^2 + eps)^-1/2 w; then each pair (y_i, y_j) of the first
+// `rot` turns by the angle position * freqs[i]: (y_i c - y_j s, y_j c + y_i s), with j = i + rot/2 or,
+// interleaved, neighbouring values.
+//
+// One lane holds 8 consecutive values, dim / 8 lanes (rounded up to a power of two) a row, so a wave
+// holds up to 64 / that many rows at a time.  A wave takes one token and walks over its heads: the 8
+// cosines and sines of a lane depend on the token and the lane's place in the row only, and are formed
+// once a token.  Bound by memory where there are many tokens, by the launch where there are few.
+#include "quant_device.h"
+
+namespace fp4k {
+
+namespace {
+
+// sin and cos of a quarter turns: position * freq is taken to quarter turns and reduced in 64 bits
+// (2^31 positions at 1 radian each lose 2^-22 of a turn; in 32 bits a position of 10^6 would be off
+// by 0.06 radian), the rest |t| <= 1/2 goes through polynomials of degree 9 and 8 fitted over that
+// interval (largest error 9e-8).
+__device__ __forceinline__ void turn(double position, double freq, float &c, float &s)
+{
+    const double a = position * (freq * 0.63661977236758134308);  // 2 / pi
+    const double n = __builtin_rint(a);
+    const float t = (float)(a - n), u = t * t;
+    // the quarter, modulo 4: n - 4 rint(n / 4) is in [-2, 2] and exact
+    const int q = (int)(float)__builtin_fma(-4.0, __builtin_rint(n * 0.25), n) & 3;
+    float sn = __builtin_fmaf(u, 1.5820653061382473e-4f, -4.681266378611326e-3f);
+    sn = __builtin_fmaf(u, sn, 0.07969257980585098f);
+    sn = __builtin_fmaf(u, sn, -0.6459640860557556f);
+    sn = __builtin_fmaf(u, sn, 1.5707963705062866f) * t;
+    float cn = __builtin_fmaf(u, 9.0362987248227e-4f, -0.02086007036268711f);
+    cn = __builtin_fmaf(u, cn, 0.25366920232772827f);
+    cn = __builtin_fmaf(u, cn, -1.2337005138397217f);
+    cn = __builtin_fmaf(u, cn, 1.0f);
+    const float x = (q & 1) ? sn : cn, y = (q & 1) ? cn : sn;
+    c = (q == 1 || q == 2) ? -x : x;
+    s = (q & 2) ? -y : y;
+}
+
+// Sum over the 2^lane_shift neighbouring lanes of a row; every lane gets it, in the same order.
+__device__ __forceinline__ float row_sum(float v, int lane_shift)
+{
+    if (lane_shift >= 1) v += xor1(v);
+    if (lane_shift >= 2) v += xor2(v);
+    if (lane_shift >= 3) v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x141, 0xF, 0xF, false));
+    if (lane_shift >= 4) v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x140, 0xF, 0xF, false));
+    if (lane_shift >= 5) v += __shfl_xor(v, 16, kWave);
+    if (lane_shift >= 6) v += __shfl_xor(v, 32, kWave);
+    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T *p, const float (&v)[8])
+{
+    if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]),
+                                                   bf16x2_rne(v[6], v[7]));
+    } else {
+        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    }
+}
+
+// 8 values of a row into the cache (the lanes of a block come here together)
+template <int FMT>
+__device__ __forceinline__ void cache8(const KvArgs &a, int side, int head, int64_t slot, uint32_t c8, int lane_shift,
+                                       const float (&v)[8])
+{
+    const int64_t page = slot >> a.page_shift;
+    const uint32_t off = (uint32_t)slot & ((1u << a.page_shift) - 1u);
+    const int64_t block = (page * a.kv_heads + head) << a.page_shift;
+    uint8_t *codes = side ? a.codes[1] : a.codes[0], *scales = side ? a.scales[1] : a.scales[0];
+    const int64_t unit = ((block + off) << lane_shift) + c8;
+    if constexpr (FMT == FP4_KV_BF16) {
+        store8(reinterpret_cast<uint16_t *>(codes) + unit * 8, v);
+    } else {
+        constexpr int kBlkShift = FMT == FP4_KV_NVFP4 ? 1 : 2;  // lanes of a block
+        constexpr int kUnitB = FMT == FP4_KV_MXFP8 ? 8 : 4;     // code bytes of a unit
+        uint32_t byte;
+        int bad = 0;
+        const float s = FMT == FP4_KV_NVFP4 ? (side ? a.tscale[1] : a.tscale[0])[head] : 0.0f;
+        const uint2 w = kv_encode8<FMT>(v, s, a.rule, byte, bad);
+        uint8_t *cp = codes + unit * kUnitB;
+        if constexpr (kUnitB == 8) *reinterpret_cast<uint2 *>(cp) = w;
+        else *reinterpret_cast<uint32_t *>(cp) = w.x;
+        if ((c8 & ((1u << kBlkShift) - 1u)) == 0u)
+            scales[(block << (lane_shift - kBlkShift)) + ((c8 >> kBlkShift) << a.page_shift) + off] = (uint8_t)byte;
+        if (bad && a.nonfinite) *a.nonfinite = 1;
+    }
+}
+
+constexpr int kRowsOut = -1;  // FMT: key rows are outputs, there is no cache
+
+template <typename TI, typename TO, int FMT>
+__global__ __launch_bounds__(256) void k_head_norm_rope(HeadNormArgs a, int lane_shift)
+{
+    const int64_t token = a.first + (int64_t)blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6);
+    if (token >= a.tokens) return;  // a whole wave
+    const int lane = threadIdx.x & 63;
+    const uint32_t c8 = lane & ((1u << lane_shift) - 1u);
+    const int e0 = (int)c8 * 8;
+    const bool live = e0 < a.dim;
+
+    // cosines and sines of this lane's values: the sign of the partner's share is in sn
+    const bool turns = e0 < a.rot;
+    const int half = a.rot >> 1;
+    float cs[8], sn[8];
+    int partner = lane;
+    if (turns) {
+        const double pos = (double)a.positions[token];
+        if (a.interleaved) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float c, s;
+                turn(pos, a.freqs[(e0 >> 1) + i], c, s);
+                cs[2 * i] = cs[2 * i + 1] = c;
+                sn[2 * i] = -s;
+                sn[2 * i + 1] = s;
+            }
+        } else {
+            const bool upper = e0 >= half;  // rot is a multiple of 16: a lane lies on one side
+            partner = upper ? lane - (half >> 3) : lane + (half >> 3);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                turn(pos, a.freqs[e0 - (upper ? half : 0) + i], cs[i], sn[i]);
+                if (!upper) sn[i] = -sn[i];
+            }
+        }
+    }
+    int64_t slot = -1;
+    if constexpr (FMT != kRowsOut) slot = a.kv.slots[token];
+    const bool stored = FMT != kRowsOut && slot >= 0 && slot < (a.kv.pages << a.kv.page_shift);
+
+    const int last = min(a.rows, (int)(blockIdx.y + 1) * a.slice_rows);
+    for (int r = (int)blockIdx.y * a.slice_rows + (lane >> lane_shift); r - (lane >> lane_shift) < last; r += 64 >> lane_shift) {
+        const int side = r < a.heads ? 0 : r < a.heads + a.kv_heads ? 1 : 2;
+        const int head = r - (side == 0 ? 0 : side == 1 ? a.heads : a.heads + a.kv_heads);
+        const bool here = live && r < last;
+        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (here) Vec8<TI>::load(reinterpret_cast<const TI *>(a.x[side]) + token * a.x_tok[side] + head * a.x_head[side] + e0, v);
+        if (side < 2) {
+            if (a.norm) {
+                float ss = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(v[i], v[i], ss);
+                const float inv = __builtin_amdgcn_rsqf(__builtin_fmaf(row_sum(ss, lane_shift), a.inv_dim, a.eps));
+                float w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                if (here) Vec8<float>::load(a.w[side] + head * a.w_head[side] + e0, w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = v[i] * inv * w[i];
+            }
+            if (a.rot > 0) {
+                float p[8];
+                if (a.interleaved) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) p[i] = v[i ^ 1];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) p[i] = __shfl(v[i], partner, kWave);
+                }
+                if (turns) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = __builtin_fmaf(v[i], cs[i], p[i] * sn[i]);
+                }
+            }
+        }
+        if (!here) continue;
+        if (FMT == kRowsOut || side == 0)
+            store8(reinterpret_cast<TO *>(a.y[side & 1]) + token * a.y_tok[side & 1] + head * a.y_head[side & 1] + e0, v);
+        if constexpr (FMT != kRowsOut) {
+            if (side > 0 && stored) cache8<FMT>(a.kv, side - 1, head, slot, c8, lane_shift, v);
+        }
+    }
+}
+
+}  // namespace
+
+template <typename TI, typename TO, int FMT>
+static void launch_form(HeadNormArgs a, hipStream_t st)
+{
+    int lane_shift = 0;
+    while ((8 << lane_shift) < a.dim) ++lane_shift;
+    const int at_once = 64 >> lane_shift, passes = (a.rows + at_once - 1) / at_once;
+    int64_t slices = 4096 / a.tokens;
+    slices = slices < 1 ? 1 : slices > passes ? passes : slices;
+    const int per = (int)((passes + slices - 1) / slices);
+    a.slice_rows = per * at_once;
+    const int waves = a.tokens >= 1024 ? 4 : 1;
+    // a launch holds fewer than 2^32 threads
+    const int64_t slabs = (passes + per - 1) / per, most = (int64_t(1) << 25) / slabs / waves * waves;
+    for (a.first = 0; a.first < a.tokens; a.first += most) {
+        const int64_t n = a.tokens - a.first < most ? a.tokens - a.first : most;
+        const dim3 grid((unsigned)((n + waves - 1) / waves), (unsigned)slabs);
+        hipLaunchKernelGGL((k_head_norm_rope<TI, TO, FMT>), grid, dim3(64 * waves), 0, st, a, lane_shift);
+    }
+}
+
+template <int FMT>
+static void launch_types(const HeadNormArgs &a, fp4_dtype xt, fp4_dtype yt, hipStream_t st)
+{
+    if (xt == FP4_BF16) {
+        if (yt == FP4_BF16) launch_form<uint16_t, uint16_t, FMT>(a, st);
+        else launch_form<uint16_t, float, FMT>(a, st);
+    } else {
+        if (yt == FP4_BF16) launch_form<float, uint16_t, FMT>(a, st);
+        else launch_form<float, float, FMT>(a, st);
+    }
+}
+
+fp4_status launch_head_norm_rope(const HeadNormArgs &a, int fmt, fp4_dtype xt, fp4_dtype yt, hipStream_t st)
+{
+    if (fmt < 0) launch_types<kRowsOut>(a, xt, yt, st);
+    else if (fmt == FP4_KV_BF16) launch_types<FP4_KV_BF16>(a, xt, yt, st);
+    else if (fmt == FP4_KV_MXFP8) launch_types<FP4_KV_MXFP8>(a, xt, yt, st);
+    else if (fmt == FP4_KV_NVFP4) launch_types<FP4_KV_NVFP4>(a, xt, yt, st);
+    else launch_types<FP4_KV_MXFP4>(a, xt, yt, st);
+    return hipGetLastError() == hipSuccess ? FP4_OK : FP4_ERR_HIP;
+}
+
+}  // namespace fp4k

@@ -227,6 +227,81 @@ int prefill_splits(int64_t q_tokens, int64_t k_tokens, int64_t seqs, int64_t kv_
 size_t prefill_part_rows(int64_t q_tokens, int64_t seqs, int64_t kv_heads, int64_t group, int splits);
 fp4_status launch_attn_prefill(const PrefillArgs &a, hipStream_t st);
 
+// ---- what surrounds attention (head_norm.hip, pages.hip, beam.hip)
+
+struct HeadNormArgs {
+    const void *x[3];             // q, k, v (v: with a cache only)
+    int64_t x_tok[3], x_head[3];  // strides in elements
+    void *y[2];                   // q, k out (k: without a cache only)
+    int64_t y_tok[2], y_head[2];
+    const float *w[2];            // weights of q and k, from head to head w_head
+    int64_t w_head[2];
+    const int32_t *positions;
+    const double *freqs;
+    int64_t tokens, first;        // first token of this launch (set by the launcher)
+    int heads, kv_heads, rows;    // rows of a token: heads, kv_heads and, with a cache, kv_heads again
+    int dim, rot, interleaved, norm;
+    float eps, inv_dim;
+    int slice_rows;               // rows of a wave (set by the launcher)
+    KvArgs kv;                    // the cache: codes, scales, slots, rule, nonfinite
+};
+
+// fmt: the cache's format, or -1: key rows are outputs
+fp4_status launch_head_norm_rope(const HeadNormArgs &a, int fmt, fp4_dtype xt, fp4_dtype yt, hipStream_t st);
+
+struct PageArgs {
+    int32_t *free_list;
+    const int32_t *state_in;
+    int32_t *state_out;
+    int32_t *table;
+    int64_t table_stride;
+    const int32_t *seq_lens, *new_lens;
+    int32_t *lens_out;
+    int64_t *slots;
+    int32_t *positions, *cu_q, *cu_k;
+    int32_t *ws;
+    int64_t tokens;
+    int pages, page_shift, width, seqs;
+};
+
+size_t pages_extend_bytes(int64_t seqs, int64_t tokens);
+fp4_status launch_pages_extend(const PageArgs &a, hipStream_t st);
+size_t pages_collect_bytes(int64_t pages, int64_t seqs, int64_t width);
+fp4_status launch_pages_collect(const PageArgs &a, hipStream_t st);
+
+struct BeamTableArgs {
+    const int32_t *table;
+    int64_t table_stride;
+    int32_t *out;
+    int64_t out_stride;
+    const int32_t *seq_lens, *parents;
+    int32_t *copies;
+    int batch, beams, width, page_shift;
+    int tiles;  // column tiles of a group (set by the launcher)
+};
+
+int64_t pages_reorder_grid(int64_t batch, int64_t width);
+fp4_status launch_pages_reorder(BeamTableArgs a, hipStream_t st);
+fp4_status launch_kv_copy(const KvArgs &a, fp4_kv_format fmt, const int32_t *copies, int64_t n, hipStream_t st);
+
+struct BeamArgs {
+    const void *logits;
+    int64_t ld;
+    const float *scores;
+    const uint8_t *done;
+    int batch, beams, vocab, k, end_token;
+    int parts;            // of a row (set by the launcher)
+    double *part_sum;     // [row][part]
+    float *part_top;
+    float *part_value;    // [row][part][k], best first
+    int32_t *part_token;
+    float *out_scores;
+    int32_t *out_parents, *out_tokens;
+};
+
+int64_t beam_parts(int64_t rows, int64_t vocab, fp4_dtype xt);  // of a row
+fp4_status launch_beam_select(BeamArgs a, fp4_dtype xt, hipStream_t st);
+
 }  // namespace fp4k
 
 // host-side construction of the device divider

@@ -563,6 +563,148 @@ fp4_status attn_prefill(const void *q, int64_t q_tokens, int64_t heads, int64_t 
                         fp4_dtype ot, int64_t o_token_stride, int64_t o_head_stride, float *lse, void *ws,
                         size_t ws_bytes, hipStream_t stream);
 
+/* ------------------------------------------- around the attention ---
+ *
+ * The other steps of serving a layer over the paged cache, so that a generate loop stays on
+ * the device (and can be captured): heads normed and rotated between the projection and the
+ * cache, pages dealt to growing sequences and taken back, beam search.  The decode phase is
+ * bound by the bytes it reads (edge-FP4 article, eefocus.com, "Compute, memory and
+ * precision"); steps of many small launches and host round trips would cost more than that.
+ *
+ * qk_norm_rope: norm and rotation of every head's row, in one pass.  For a row x of q or k,
+ *   y = x (mean_d x^2 + eps)^-1/2 w;   the first `rot` values of y then turn in pairs by
+ *   t_i = position * freqs[i]:  (y_a cos t_i - y_b sin t_i, y_b cos t_i + y_a sin t_i)
+ * with (a, b) = (i, i + rot/2), or (2i, 2i + 1) when interleaved, i < rot/2.
+ *  q, k   [tokens][heads][head_dim], [tokens][kv_heads][head_dim] fp32 or bf16 (xt), any
+ *         token and head strides as above; kv_heads 0: no k (k, k_out null).
+ *  weights fp32 [head_dim], one head's at `stride` elements from the last one's (0: the
+ *         same for every head); 16-byte aligned, strides multiples of 4.  eps > 0 (1e-30 to
+ *         1e30); eps == 0: rows are not normed, weights are not read and may be null.
+ *  positions device int32 [tokens], any values; freqs device fp64 [rot/2] (radians a
+ *         position).  Angles are formed and reduced in 64 bits.  rot == 0: no rotation
+ *         (positions and freqs may be null).
+ *  q_out, k_out fp32 or bf16 (yt), strides as above; the same memory and strides as q, k (with
+ *         xt == yt) is allowed, another overlap is not.
+ * fp32 throughout, rounded once to yt.  head_dim a multiple of 8 up to 512, rot a multiple of
+ * 16 up to head_dim, heads and kv_heads up to 65535, tokens < 2^31 (FP4_ERR_SHAPE).  tokens == 0 returns FP4_OK. */
+fp4_status qk_norm_rope(const void *q, const void *k, fp4_dtype xt, int64_t tokens, int64_t heads, int64_t kv_heads,
+                        int64_t head_dim, int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride,
+                        int64_t k_head_stride, const float *q_weight, const float *k_weight,
+                        int64_t q_weight_stride, int64_t k_weight_stride, float eps, const int32_t *positions,
+                        const double *freqs, int64_t rot, int interleaved, void *q_out, void *k_out, fp4_dtype yt,
+                        int64_t qo_token_stride, int64_t qo_head_stride, int64_t ko_token_stride,
+                        int64_t ko_head_stride, hipStream_t stream);
+
+/* The same with the keys and the values written into the cache: what qk_norm_rope followed by
+ * kv_cache_append does, but the keys are quantized from fp32 (rounded once), and in one
+ * launch.  q and k as qk_norm_rope (kv_heads and head_dim are the cache's); v, slots, rule
+ * and nonfinite as kv_cache_append. */
+fp4_status qk_norm_rope_append(const fp4_kv_cache *cache, const void *q, const void *k, const void *v, fp4_dtype xt,
+                               int64_t tokens, int64_t heads, int64_t q_token_stride, int64_t q_head_stride,
+                               int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                               int64_t v_head_stride, const float *q_weight, const float *k_weight,
+                               int64_t q_weight_stride, int64_t k_weight_stride, float eps,
+                               const int32_t *positions, const double *freqs, int64_t rot, int interleaved,
+                               const int64_t *slots, fp4_mx_rule rule, int32_t *nonfinite, void *q_out,
+                               fp4_dtype yt, int64_t qo_token_stride, int64_t qo_head_stride, hipStream_t stream);
+
+/* Pages that no sequence holds.
+ *  free_list device int32 [pages]: the first state[0] entries are free page ids; pages are
+ *         taken from the end.
+ *  state  device int32 [2]: the number of free pages, and how many sequences kv_pages_extend
+ *         has refused (added up, never cleared by the library).
+ * pages, page_size: as fp4_kv_cache.  One pool serves the caches of all layers.  Calls that
+ * change a pool or a block table are ordered by the caller, like any calls on one memory. */
+typedef struct {
+    int32_t *free_list;
+    int32_t *state;
+    int64_t pages, page_size;
+} fp4_kv_pages;
+
+/* Workspace bytes of kv_pages_extend: 0 when one launch serves the sizes (ws may be null). */
+size_t kv_pages_extend_workspace(int64_t seqs, int64_t tokens);
+
+/* New tokens for sequences: pages dealt, block table extended, slots and positions listed.
+ * Sequence b holds seq_lens[b] tokens in row b of the block table and takes new_lens[b]
+ * (negative: 0) more, packed one sequence behind the other.
+ *  block_table device int32 [seqs][table_stride]: entries of new pages are written, others
+ *         left as they are.
+ *  tokens slots and positions written; at least the sum of new_lens (known to the caller,
+ *         so that nothing waits for the device).  Those past the sum get slot -1, position 0.
+ *  lens_out int32 [seqs], state_out int32 [2]: the lengths and the pool's state after; may be
+ *         seq_lens and the pool's state themselves.
+ *  slots  int64 [tokens] as kv_cache_append; positions int32 [tokens].
+ *  cu_q, cu_k optional int32 [seqs+1]: offsets of the new tokens, and of the whole contexts
+ *         (lens_out), as attn_prefill and kv_cache_read take them.
+ * Pages are dealt in the order of the sequences and their positions.  A sequence that cannot
+ * be served whole (too few free pages are left, the table's row is too narrow, its tokens
+ * lie past `tokens`, its length is negative) is refused: its length, its row and the pool stay as
+ * they are, its slots are -1 (its positions are those it asked for), and state_out[1] counts it.  Later
+ * sequences that need no page are still served.
+ * No page id or length makes the call access anything outside the buffers.
+ * seqs < 2^24, table_width * page_size < 2^30, tokens < 2^30 (FP4_ERR_SHAPE). */
+fp4_status kv_pages_extend(const fp4_kv_pages *pool, int32_t *block_table, int64_t seqs, int64_t table_width,
+                           int64_t table_stride, const int32_t *seq_lens, const int32_t *new_lens, int64_t tokens,
+                           int32_t *lens_out, int32_t *state_out, int64_t *slots, int32_t *positions,
+                           int32_t *cu_q, int32_t *cu_k, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* Workspace bytes of kv_pages_collect (0: ws may be null). */
+size_t kv_pages_collect_workspace(int64_t pages, int64_t seqs, int64_t table_width);
+
+/* The free list anew: every page that no row holds in its first ceil(seq_lens[b] / page_size)
+ * entries, in ascending order; state[0] is their number, entries past it are left.  So the pages of a
+ * sequence that ended (its length set to 0), of dropped beams or of a shortened sequence come
+ * back; a page held by several rows stays held.  Entries outside [0, pages) are passed over. */
+fp4_status kv_pages_collect(const fp4_kv_pages *pool, const int32_t *block_table, int64_t seqs, int64_t table_width,
+                            int64_t table_stride, const int32_t *seq_lens, void *ws, size_t ws_bytes,
+                            hipStream_t stream);
+
+/* Block tables of beams after a selection: row j of a group of `beams` rows takes the row of
+ * its parent.
+ *  block_table, out device int32 [batch * beams][stride]; out may be block_table itself (with the same
+ *         stride; another overlap is not allowed).
+ *  seq_lens int32 [batch * beams]; the rows of a group have the same length.
+ *  parents int32 [batch * beams], each in [0, beams) (another value: the row keeps its own).
+ *  copies int32 [batch * beams][3], out: {source page, destination page, tokens}, or
+ *         {-1, -1, 0}.
+ * Full pages are shared by the rows that hold them.  A partly filled page belongs to one row
+ * (as kv_pages_extend deals them): a parent's first child keeps it, each further child gets
+ * the partly filled page of a row that has no child, into which the parent's tokens have to be copied
+ * (kv_cache_copy, once for each layer's cache).  Pages that no row holds any more come back with
+ * kv_pages_collect.  Entries past a row's pages are left as they are.
+ * beams <= 64; batch * ceil(table_width / 256) < 2^24 (FP4_ERR_SHAPE). */
+fp4_status kv_pages_reorder(const int32_t *block_table, int64_t batch, int64_t beams, int64_t table_width,
+                            int64_t table_stride, const int32_t *seq_lens, const int32_t *parents,
+                            int64_t page_size, int32_t *out, int64_t out_stride, int32_t *copies,
+                            hipStream_t stream);
+
+/* For each of n records of `copies` (device int32 [n][3]) the first `tokens` tokens of the source page
+ * are copied into the destination page: keys and values, codes and scale bytes, of all heads.  Records with
+ * an id outside the cache or no tokens are skipped.  No page may be the destination of two records, or of one
+ * and the source of another.  n * kv_heads < 2^23 (FP4_ERR_SHAPE); n == 0 returns FP4_OK. */
+fp4_status kv_cache_copy(const fp4_kv_cache *cache, const int32_t *copies, int64_t n, hipStream_t stream);
+
+/* Workspace bytes of beam_select. */
+size_t beam_select_workspace(int64_t batch, int64_t beams, int64_t vocab, int64_t k, fp4_dtype xt);
+
+/* Beam search's selection: for each of `batch` groups the k best of all beams' continuations,
+ *   total(i, v) = score_i + logit_iv - log sum_u exp(logit_iu),
+ * best first, equal ones by beam, then token.
+ *  logits [batch * beams][ld] fp32 or bf16 (xt), ld >= vocab, any alignment of an element.
+ *  scores fp32 [batch * beams], finite, or -infinity: the beam offers nothing.
+ *  done   optional uint8 [batch * beams]: nonzero: the beam has ended and offers one
+ *         continuation, end_token at its own score; its logits are not read.
+ *  out_scores fp32, out_parents (the beam within its group) and out_tokens int32, [batch][k].
+ * Only totals above -infinity are chosen (logits of -infinity are masked tokens; a row that
+ * holds a NaN or +infinity offers nothing).  Places that are left get score -infinity, token -1 and parent
+ * min(place, beams - 1).
+ *  ws     beam_select_workspace() bytes, 16-byte aligned.
+ * Totals are compared in 64 bits; a row's sum is within 2^-22 relative.  1 <= k <= 64,
+ * beams <= 64, beams * vocab <= 2^30, 0 <= end_token < vocab, batch * beams * vocab < 2^40 (FP4_ERR_SHAPE). */
+fp4_status beam_select(const void *logits, fp4_dtype xt, int64_t batch, int64_t beams, int64_t vocab, int64_t ld,
+                       const float *scores, const uint8_t *done, int64_t end_token, int64_t k, float *out_scores,
+                       int32_t *out_parents, int32_t *out_tokens, void *ws, size_t ws_bytes, hipStream_t stream);
+
 /* ---------------------------------------------------------- measurement --
  * fp4blk_read_ceiling: reads `bytes` bytes at `buf` once, with `grid`
  * workgroups of 512 threads striding over 16-byte words, and computes nothing

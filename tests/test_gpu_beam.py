@@ -1,0 +1,211 @@
+"""Beam selection on the GPU against the definition in 64 bits."""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+def _fp4():
+    import block_scaled_fp4_04_amd as fp4
+
+    return fp4
+
+
+def _totals(logits, scores, done, end):
+    """float64 [batch, beams * vocab] on the host; what is not offered is -inf."""
+    batch, beams = scores.shape
+    z = logits.cpu().double().view(batch, beams, -1)
+    t = scores.cpu().double()[..., None] + z - torch.logsumexp(z, -1, keepdim=True)
+    if done is not None:
+        d = done.cpu().bool()
+        t[d] = -math.inf
+        t[..., end] = torch.where(d, scores.cpu().double(), t[..., end])
+    return torch.where(t.isnan(), -math.inf, t).flatten(1)
+
+
+def _check(logits, scores, k, done=None, end=0, exact=False, **kw):
+    """Scores within 2^-20 of the definition's (a sum's exponentials, additions and logarithm together 2^-22 of 1, the
+    result's rounding 2^-24 of it); the choice is the definition's, but that totals nearer than the sums'
+    errors (2^-20) may stand in either order (`exact`: never)."""
+    fp4 = _fp4()
+    s, p, t = fp4.beam_select(logits, scores, k=k, done=done, end_token=end, **kw)
+    batch, beams = scores.shape
+    vocab = logits.shape[1]
+    total = _totals(logits, scores, done, end)
+    best, at = torch.sort(total, dim=-1, descending=True, stable=True)
+    pad = k - min(k, beams * vocab)
+    best = torch.cat([best[:, :k], torch.full((batch, pad), -math.inf, dtype=torch.float64)], 1)
+    at = torch.cat([at[:, :k], torch.zeros(batch, pad, dtype=torch.long)], 1)
+    real = best > -math.inf
+    s, p, t = s.cpu(), p.cpu().long(), t.cpu().long()
+    assert s.shape == p.shape == t.shape == (batch, k)
+    assert torch.equal(s > -math.inf, real)
+    assert bool((s[~real] == -math.inf).all()) and bool((t[~real] == -1).all())
+    assert torch.equal(p[~real], torch.arange(k).clamp(max=beams - 1).expand(batch, k)[~real])
+    tol = 2.0 ** -20 * (1 + best.abs())
+    assert bool(((s.double() - best).abs() <= tol)[real].all()), float((s.double() - best).abs()[real].max())
+    flat = p * vocab + t
+    same = flat == at
+    assert bool((0 <= p).all()) and bool((p < beams).all()) and bool((t < vocab).all())
+    if exact:
+        assert bool(same[real].all()), (flat[~same & real], at[~same & real])
+    chosen = total.gather(1, flat.clamp(min=0))
+    assert bool(((chosen - best).abs() <= tol)[real].all())
+    for b in range(batch):  # nothing twice
+        f = flat[b][real[b]]
+        assert f.unique().numel() == f.numel()
+    return s, p, t
+
+
+def _logits(rows, vocab, dtype, seed, spread=2.0):
+    g = torch.Generator("cuda").manual_seed(seed)
+    x = spread * torch.randn(rows, vocab, device="cuda", generator=g)
+    x[torch.rand(rows, vocab, device="cuda", generator=g) < 0.002] += 5.0
+    return x.to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("batch,beams,vocab,k", [(1, 1, 1, 1), (1, 1, 7, 3), (2, 3, 5, 16), (3, 4, 257, 4), (1, 4, 32000, 4), (5, 2, 2047, 2), (4, 5, 2049, 10),
+                                                 (2, 8, 8191, 16), (2, 7, 50003, 14), (1, 64, 1000, 64), (3, 16, 5000, 33), (40, 8, 131072, 8),
+                                                 (65, 8, 40009, 16)])
+def test_select(batch, beams, vocab, k, dtype):
+    logits = _logits(batch * beams, vocab, dtype, vocab + k)
+    scores = -10 * torch.rand(batch, beams, device="cuda", generator=torch.Generator("cuda").manual_seed(k))
+    _check(logits, scores, k)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("off", range(8))
+def test_rows_at_any_element(off, dtype):
+    """Rows that begin anywhere and a stride that moves them: every alignment of a first and last vector."""
+    rows, vocab = 6, 2050 + off
+    room = torch.full((rows * (vocab + 13) + 40,), 1e4, dtype=dtype, device="cuda")  # read by mistake it would win
+    logits = room[off:off + rows * (vocab + 13)].view(rows, vocab + 13)[:, :vocab]
+    logits.copy_(_logits(rows, vocab, dtype, off))
+    logits[:, 0], logits[:, -1] = 9.0, 9.5
+    s, p, t = _check(logits, torch.zeros(2, 3, device="cuda"), 6)
+    contiguous = logits.contiguous()
+    assert all(torch.equal(a, b) for a, b in zip(_check(contiguous, torch.zeros(2, 3, device="cuda"), 6)[1:], (p, t)))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("vocab", [3, 500, 9000, 40000])
+def test_ties(vocab, dtype):
+    """Equal totals go to the lowest beam, then token: constant rows, equal beams, few levels."""
+    fp4 = _fp4()
+    zero = torch.zeros(1, 4, device="cuda")
+    x = torch.zeros(4, vocab, dtype=dtype, device="cuda")
+    s, p, t = fp4.beam_select(x, zero, k=6)
+    want = [(i // vocab, i % vocab) for i in range(6)]
+    assert p.tolist() == [[a for a, _ in want]] and t.tolist() == [[b for _, b in want]]
+    row = torch.randint(0, 4, (vocab,), generator=torch.Generator().manual_seed(vocab)).to(dtype)
+    x = row.cuda().expand(4, vocab).contiguous()
+    order = torch.sort(row.double(), descending=True, stable=True).indices
+    s, p, t = fp4.beam_select(x, zero, k=8)
+    top = int((row == row.max()).sum())
+    want = [(b, int(order[i])) for b in range(4) for i in range(min(top, 8))][:8]  # of equal rows, beam 0's first
+    assert list(zip(p[0].tolist(), t[0].tolist()))[:len(want)] == want
+    s, p, t = fp4.beam_select(x[:1], zero[:, :1], k=min(64, vocab))
+    assert t[0].tolist() == order[:min(64, vocab)].tolist()
+    # -0 and 0 are equal
+    x = torch.zeros(1, vocab, dtype=dtype, device="cuda")
+    x[0, 0] = -0.0
+    assert fp4.beam_select(x, zero[:, :1], k=2)[2].tolist() == [[0, 1]]
+
+
+@pytest.mark.parametrize("vocab", [40, 3000, 20000])
+def test_masked_and_nonfinite(vocab):
+    fp4 = _fp4()
+    inf = math.inf
+    x = _logits(8, vocab, torch.float32, 3)
+    scores = torch.tensor([[0.0, -1.0, -inf, -2.0], [-1.0, -1.0, -1.0, -1.0]], device="cuda")
+    x[0, 5:] = -inf                                   # five tokens are left
+    x[1, :] = -inf                                    # nothing
+    x[3, 7] = float("nan")                            # spoils its row
+    x[4, 11] = inf
+    x[5, :] = torch.finfo(torch.float32).min          # all equal, at the lowest value
+    x[6, ::2] = torch.finfo(torch.float32).min
+    _check(x, scores, 8)
+    _check(x, scores, 3)
+    s, p, t = _check(x, torch.full((2, 4), -inf, device="cuda"), 5)
+    assert bool((s == -inf).all())
+    # one token alone, at the far end
+    y = torch.full((4, vocab), -inf, dtype=torch.bfloat16, device="cuda")
+    y[2, vocab - 1] = -3.0
+    s, p, t = fp4.beam_select(y, torch.zeros(1, 4, device="cuda"))
+    assert t.tolist() == [[vocab - 1, -1, -1, -1]] and p.tolist() == [[2, 1, 2, 3]] and s[0, 0] == 0.0
+
+
+@pytest.mark.parametrize("kind", [torch.bool, torch.uint8])
+def test_ended_beams(kind):
+    fp4 = _fp4()
+    batch, beams, vocab = 6, 5, 9001
+    x = _logits(batch * beams, vocab, torch.bfloat16, 9)
+    g = torch.Generator("cuda").manual_seed(2)
+    scores = -6 * torch.rand(batch, beams, device="cuda", generator=g)
+    done = (torch.rand(batch, beams, device="cuda", generator=g) < 0.4)
+    done[0] = True
+    done[1] = False
+    x[done.flatten()] = float("nan")  # not read
+    d = done.to(kind) * (3 if kind == torch.uint8 else 1) if kind == torch.uint8 else done
+    for k in (5, 10):
+        _check(x, scores, k, done=d, end=vocab - 1)
+    s, p, t = fp4.beam_select(x, scores, k=10, done=d, end_token=77)
+    assert t[0].tolist() == [77] * 5 + [-1] * 5
+    order = torch.sort(scores[0], descending=True, stable=True)
+    assert p[0, :5].tolist() == order.indices.tolist() and torch.equal(s[0, :5], order.values)
+
+
+def test_small_differences_of_low_scores():
+    """Logits of neighbouring fp32 values under scores where fp32 sums would merge them."""
+    fp4 = _fp4()
+    base = torch.full((1, 4000), -20.0, device="cuda")
+    eps = 2.0 ** -23
+    at = [3000, 17, 2999, 5]
+    for i, a in enumerate(at):
+        base[0, a] = 1.0 + (4 - i) * eps
+    s, p, t = fp4.beam_select(base, torch.full((1, 1), -400.0, device="cuda"), k=4)
+    assert t.tolist() == [at]
+
+
+def test_large_logits():
+    """Differences past the range of the exponential, and rows whose best are far apart between parts."""
+    x = _logits(3, 30000, torch.float32, 4) * 50
+    x[0, 29999] = 1e30
+    x[1, 12345] = -1e30
+    x[2] = x[2] * 1e30
+    _check(x, torch.tensor([[-1.0, -2.0, -3.0]], device="cuda"), 6)
+
+
+def test_captured_with_one_workspace():
+    fp4 = _fp4()
+    batch, beams, vocab, k = 3, 4, 5001, 8
+    ws = fp4.beam_select_workspace(batch, beams, vocab, k)
+    x, scores = _logits(12, vocab, torch.bfloat16, 1), torch.zeros(batch, beams, device="cuda")
+    out = tuple(torch.empty(batch, k, dtype=d, device="cuda") for d in (torch.float32, torch.int32, torch.int32))
+    fp4.beam_select(x, scores, k=k, workspace=ws)
+    graphs = []
+    for _ in range(2):  # two graphs share the workspace, replayed one behind the other
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = fp4.beam_select(x, scores, k=k, workspace=ws, out=out)
+        assert got is out
+        graphs.append(g)
+    for i in range(4):
+        x.copy_(_logits(12, vocab, torch.bfloat16, 30 + i))
+        scores.copy_(-torch.rand(batch, beams))
+        graphs[i % 2].replay()
+        want = fp4.beam_select(x, scores, k=k)
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), i
+
+
+def test_many_parts():
+    """A vocabulary of many parts, few rows; the best at a part's first and last place."""
+    vocab = 1 << 20
+    x = torch.zeros(2, vocab, dtype=torch.bfloat16, device="cuda")
+    at = [0, 2047, 2048, 8191, 8192, 524287, vocab - 1]
+    for i, a in enumerate(at):
+        x[0, a], x[1, a] = 20.0 - i, 13.0 + i / 2
+    _check(x, torch.tensor([[0.0, -0.25]], device="cuda"), 12)

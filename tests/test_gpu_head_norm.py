@@ -1,0 +1,267 @@
+"""Norm and rotation of heads on the GPU against the formula in 64 bits, and the form that writes the cache
+against the two calls it stands for."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+def _fp4():
+    import block_scaled_fp4_04_amd as fp4
+
+    return fp4
+
+
+def _ref(x, positions, freqs, weight, eps, interleaved):
+    """Rows in float64, and what an error of the pair (a, b) is measured against: |a| + |b|."""
+    y = x.double().cpu()
+    if eps is not None:
+        y = y / torch.sqrt((y * y).mean(-1, keepdim=True) + eps) * weight.double().cpu()
+    size = y.abs()
+    rot = 0 if freqs is None else 2 * freqs.shape[0]
+    if rot:
+        a = positions.cpu().double()[:, None] * freqs.cpu()
+        c, s = a.cos()[:, None], a.sin()[:, None]
+        h = y[..., :rot].clone()
+        first = slice(0, rot, 2) if interleaved else slice(0, rot // 2)
+        second = slice(1, rot, 2) if interleaved else slice(rot // 2, rot)
+        u, w = h[..., first], h[..., second]
+        both = u.abs() + w.abs()
+        y, size = y.clone(), size.clone()
+        turned = torch.empty_like(h)
+        turned[..., first], turned[..., second] = u * c - w * s, w * c + u * s
+        y[..., :rot] = turned
+        sizes = torch.empty_like(h)
+        sizes[..., first] = sizes[..., second] = both
+        size[..., :rot] = sizes
+    return y, size
+
+
+def _close(got, ref, what):
+    """fp32: a mean of squares has at most 8 + 6 additions and a rounding more (15 2^-24, halved by the root), the
+    root and two products 4 2^-24 at most, so 2^-20 covers the norm; cosine and sine are within 2^-22 and the products and
+    their sum 2 2^-24 of |a| + |b|.  In all 2^-19.  bf16: half a step, 2^-8, of the result more."""
+    y, size = ref
+    assert tuple(got.shape) == tuple(y.shape), what
+    lim = 2.0 ** -19 * size + (2.0 ** -8 * y.abs() if got.dtype == torch.bfloat16 else 0)
+    err = (got.double().cpu() - y).abs()
+    bad = ~(err <= lim + 1e-37)
+    assert not bool(bad.any()), f"{what}: {int(bad.sum())} of {bad.numel()}, first {bad.nonzero()[0].tolist()}, worst {float((err / (lim + 1e-37)).max()):.3g}"
+
+
+def _rows(n, h, d, dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(n, h, d, generator=g)
+    x[torch.rand(n, h, d, generator=g) < 0.02] *= 50.0
+    if n > 1:
+        x[1] = 0.0  # a row of zeros stays zeros
+        x[0, 0] *= 1e-12
+    return x.to(dtype).cuda()
+
+
+def _weight(shape, seed):
+    return (1.0 + 0.3 * torch.randn(shape, generator=torch.Generator().manual_seed(seed))).cuda()
+
+
+@pytest.mark.parametrize("dim,rot", [(16, 16), (24, 16), (48, 0), (64, 64), (80, 32), (96, 96), (128, 128), (128, 32),
+                                     (160, 160), (256, 64), (256, 256), (512, 512), (504, 496)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rows(dim, rot, interleaved):
+    fp4 = _fp4()
+    for n, hq, hk, xt, yt, eps, by_head in [(5, 3, 1, torch.bfloat16, torch.bfloat16, 1e-6, False),
+                                            (1, 33, 2, torch.bfloat16, torch.float32, 1e-5, True),
+                                            (1100, 5, 3, torch.float32, torch.float32, None, False),
+                                            (37, 8, 8, torch.float32, torch.bfloat16, 1e-6, True)]:
+        q, k = _rows(n, hq, dim, xt, 1), _rows(n, hk, dim, xt, 2)
+        pos = torch.randint(-5, 1 << 20, (n,), generator=torch.Generator().manual_seed(3), dtype=torch.int32).cuda()
+        freqs = fp4.rope_frequencies(rot) if rot else None
+        qw, kw = (_weight((h, dim) if by_head else (dim,), h) if eps else None for h in (hq, hk))
+        qo, ko = fp4.qk_norm_rope(q, k, pos, freqs, qw, kw, eps=eps, interleaved=interleaved, dtype=yt)
+        _close(qo, _ref(q, pos, freqs, qw, eps, interleaved), f"q {n} {hq} {eps} {yt}")
+        _close(ko, _ref(k, pos, freqs, kw, eps, interleaved), f"k {n} {hk} {eps} {yt}")
+
+
+def test_far_positions_and_steep_frequencies():
+    fp4 = _fp4()
+    pos = torch.tensor([0, 1, -1, 2 ** 24 + 1, 2 ** 31 - 1, -2 ** 31, 12345678], dtype=torch.int32).cuda()
+    freqs = torch.tensor([1.0, 3.14159265358979, 1e-9, 0.5, 2.75, 0.0, 1e-3, 7e-5], dtype=torch.float64).cuda()
+    x = _rows(7, 2, 16, torch.float32, 5)
+    got, none = fp4.qk_norm_rope(x, None, pos, freqs, dtype=torch.float32)
+    assert none is None
+    # 64-bit angles of 2^33 radians carry 2^-20 of their own in the reference: take the angle modulo 2 pi from its parts
+    y = x.double().cpu()
+    import math
+    from fractions import Fraction
+    pi = Fraction(314159265358979323846264338327950288419716939937510, 10 ** 50)
+    a = torch.tensor([[float(Fraction(int(p)) * Fraction(float(f)) % (2 * pi)) for f in freqs.cpu()] for p in pos.cpu()], dtype=torch.float64)
+    c, s = a.cos()[:, None], a.sin()[:, None]
+    u, w = y[..., :8], y[..., 8:]
+    want = torch.cat([u * c - w * s, w * c + u * s], -1)
+    size = (u.abs() + w.abs()).repeat(1, 1, 2)
+    # the product of position and frequency is rounded at 2^-53 of up to 2^33 radians, twice
+    err = (got.double().cpu() - want).abs()
+    assert bool((err <= (2.0 ** -19 + 2.0 ** -18 * (a.new_tensor(pos.cpu().double().abs() / 2 ** 31)[:, None, None])) * size + 1e-37).all()), float((err / size.clamp(min=1e-30)).max())
+    assert math.isfinite(float(err.max()))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_strides_and_in_place(interleaved):
+    fp4 = _fp4()
+    n, hq, hk, d = 41, 6, 2, 64
+    whole = _rows(n, hq + 2 * hk, d, torch.bfloat16, 7)
+    q, k = whole[:, :hq], whole[:, hq:hq + hk]
+    pos = torch.arange(n, dtype=torch.int32).cuda() * 17
+    freqs, qw, kw = fp4.rope_frequencies(d, 5e5), _weight((d,), 1), _weight((hk, d), 2)
+    args = (pos, freqs, qw, kw)
+    want = fp4.qk_norm_rope(q, k, *args, eps=1e-6, interleaved=interleaved)
+    _close(want[0], _ref(q, pos, freqs, qw, 1e-6, interleaved), "columns of a projection")
+    # heads outermost, repeated rows, a view with room between the rows
+    hf = q.transpose(0, 1).contiguous().transpose(0, 1)
+    assert torch.equal(fp4.qk_norm_rope(hf, k, *args, eps=1e-6, interleaved=interleaved)[0], want[0])
+    same = k[:, :1].expand(n, hk, d)
+    got = fp4.qk_norm_rope(q, same, *args, eps=1e-6, interleaved=interleaved)[1]
+    _close(got, _ref(same, pos, freqs, kw, 1e-6, interleaved), "one head repeated")
+    room = torch.full((n, hq + 3, d + 32), 7.0, dtype=torch.bfloat16, device="cuda")
+    fp4.qk_norm_rope(q, k, *args, eps=1e-6, interleaved=interleaved, q_out=room[:, 2:2 + hq, :d])
+    assert torch.equal(room[:, 2:2 + hq, :d], want[0])
+    assert bool((room[:, :2] == 7).all()) and bool((room[:, :, d:] == 7).all()) and bool((room[:, 2 + hq:] == 7).all())
+    # in place; the values' columns stay
+    before = whole.clone()
+    got = fp4.qk_norm_rope(q, k, *args, eps=1e-6, interleaved=interleaved, q_out=q, k_out=k)
+    assert got[0] is q and torch.equal(q, want[0]) and torch.equal(k, want[1])
+    assert torch.equal(whole[:, hq + hk:], before[:, hq + hk:])
+
+
+def test_nonfinite_rows_stay_apart():
+    """A row with an infinity or NaN spoils itself only."""
+    fp4 = _fp4()
+    for dim in (64, 80, 128):
+        x = _rows(9, 5, dim, torch.float32, 11)
+        pos = torch.arange(9, dtype=torch.int32).cuda()
+        args = (pos, fp4.rope_frequencies(32), _weight((dim,), 1))
+        clean = fp4.qk_norm_rope(x, None, *args, eps=1e-6, dtype=torch.float32)[0]
+        x[3, 2, 7], x[4, 0, 50] = float("nan"), float("inf")
+        got = fp4.qk_norm_rope(x, None, *args, eps=1e-6, dtype=torch.float32)[0]
+        hit = torch.zeros(9, 5, dtype=torch.bool)
+        hit[3, 2] = hit[4, 0] = True
+        assert torch.equal(got[~hit.cuda()], clean[~hit.cuda()])
+        assert bool(got[3, 2].isnan().all())
+        # not normed: values that do not turn with it are untouched
+        got = fp4.qk_norm_rope(x, None, pos, fp4.rope_frequencies(32), dtype=torch.float32)[0]
+        assert torch.equal(got[4, 0, 32:], x[4, 0, 32:]) and bool(got[3, 2, [8, 9, 40]].isfinite().all())
+
+
+def test_many_tokens():
+    """More tokens than one wave each: the first, the last and those between give what they give alone."""
+    fp4 = _fp4()
+    n, d = 70001, 64
+    q = torch.randn(n, 2, d, device="cuda", generator=torch.Generator("cuda").manual_seed(1)).to(torch.bfloat16)
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    freqs, w = fp4.rope_frequencies(d), _weight((d,), 4)
+    got = fp4.qk_norm_rope(q, None, pos, freqs, w, eps=1e-6)[0]
+    at = torch.tensor([0, 1, 255, 256, 4095, 4096, 65535, 65536, n - 1], device="cuda")
+    alone = fp4.qk_norm_rope(q[at], None, pos[at], freqs, w, eps=1e-6)[0]
+    assert torch.equal(got[at], alone)
+    _close(alone, _ref(q[at], pos[at], freqs, w, 1e-6, False), "tokens picked")
+
+
+def test_past_4gib():
+    """Offsets past 32 bits: rows of a buffer of 6 GB."""
+    fp4 = _fp4()
+    n, step = 4, 3 * (1 << 28)  # elements between tokens
+    base = torch.empty(n * step, dtype=torch.bfloat16, device="cuda")
+    q = base.as_strided((n, 3, 128), (step, 128, 1))
+    q.copy_(_rows(n, 3, 128, torch.bfloat16, 9))
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    want = fp4.qk_norm_rope(q.contiguous(), None, pos, fp4.rope_frequencies(128))[0]
+    assert torch.equal(fp4.qk_norm_rope(q, None, pos, fp4.rope_frequencies(128))[0], want)
+    fp4.qk_norm_rope(q, None, pos, fp4.rope_frequencies(128), q_out=q)
+    assert torch.equal(q, want)
+
+
+def _cache(fp4, fmt, pages, heads, page, dim):
+    ts = [None, None]
+    if fmt == "nvfp4":
+        ts = [(0.001 + 0.01 * torch.rand(heads, generator=torch.Generator().manual_seed(s))).cuda() for s in (1, 2)]
+    c = fp4.KVCache.alloc(fmt, pages, heads, page, dim, "cuda", *ts)
+    for t in (c.k_codes, c.v_codes, c.k_scales, c.v_scales):
+        if t is not None:
+            t.view(torch.uint8).fill_(0xA5)  # what is not written has to stay
+    return c
+
+
+def _same(a, b):
+    for x in ("k_codes", "v_codes", "k_scales", "v_scales"):
+        u, w = getattr(a, x), getattr(b, x)
+        if u is not None:
+            assert torch.equal(u.view(torch.uint8), w.view(torch.uint8)), x
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8", "nvfp4", "mxfp4"])
+@pytest.mark.parametrize("dim,heads,kv,page", [(64, 4, 1, 16), (128, 15, 5, 64), (256, 2, 2, 256)])
+def test_append_is_the_two_calls(fmt, dim, heads, kv, page):
+    """Keys quantized from fp32 are what kv_cache_append makes of fp32 rows; q is what qk_norm_rope gives."""
+    fp4 = _fp4()
+    for n, xt, rule, eps, inter, rot in [(37, torch.bfloat16, "ocp", 1e-6, False, dim), (1, torch.float32, "ceil", None, True, 32),
+                                         (1200, torch.bfloat16, "ceil", 1e-6, True, 0)]:
+        pages = (n + page - 1) // page + 3
+        whole = _rows(n, heads + 2 * kv, dim, xt, 3)
+        q, k, v = whole.split([heads, kv, kv], 1)
+        g = torch.Generator().manual_seed(5)
+        slots = torch.randperm(pages * page, generator=g)[:n]
+        if n > 5:
+            slots[2], slots[5] = -1, pages * page  # skipped
+        slots = slots.cuda()
+        pos = torch.randint(0, 100000, (n,), generator=g, dtype=torch.int32).cuda()
+        freqs = fp4.rope_frequencies(rot) if rot else None
+        qw, kw = (_weight((h, dim), h) if eps else None for h in (heads, kv))
+        one, two = _cache(fp4, fmt, pages, kv, page, dim), _cache(fp4, fmt, pages, kv, page, dim)
+        bad = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = fp4.qk_norm_rope_append(one, q, k, v, pos, slots, freqs, qw, kw, eps=eps, interleaved=inter, rule=rule, nonfinite=bad)
+        want, kr = fp4.qk_norm_rope(q, k, pos, freqs, qw, kw, eps=eps, interleaved=inter, dtype=torch.float32)
+        fp4.kv_cache_append(two, kr, v.float(), slots, rule=rule)
+        assert torch.equal(got, want.to(torch.bfloat16))
+        _same(one, two)
+        assert int(bad) == 0
+        if n > 5 and fmt != "bf16":
+            v = v.clone()
+            v[2, 0, 0] = float("nan")  # a token that is not stored
+            fp4.qk_norm_rope_append(one, q, k, v, pos, slots, freqs, qw, kw, eps=eps, interleaved=inter, rule=rule, nonfinite=bad)
+            assert int(bad) == 0
+            v[3, 0, 0] = float("nan")
+            fp4.qk_norm_rope_append(one, q, k, v, pos, slots, freqs, qw, kw, eps=eps, interleaved=inter, rule=rule, nonfinite=bad)
+            assert int(bad) == 1
+
+
+def test_no_tokens():
+    fp4 = _fp4()
+    q = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    pos = torch.empty(0, dtype=torch.int32, device="cuda")
+    a, b = fp4.qk_norm_rope(q, q, pos, fp4.rope_frequencies(64))
+    assert a.shape == b.shape == (0, 4, 64)
+
+
+def test_captured_and_on_another_stream():
+    fp4 = _fp4()
+    n, heads, kv, dim, page = 16, 8, 2, 128, 16
+    side = torch.cuda.Stream()
+    cache, want = _cache(fp4, "mxfp8", 4, kv, page, dim), _cache(fp4, "mxfp8", 4, kv, page, dim)
+    whole = _rows(n, heads + 2 * kv, dim, torch.bfloat16, 3)
+    q, k, v = whole.split([heads, kv, kv], 1)
+    pos, slots = torch.zeros(n, dtype=torch.int32, device="cuda"), torch.full((n,), -1, dtype=torch.int64, device="cuda")
+    freqs, w = fp4.rope_frequencies(dim), _weight((dim,), 1)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        fp4.qk_norm_rope_append(cache, q, k, v, pos, slots, freqs, w, w, eps=1e-6)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out = fp4.qk_norm_rope_append(cache, q, k, v, pos, slots, freqs, w, w, eps=1e-6)
+        for i in range(3):
+            whole.copy_(_rows(n, heads + 2 * kv, dim, torch.bfloat16, 20 + i))
+            pos.fill_(100 * i)
+            slots.copy_(torch.randperm(4 * page)[:n])
+            graph.replay()
+            got = fp4.qk_norm_rope_append(want, q, k, v, pos, slots, freqs, w, w, eps=1e-6)
+            side.synchronize()
+            assert torch.equal(out, got)
+            _same(cache, want)
