@@ -53,111 +53,247 @@ __device__ __forceinline__ uint32_t order_of(float f)
 }
 __device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : ~0u)); }
 
+template <int CTRL>
+__device__ __forceinline__ int dpp(int v)
+{
+    return __builtin_amdgcn_mov_dpp(v, CTRL, 0xF, 0xF, false);
+}
+
+// lane ^ M's value; within a row of 16 lanes by DPP
+template <int M>
+__device__ __forceinline__ int lane_xor(int v)
+{
+    if constexpr (M == 1) return dpp<0xB1>(v);
+    else if constexpr (M == 2) return dpp<0x4E>(v);
+    else if constexpr (M == 3) return dpp<0x1B>(v);
+    else if constexpr (M == 7) return dpp<0x141>(v);   // half mirror
+    else if constexpr (M == 4) return dpp<0x1B>(dpp<0x141>(v));
+    else if constexpr (M == 15) return dpp<0x140>(v);  // mirror
+    else if constexpr (M == 8) return dpp<0x128>(v);   // rotation by 8 of 16
+    else return __shfl_xor(v, M, kWave);
+}
+
 // lane i takes lane i - 1's value
 __device__ __forceinline__ int wave_shr1(int v) { return __builtin_amdgcn_mov_dpp(v, 0x138, 0xF, 0xF, false); }
 
-// A part of a row: 64 lanes x NV vectors of 16 bytes.
-template <typename T, int NV>
-__global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a)
+constexpr int kVec = 4;      // 16-byte vectors of a lane in a group
+constexpr int kMost = 8;     // groups of a part, at most
+constexpr int kListed = 64;  // vectors listed before they are looked through
+
+// The k best of a wave so far, best first, in lanes 0 .. k - 1
+struct Best {
+    float v;
+    int i;
+};
+
+// val (uniform) into its place, if it has one: behind what is equal, which came before it
+__device__ __forceinline__ void insert(Best &s, float val, int idx, uint64_t seats, int lane)
+{
+    const uint64_t beaten = __ballot(val > s.v) & seats;
+    if (!beaten) return;
+    const int at = __builtin_ctzll(beaten);
+    const float pv = __int_as_float(wave_shr1(__float_as_int(s.v)));
+    const int pi = wave_shr1(s.i);
+    s.v = lane > at ? pv : lane == at ? val : s.v;
+    s.i = lane > at ? pi : lane == at ? idx : s.i;
+}
+
+__device__ __forceinline__ float lane_of(float v, int lane) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane)); }
+
+// Maximum and sum over a wave, the same in every lane: within rows of 16 lanes by DPP, then the four rows'
+__device__ __forceinline__ float wave_top(float v)
+{
+    v = fmaxf(v, __int_as_float(lane_xor<1>(__float_as_int(v))));
+    v = fmaxf(v, __int_as_float(lane_xor<2>(__float_as_int(v))));
+    v = fmaxf(v, __int_as_float(lane_xor<7>(__float_as_int(v))));
+    v = fmaxf(v, __int_as_float(lane_xor<15>(__float_as_int(v))));
+    return fmaxf(fmaxf(lane_of(v, 0), lane_of(v, 16)), fmaxf(lane_of(v, 32), lane_of(v, 48)));
+}
+
+template <typename Get>
+__device__ __forceinline__ double moved(double v, Get get)
+{
+    uint64_t u;
+    __builtin_memcpy(&u, &v, 8);
+    u = ((uint64_t)(uint32_t)get((int)(u >> 32)) << 32) | (uint32_t)get((int)u);
+    __builtin_memcpy(&v, &u, 8);
+    return v;
+}
+
+__device__ __forceinline__ double wave_sum(double v)
+{
+    v += moved(v, [](int x) { return lane_xor<1>(x); });
+    v += moved(v, [](int x) { return lane_xor<2>(x); });
+    v += moved(v, [](int x) { return lane_xor<7>(x); });
+    v += moved(v, [](int x) { return lane_xor<15>(x); });
+    auto row = [&](int r) { return moved(v, [r](int x) { return __builtin_amdgcn_readlane(x, r); }); };
+    return (row(0) + row(16)) + (row(32) + row(48));
+}
+
+// A group of vectors from token e0 on.  Vectors begin at multiples of kPer tokens whatever the row's address
+// (unaligned 16-byte loads), so that equal rows have equal sums and their ties go to the lowest beam.
+template <typename T>
+__device__ __forceinline__ void load_group(uint32_t (&w)[kVec][4], const T *x, int e0, int vocab, int lane)
 {
     constexpr int kPer = Row<T>::kPer;
-    const float kInf = __builtin_inff();
-    const int64_t id = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (id >= (int64_t)a.batch * a.beams * a.parts) return;
-    const int row = (int)(id / a.parts), part = (int)(id - (int64_t)row * a.parts), lane = threadIdx.x & 63;
-    if (a.done && a.done[row]) return;
-    const T *x = reinterpret_cast<const T *>(a.logits) + row * a.ld;
-    // Vectors begin at multiples of kPer tokens whatever the row's address (unaligned 16-byte loads): so
-    // equal rows have equal sums, and their ties go to the lowest beam.
-    const int first = part * (64 * NV * kPer);
-    uint32_t w[NV][4];
+    int e = e0 + lane * kPer;
+    if (e0 + kVec * 64 * kPer <= vocab) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int e = first + (v * 64 + lane) * kPer;
-        if (e + kPer <= a.vocab) {
+        for (int v = 0; v < kVec; ++v) __builtin_memcpy(w[v], x + e + v * 64 * kPer, 16);
+        return;
+    }
+#pragma unroll
+    for (int v = 0; v < kVec; ++v, e += 64 * kPer) {
+        if (e + kPer <= vocab) {
             __builtin_memcpy(w[v], x + e, 16);
         } else {
             w[v][0] = w[v][1] = w[v][2] = w[v][3] = Row<T>::kNone;
 #pragma unroll
             for (int j = 0; j < kPer; ++j)
-                if (e + j < a.vocab) Row<T>::put(w[v], j, x[e + j]);
+                if (e + j < vocab) Row<T>::put(w[v], j, x[e + j]);
         }
     }
+}
 
-    // maxima: of each vector, the lane, the part.  NaN is passed over here and spoils the sum below.
-    float vmax[NV], lmax = -kInf;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        float m = -kInf;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) m = fmaxf(m, Row<T>::get(w[v], j));
-        vmax[v] = m;
-        lmax = fmaxf(lmax, m);
-    }
-    float top = lmax;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
+template <typename T>
+__device__ __forceinline__ float widen(T v)
+{
+    if constexpr (sizeof(T) == 2) return __uint_as_float((uint32_t)v << 16);
+    else return v;
+}
 
-    // sum of exponentials against the part's maximum
-    const float ref = top == -kInf ? 0.0f : top;
+// A wave walks over a part of a row, a.groups groups, the next group's loads in flight.
+//
+// First pass: sums of exponentials, and every vector's maximum into LDS.  The k-th largest of the lanes'
+// maxima is then a bar that at least k values reach and all of the k best do.  Second pass: the vectors whose
+// maximum reaches it (about k of them) are listed and read again, and their values put in their places one at a
+// time, the bar rising.
+template <typename T>
+__global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a)
+{
+    constexpr int kPer = Row<T>::kPer, kGroup = kVec * 64 * kPer;
+    constexpr float kLowest = -3.4028234663852886e38f;
+    const float kInf = __builtin_inff();
+    __shared__ float4 sm_top[4][kMost][64];
+    __shared__ int sm_listed[4][kListed + kVec * 64];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int64_t id = (int64_t)blockIdx.x * 4 + wave;
+    if (id >= (int64_t)a.batch * a.beams * a.parts) return;
+    const int row = (int)(id / a.parts), part = (int)(id - (int64_t)row * a.parts);
+    if (a.done && a.done[row]) return;
+    const T *x = reinterpret_cast<const T *>(a.logits) + row * a.ld;
+    const int first = part * a.groups * kGroup;
+    const int groups = min(a.groups, (a.vocab - first + kGroup - 1) / kGroup);
+    uint32_t w[kVec][4];
+    load_group(w, x, first, a.vocab, lane);
+
+    // Exponentials are taken against the first group's maximum `ref` until one would be e^80 times as large.
+    // (2^(x log2e - c) is one instruction less a value, but then not even the largest term is exact.)
+    float top = -kInf;  // NaN is passed over here and spoils the sum
+#pragma unroll
+    for (int v = 0; v < kVec; ++v)
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) top = fmaxf(top, Row<T>::get(w[v], j));
+    float ref = fmaxf(wave_top(top), kLowest);
     double sum = 0.0;
+    for (int g = 0; g < groups; ++g) {
+        uint32_t next[kVec][4];
+        if (g + 1 < groups) load_group(next, x, first + (g + 1) * kGroup, a.vocab, lane);
+        float m[kVec];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        float e[kPer];
+        for (int v = 0; v < kVec; ++v) {
+            m[v] = -kInf;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) e[j] = __builtin_amdgcn_exp2f((Row<T>::get(w[v], j) - ref) * kLog2e);
+            for (int j = 0; j < kPer; ++j) m[v] = fmaxf(m[v], Row<T>::get(w[v], j));
+        }
+        sm_top[wave][g][lane] = make_float4(m[0], m[1], m[2], m[3]);
+        const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+        top = fmaxf(top, most);
+        if (__ballot(most - ref > 80.0f)) {
+            const float now = wave_top(most);
+            sum *= exp((double)ref - (double)now);
+            ref = now;
+        }
+        float part_sum = 0.0f;
 #pragma unroll
-        for (int d = kPer / 2; d > 0; d >>= 1)
+        for (int v = 0; v < kVec; ++v) {
+            float f[kPer];
 #pragma unroll
-            for (int j = 0; j < d; ++j) e[j] += e[j + d];
-        sum += (double)e[0];
+            for (int j = 0; j < kPer; ++j) f[j] = __builtin_amdgcn_exp2f((Row<T>::get(w[v], j) - ref) * kLog2e);
+#pragma unroll
+            for (int d = kPer / 2; d > 0; d >>= 1)
+#pragma unroll
+                for (int j = 0; j < d; ++j) f[j] += f[j + d];
+            part_sum += f[0];
+        }
+        sum += (double)part_sum;
+#pragma unroll
+        for (int v = 0; v < kVec; ++v)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) w[v][c] = next[v][c];
     }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, kWave);
+    sum = wave_sum(sum);
     if (lane == 0) {
-        a.part_top[id] = top;
+        a.part_top[id] = ref;
         a.part_sum[id] = sum;
     }
 
-    // The k-th largest of the lanes' maxima: at least k values reach it, and no smaller one is among the
-    // k best.  Found bit by bit from the top, by counting lanes.
-    const uint32_t key = order_of(lmax) >> Row<T>::kKeyShift;
+    // the bar, bit by bit from the top, by counting lanes; what counts is above it
+    const uint32_t key = order_of(top) >> Row<T>::kKeyShift;
     uint32_t t = 0;
     for (int b = 31 - Row<T>::kKeyShift; b >= 0; --b) {
         const uint32_t c = t | (1u << b);
         if (__builtin_popcountll(__ballot(key >= c)) >= a.k) t = c;
     }
-    const float bar = __uint_as_float(__float_as_uint(value_of(t << Row<T>::kKeyShift)) & (~0u << Row<T>::kKeyShift));
+    float bar = __uint_as_float(__float_as_uint(value_of(t << Row<T>::kKeyShift)) & (~0u << Row<T>::kKeyShift));
+    if (bar > -kInf) bar = bar == 0.0f ? -0x1p-149f : value_of(order_of(bar) - 1);
 
-    // the k best in lanes 0 .. k - 1, best first: what reaches the bar is put in its place, one at a time
-    float lv = -kInf;
-    int li = 0x7FFFFFFF;
+    Best s{-kInf, 0x7FFFFFFF};
     const uint64_t seats = ~0ull >> (64 - a.k);
+    int *listed = sm_listed[wave], n = 0;
+    // the listed vectors, 64 / kPer at a time, a value a lane, in the order of the tokens; four such loads in flight
+    auto look = [&]() {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        constexpr int kOnce = 64 / kPer;
+        for (int i0 = 0; i0 < n; i0 += 4 * kOnce) {
+            float f[4];
+            int at[4];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        if (!__ballot(vmax[v] >= bar && vmax[v] > -kInf)) continue;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const float f = Row<T>::get(w[v], j);
-            uint64_t hit = __ballot(f >= bar && f > -kInf);
-            while (hit) {
-                const int l = __builtin_ctzll(hit);
-                hit &= hit - 1;
-                const float val = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f), l));
-                const int idx = first + (v * 64 + l) * kPer + j;
-                const uint64_t beaten = __ballot(val > lv || (val == lv && idx < li)) & seats;
-                if (!beaten) continue;
-                const int at = __builtin_ctzll(beaten);
-                const float pv = __int_as_float(wave_shr1(__float_as_int(lv)));
-                const int pi = wave_shr1(li);
-                lv = lane > at ? pv : lane == at ? val : lv;
-                li = lane > at ? pi : lane == at ? idx : li;
+            for (int c = 0; c < 4; ++c) {
+                const int i = i0 + c * kOnce + lane / kPer;
+                at[c] = i < n ? listed[i] + lane % kPer : a.vocab;
+                f[c] = at[c] < a.vocab ? widen(x[at[c]]) : -kInf;
             }
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                for (uint64_t in = __ballot(f[c] > bar); in; in &= in - 1) {
+                    const int l = __builtin_ctzll(in);
+                    insert(s, lane_of(f[c], l), __builtin_amdgcn_readlane(at[c], l), seats, lane);
+                    bar = fmaxf(bar, lane_of(s.v, a.k - 1));
+                }
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        n = 0;
+    };
+    for (int g = 0; g < groups; ++g) {
+        const float4 q = sm_top[wave][g][lane];
+        const float m[kVec] = {q.x, q.y, q.z, q.w};
+        uint64_t hit[kVec];
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) hit[v] = __ballot(m[v] > bar);
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) {
+            if (!hit[v]) continue;
+            if ((hit[v] >> lane) & 1ull)
+                listed[n + __builtin_popcountll(hit[v] & ((1ull << lane) - 1))] = first + g * kGroup + (v * 64 + lane) * kPer;
+            n += __builtin_popcountll(hit[v]);
+        }
+        if (n >= kListed) look();
     }
+    look();
     if (lane < a.k) {
-        a.part_value[id * a.k + lane] = lv;
-        a.part_token[id * a.k + lane] = li;
+        a.part_value[id * a.k + lane] = s.v;
+        a.part_token[id * a.k + lane] = s.i;
     }
 }
 
@@ -173,132 +309,155 @@ __device__ __forceinline__ bool better(const Entry &x, const Entry &y)
     return x.total > y.total || (x.total == y.total && x.flat < y.flat);
 }
 
-__device__ __forceinline__ Entry lane_xor(const Entry &x, int mask)
+template <int M>
+__device__ __forceinline__ Entry lane_xor(const Entry &x)
 {
-    return Entry{__shfl_xor(x.total, mask, kWave), (uint32_t)__shfl_xor((int)x.flat, mask, kWave)};
+    return Entry{moved(x.total, [](int v) { return lane_xor<M>(v); }), (uint32_t)lane_xor<M>((int)x.flat)};
 }
 
-// x: a bitonic run of `kp` lanes -> sorted, best first
-__device__ __forceinline__ Entry settle(Entry x, int kp, int lane)
+// x: a bitonic run of 2 D lanes -> sorted, best first
+template <int D>
+__device__ __forceinline__ void settle(Entry &x, int lane)
 {
-    for (int d = kp >> 1; d > 0; d >>= 1) {
-        const Entry y = lane_xor(x, d);
-        const bool swap = (lane & d) ? better(x, y) : better(y, x);
-        if (swap) x = y;
-    }
-    return x;
+    const Entry y = lane_xor<D>(x);
+    if ((lane & D) ? better(x, y) : better(y, x)) x = y;
+    if constexpr (D > 1) settle<D / 2>(x, lane);
 }
 
-// sorted runs x and y (the same lanes): the best of both, sorted.  Against the reverse of y, the better of
-// each pair are the kp best, and form a bitonic run.
-__device__ __forceinline__ Entry merge(Entry x, const Entry &y, int kp, int lane)
+// Sorted runs x and y of KP lanes: the best of both, sorted.  Against the reverse of y, the better of each
+// pair are the KP best, and form a bitonic run.
+template <int KP>
+__device__ __forceinline__ void merge(Entry &x, const Entry &y, int lane)
 {
-    const Entry z = lane_xor(y, kp - 1);
+    const Entry z = lane_xor<KP - 1>(y);
     if (better(z, x)) x = z;
-    return settle(x, kp, lane);
+    settle<KP / 2>(x, lane);
 }
 
-// all runs of a wave into the one of lanes 0 .. kp - 1 (every run ends up the same)
-__device__ __forceinline__ Entry merge_wave(Entry x, int kp, int lane)
+// all runs of a wave into one (every run ends up as it), H lanes of them done
+template <int KP, int H>
+__device__ __forceinline__ void merge_wave(Entry &x, int lane)
 {
-    for (int h = kp; h < 64; h <<= 1) {
-        const Entry z = lane_xor(x, h | (kp - 1));
+    if constexpr (H < 64) {
+        const Entry z = lane_xor<(H | (KP - 1))>(x);
         if (better(z, x)) x = z;
-        x = settle(x, kp, lane);
+        settle<KP / 2>(x, lane);
+        merge_wave<KP, 2 * H>(x, lane);
     }
-    return x;
 }
 
-// One workgroup a group of beams
-__global__ __launch_bounds__(1024) void k_beam_join(BeamArgs a, int kp)
+// One workgroup a group of beams; lists of KP places, a.k of them in use
+template <int KP>
+__global__ __launch_bounds__(1024) void k_beam_join(BeamArgs a)
 {
     __shared__ double base[64];
-    __shared__ double sm_total[16 * 64];
-    __shared__ uint32_t sm_flat[16 * 64];
+    __shared__ Entry found[16][KP];
     const double kInf = __builtin_inf();
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     const int row0 = (int)blockIdx.x * a.beams;
-    // score - log of the whole row's sum
+    constexpr int kPer = 64 / KP;
+    const int lists = a.beams * a.parts, slot = lane & (KP - 1);
+
+    // One list place; of an ended beam the first one stands for its own score (+0).  What an ended beam's rows
+    // hold in the workspace is old, and not used.  All loads are issued before any is waited for, here and
+    // below: the data comes from the other chiplets' caches, and a wait costs more than the arithmetic.
+    auto load = [&](int l, float &v, uint32_t &token, int &beam) {
+        const bool is = l < lists && slot < a.k;
+        beam = is ? l / a.parts : 0;
+        const int64_t at = is ? ((int64_t)row0 * a.parts + l) * a.k + slot : 0;
+        const uint8_t ended = a.done ? a.done[row0 + beam] : 0;
+        v = a.part_value[at];
+        token = (uint32_t)a.part_token[at];
+        if (ended) {
+            v = l == beam * a.parts && slot == 0 ? 0.0f : -__builtin_inff();
+            token = (uint32_t)a.end_token;
+        }
+        if (!is) v = -__builtin_inff();
+    };
+    float v;
+    uint32_t token;
+    int beam;
+    load(wave * kPer + lane / KP, v, token, beam);
+
+    // score - log of the whole row's sum; an ended beam's score
     for (int i = wave; i < a.beams; i += waves) {
         const int row = row0 + i;
+        const int64_t at = (int64_t)row * a.parts;
+        const uint8_t ended = a.done ? a.done[row] : 0;
         double b = (double)a.scores[row];
-        if (!(a.done && a.done[row])) {
-            float top = -__builtin_inff();
-            for (int p = lane; p < a.parts; p += 64) top = fmaxf(top, a.part_top[(int64_t)row * a.parts + p]);
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
-            double sum = 0.0;
-            for (int p = lane; p < a.parts; p += 64) {
-                const float t = a.part_top[(int64_t)row * a.parts + p];
-                const double s = a.part_sum[(int64_t)row * a.parts + p];
-                sum += t == -__builtin_inff() ? s : s * exp((double)t - (double)top);
-            }
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, kWave);
-            b -= (double)top + log(sum);
+        float top = -__builtin_inff();
+        double sum = 0.0;
+        for (int p0 = 0; p0 < a.parts; p0 += 64) {
+            const int p = p0 + lane;
+            const float t = p < a.parts ? a.part_top[at + p] : -__builtin_inff();
+            const double u = p < a.parts ? a.part_sum[at + p] : 0.0;
+            const float now = fmaxf(top, wave_top(t));
+            // e^d <= 1 by v_exp_f32: its argument's rounding, 2^-24 |d|, weighs e^d
+            auto share = [&](float x) { return (double)__builtin_amdgcn_exp2f((float)(((double)x - (double)now) * 1.4426950408889634)); };
+            sum = (top == -__builtin_inff() ? 0.0 : sum * share(top)) + (p < a.parts ? u * share(t) : 0.0);
+            top = now;
         }
+        if (!ended) b -= (double)top + log(wave_sum(sum));
         if (lane == 0) base[i] = b;
     }
     __syncthreads();
 
-    // lists of kp (k of them real), 64 / kp of them a wave and step
-    const int lists = a.beams * a.parts, per = 64 / kp, slot = lane & (kp - 1);
     Entry best{-kInf, ~0u};
-    for (int l0 = wave * per; l0 < lists; l0 += waves * per) {
-        const int l = l0 + lane / kp;
+    for (int l0 = wave * kPer; l0 < lists; l0 += waves * kPer) {
+        if (l0 != wave * kPer) load(l0 + lane / KP, v, token, beam);
         Entry e{-kInf, ~0u};
-        if (l < lists && slot < a.k) {
-            const int i = l / a.parts, row = row0 + i;
-            const int64_t at = ((int64_t)row0 * a.parts + l) * a.k + slot;
-            if (a.done && a.done[row]) {
-                if (l == i * a.parts && slot == 0) e = Entry{base[i], (uint32_t)i * (uint32_t)a.vocab + (uint32_t)a.end_token};
-            } else {
-                const float v = a.part_value[at];
-                if (v > -__builtin_inff()) e = Entry{base[i] + (double)v, (uint32_t)i * (uint32_t)a.vocab + (uint32_t)a.part_token[at]};
-            }
-            if (!(e.total > -kInf)) e = Entry{-kInf, ~0u};  // NaN too
+        if (v > -__builtin_inff()) {
+            const double total = base[beam] + (double)v;
+            if (total > -kInf) e = Entry{total, (uint32_t)beam * (uint32_t)a.vocab + token};  // (NaN is not)
         }
-        best = merge(best, e, kp, lane);
+        if (l0 == wave * kPer) best = e;
+        else merge<KP>(best, e, lane);
     }
-    best = merge_wave(best, kp, lane);
+    merge_wave<KP, KP>(best, lane);
     if (waves > 1) {
-        if (lane < kp) {
-            sm_total[wave * kp + lane] = best.total;
-            sm_flat[wave * kp + lane] = best.flat;
-        }
+        if (lane < KP) found[wave][lane] = best;
         __syncthreads();
         if (wave > 0) return;
-        best = Entry{-kInf, ~0u};
-        for (int w0 = 0; w0 < waves; w0 += per) {
-            Entry e{-kInf, ~0u};
-            const int w = w0 + lane / kp;
-            if (w < waves) e = Entry{sm_total[w * kp + slot], sm_flat[w * kp + slot]};
-            best = merge(best, e, kp, lane);
+        for (int w = lane / KP; w - lane / KP < waves; w += kPer) {
+            const Entry e = w < waves ? found[w][slot] : Entry{-kInf, ~0u};
+            if (w < kPer) best = e;
+            else merge<KP>(best, e, lane);
         }
-        best = merge_wave(best, kp, lane);
+        merge_wave<KP, KP>(best, lane);
     }
-    if (wave == 0 && lane < a.k) {
+    if (lane < a.k) {
         const int64_t at = (int64_t)blockIdx.x * a.k + lane;
         const bool real = best.flat != ~0u;
-        const uint32_t beam = real ? best.flat / (uint32_t)a.vocab : (uint32_t)min(lane, a.beams - 1);
+        const uint32_t i = real ? best.flat / (uint32_t)a.vocab : (uint32_t)min(lane, a.beams - 1);
         a.out_scores[at] = (float)best.total;
-        a.out_parents[at] = (int32_t)beam;
-        a.out_tokens[at] = real ? (int32_t)(best.flat - beam * (uint32_t)a.vocab) : -1;
+        a.out_parents[at] = (int32_t)i;
+        a.out_tokens[at] = real ? (int32_t)(best.flat - i * (uint32_t)a.vocab) : -1;
     }
 }
 
-// Vectors a lane: 16 where that still gives the chip its waves, else 4, so that a few rows spread over it
-int vectors(int64_t rows, int64_t vocab, fp4_dtype xt)
+// a wave a list step and a beam, up to 16
+template <int KP>
+void launch_join(const BeamArgs &a, int64_t lists, hipStream_t st)
 {
-    const int64_t part = 64 * 16 * (xt == FP4_BF16 ? 8 : 4);
-    return rows * ((vocab + part - 1) / part) >= 2048 ? 16 : 4;
+    const int64_t steps = (lists + 64 / KP - 1) / (64 / KP), most = steps > a.beams ? steps : a.beams;
+    int waves = 1;
+    while (waves < most && waves < 16) waves <<= 1;
+    hipLaunchKernelGGL(k_beam_join<KP>, dim3((unsigned)a.batch), dim3(64 * waves), 0, st, a);
+}
+
+// Groups of a part: as many as leave the chip four waves a SIMD
+int groups_of(int64_t rows, int64_t vocab, fp4_dtype xt)
+{
+    const int64_t group = kVec * 64 * (xt == FP4_BF16 ? 8 : 4);
+    const int64_t all = rows * ((vocab + group - 1) / group) / (16 * device_cu_count());
+    return all < 1 ? 1 : all > kMost ? kMost : (int)all;
 }
 
 }  // namespace
 
 int64_t beam_parts(int64_t rows, int64_t vocab, fp4_dtype xt)
 {
-    const int64_t part = 64 * (xt == FP4_BF16 ? 8 : 4) * vectors(rows, vocab, xt);
+    const int64_t part = kVec * 64 * (xt == FP4_BF16 ? 8 : 4) * groups_of(rows, vocab, xt);
     return (vocab + part - 1) / part;
 }
 
@@ -306,20 +465,16 @@ fp4_status launch_beam_select(BeamArgs a, fp4_dtype xt, hipStream_t st)
 {
     const int64_t rows = (int64_t)a.batch * a.beams;
     a.parts = (int)beam_parts(rows, a.vocab, xt);
-    const int nv = vectors(rows, a.vocab, xt);
+    a.groups = groups_of(rows, a.vocab, xt);
     const dim3 grid((unsigned)((rows * a.parts + 3) / 4));
-    if (xt == FP4_BF16) {
-        if (nv == 16) hipLaunchKernelGGL((k_beam_rows<uint16_t, 16>), grid, dim3(256), 0, st, a);
-        else hipLaunchKernelGGL((k_beam_rows<uint16_t, 4>), grid, dim3(256), 0, st, a);
-    } else {
-        if (nv == 16) hipLaunchKernelGGL((k_beam_rows<float, 16>), grid, dim3(256), 0, st, a);
-        else hipLaunchKernelGGL((k_beam_rows<float, 4>), grid, dim3(256), 0, st, a);
-    }
-    int kp = 1;
-    while (kp < a.k) kp <<= 1;
-    const int64_t steps = ((int64_t)a.beams * a.parts * kp + 63) / 64;  // of one wave
-    const int waves = steps >= 32 ? 16 : steps >= 8 ? 4 : 1;
-    hipLaunchKernelGGL(k_beam_join, dim3((unsigned)a.batch), dim3(64 * waves), 0, st, a, kp);
+    if (xt == FP4_BF16) hipLaunchKernelGGL(k_beam_rows<uint16_t>, grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL(k_beam_rows<float>, grid, dim3(256), 0, st, a);
+    const int64_t lists = (int64_t)a.beams * a.parts;
+    if (a.k <= 4) launch_join<4>(a, lists, st);
+    else if (a.k <= 8) launch_join<8>(a, lists, st);
+    else if (a.k <= 16) launch_join<16>(a, lists, st);
+    else if (a.k <= 32) launch_join<32>(a, lists, st);
+    else launch_join<64>(a, lists, st);
     return hipGetLastError() == hipSuccess ? FP4_OK : FP4_ERR_HIP;
 }
 

@@ -290,7 +290,7 @@ struct BeamArgs {
     const float *scores;
     const uint8_t *done;
     int batch, beams, vocab, k, end_token;
-    int parts;            // of a row (set by the launcher)
+    int parts, groups;    // of a row, of a part (set by the launcher)
     double *part_sum;     // [row][part]
     float *part_top;
     float *part_value;    // [row][part][k], best first
