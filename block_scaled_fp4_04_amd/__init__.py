@@ -197,8 +197,9 @@ def prepare(thunk, *keep) -> Prepared:
 
 
 def _stream() -> int:
-    """The current device's current stream (its handle, without a Stream object around it)."""
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    """The current device's current stream (its handle, without a Stream object around it).  Calls come
+    here with device tensors in hand, so the device runtime is up."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _ptr(t):
@@ -1090,9 +1091,9 @@ _BF16 = (torch.bfloat16,)
 
 
 def _i32_vec(t: torch.Tensor, n: int, what: str):
-    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
-        if t.dtype != torch.int32:
-            raise TypeError(f"{what} must be int32, got {t.dtype}")
+    if t.dtype != torch.int32:
+        raise TypeError(f"{what} must be int32, got {t.dtype}")
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous vector of {n} element(s), got {tuple(t.shape)}")
 
 
@@ -1100,7 +1101,7 @@ def _out_heads(out, n: int, h: int, d: int, dtype, like, what="out"):
     """(output, token stride, head stride): allocated when None, else checked."""
     if out is None:
         _out_dt(dtype)
-        return torch.empty((n, h, d), dtype=dtype, device=like.device), h * d, d
+        return torch.empty(n, h, d, dtype=dtype, device=like.device), h * d, d
     on, oh, od, st, sh = _heads(out, _F32_BF16, what)
     if (on, oh, od) != (n, h, d):
         raise ValueError(f"{what} has shape {tuple(out.shape)}, expected {(n, h, d)}")
@@ -1261,6 +1262,17 @@ def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q
 
 # ------------------------------------------------- around the attention ---
 
+def _elsewhere(t: torch.Tensor):
+    """None where t's device is the current one (or t is on the host, which later checks refuse); else the
+    context in which the call has to be made, since the library launches on the current device."""
+    dev = t.get_device()
+    if dev < 0 or dev == torch._C._cuda_getDevice():
+        return None
+    if _recording is not None:
+        raise ValueError("prepare() records calls on the current device only")
+    return torch.cuda.device(dev)
+
+
 def rope_frequencies(rot: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
     """The usual angles per position, base ** (-2 i / rot): float64 [rot / 2], made once."""
     return float(base) ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / max(rot, 1))
@@ -1270,9 +1282,12 @@ def _head_weight(w, heads: int, dim: int, what: str) -> int:
     """The head stride of a norm's weight: float32 [dim] (0) or [heads, dim]."""
     if w.dtype != torch.float32:
         raise TypeError(f"{what} must be float32, got {w.dtype}")
-    if not w.is_contiguous() or (tuple(w.shape) != (dim,) and tuple(w.shape) != (heads, dim)):
-        raise ValueError(f"{what} must be a contiguous [{dim}] or [{heads}, {dim}], got {tuple(w.shape)}")
-    return 0 if w.dim() == 1 else dim
+    if w.is_contiguous():
+        if w.shape == (dim,):
+            return 0
+        if w.shape == (heads, dim):
+            return dim
+    raise ValueError(f"{what} must be a contiguous [{dim}] or [{heads}, {dim}], got {tuple(w.shape)}")
 
 
 def _norm_args(n, q_heads, k_heads, d, positions, freqs, q_weight, k_weight, eps):
@@ -1313,6 +1328,9 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tenso
     rotated by positions (int32 [tokens]) times freqs (float64, `rope_frequencies`; None: not):
     value i with i + rot / 2, or neighbours when `interleaved`.  q_out and k_out may be q and k.
     Returns (q_out, k_out)."""
+    if (there := _elsewhere(q)) is not None:
+        with there:
+            return qk_norm_rope(q, k, positions, freqs, q_weight, k_weight, eps, interleaved, dtype, q_out, k_out)
     n, h, d, qt, qh = _heads(q, _F32_BF16, "q")
     hk = kt = kh = kot = koh = 0
     if k is not None:
@@ -1344,6 +1362,10 @@ def qk_norm_rope_append(cache: KVCache, q: torch.Tensor, k: torch.Tensor, v: tor
                         q_out: torch.Tensor | None = None) -> torch.Tensor:
     """qk_norm_rope with the keys, and v as it is, quantized into the cache at `slots` as
     kv_cache_append does (the keys from fp32, not from rows rounded before).  Returns q_out."""
+    if (there := _elsewhere(cache.k_codes)) is not None:
+        with there:
+            return qk_norm_rope_append(cache, q, k, v, positions, slots, freqs, q_weight, k_weight, eps, interleaved, rule, nonfinite,
+                                       dtype, q_out)
     n, h, d, qt, qh = _heads(q, _F32_BF16, "q")
     nk, hk, dk, kt, kh = _heads(k, _F32_BF16, "k")
     nv, hv, dv, vt, vh = _heads(v, _F32_BF16, "v")
@@ -1428,18 +1450,24 @@ def kv_pages_extend(pages: KVPages, block_table: torch.Tensor, seq_lens: torch.T
     caller, so that nothing waits for the device).  in_place: seq_lens and the pool's state become
     those after the call; else the plan holds new ones.  A sequence that cannot be served whole is
     left as it is: its slots are -1 and state[1] counts it.  `out`: a plan of the same sizes to write into."""
+    if (there := _elsewhere(block_table)) is not None:
+        with there:
+            return kv_pages_extend(pages, block_table, seq_lens, new_lens, tokens, in_place, offsets, out, workspace)
     seqs, width, stride = _block_table(block_table)
     _i32_vec(seq_lens, seqs, "seq_lens")
     _i32_vec(new_lens, seqs, "new_lens")
     tokens = int(tokens)
+    if tokens < 0:
+        raise ValueError(f"tokens must not be negative, got {tokens}")
+    need = lib().kv_pages_extend_workspace(seqs, tokens)
     if out is None:
-        if tokens < 0:
-            raise ValueError(f"tokens must not be negative, got {tokens}")
-        dev = block_table.device
-        cu = torch.empty((2, seqs + 1), dtype=torch.int32, device=dev).unbind(0) if offsets else (None, None)
-        out = KVPlan(torch.empty(tokens, dtype=torch.int64, device=dev), torch.empty(tokens, dtype=torch.int32, device=dev), *cu,
-                     seq_lens if in_place else torch.empty_like(seq_lens),
-                     pages.state if in_place else torch.empty_like(pages.state))
+        # one allocation: workspace, slots, positions, offsets, lengths, state
+        room = need // 4 if workspace is None else 0
+        parts = torch.empty(room + 3 * tokens + 3 * seqs + 4, dtype=torch.int32, device=block_table.device).split_with_sizes(
+            (room, 2 * tokens, tokens, seqs + 1, seqs + 1, seqs, 2))
+        out = KVPlan(parts[1].view(torch.int64), parts[2], *(parts[3:5] if offsets else (None, None)),
+                     *((seq_lens, pages.state) if in_place else parts[5:]))
+        space = parts[0]
     else:
         if out.slots.dtype != torch.int64 or out.slots.shape != (tokens,) or not out.slots.is_contiguous():
             raise ValueError(f"out.slots must be a contiguous int64 tensor of {tokens} element(s)")
@@ -1449,14 +1477,14 @@ def kv_pages_extend(pages: KVPages, block_table: torch.Tensor, seq_lens: torch.T
                 _i32_vec(x, seqs + 1, name)
         _i32_vec(out.seq_lens, seqs, "out.seq_lens")
         _i32_vec(out.state, 2, "out.state")
-    need = lib().kv_pages_extend_workspace(seqs, tokens)
-    if need or workspace is not None:
-        workspace = _workspace(workspace, need, block_table)
+        space = workspace
+    if workspace is not None or (need and space is None):
+        space = _workspace(workspace, need, block_table)
     _need_cuda(pages.free, block_table, seq_lens, new_lens, out.slots, out.positions, out.cu_q, out.cu_k, out.seq_lens,
-               out.state, workspace)
+               out.state, space)
     _run(lib().kv_pages_extend, _pool(pages), _ptr(block_table), seqs, width, stride, _ptr(seq_lens), _ptr(new_lens),
          tokens, _ptr(out.seq_lens), _ptr(out.state), _ptr(out.slots), _ptr(out.positions), _ptr(out.cu_q),
-         _ptr(out.cu_k), _ptr(workspace), need, _stream())
+         _ptr(out.cu_k), _ptr(space), need, _stream())
     return out
 
 
@@ -1469,6 +1497,9 @@ def kv_pages_collect(pages: KVPages, block_table: torch.Tensor, seq_lens: torch.
                      workspace: torch.Tensor | None = None) -> KVPages:
     """The pool's free list anew: every page that no row of the block table holds within its
     length, in ascending order.  A sequence that ended gives its pages back by a length of 0."""
+    if (there := _elsewhere(block_table)) is not None:
+        with there:
+            return kv_pages_collect(pages, block_table, seq_lens, workspace)
     seqs, width, stride = _block_table(block_table)
     _i32_vec(seq_lens, seqs, "seq_lens")
     need = lib().kv_pages_collect_workspace(pages.pages, seqs, width)
@@ -1486,6 +1517,9 @@ def kv_pages_reorder(block_table: torch.Tensor, seq_lens: torch.Tensor, parents:
     j of a group takes the row of beam parents[j], in place or into `out`.  The rows of a group have
     the same length.  Returns int32 [batch * beams, 3]: what kv_cache_copy has to copy in every layer's cache,
     because a partly filled page belongs to one row only."""
+    if (there := _elsewhere(block_table)) is not None:
+        with there:
+            return kv_pages_reorder(block_table, seq_lens, parents, page_size, out, copies)
     seqs, width, stride = _block_table(block_table)
     if parents.dtype != torch.int32:
         raise TypeError(f"parents must be int32, got {parents.dtype}")
@@ -1501,7 +1535,7 @@ def kv_pages_reorder(block_table: torch.Tensor, seq_lens: torch.Tensor, parents:
         if (oseqs, owidth) != (seqs, width):
             raise ValueError(f"out has shape {tuple(out.shape)}, expected {(seqs, width)}")
     if copies is None:
-        copies = torch.empty((seqs, 3), dtype=torch.int32, device=block_table.device)
+        copies = torch.empty(seqs, 3, dtype=torch.int32, device=block_table.device)
     else:
         _copies(copies)
         _shape(copies, (seqs, 3), "copies")
@@ -1522,6 +1556,9 @@ def kv_cache_copy(cache: KVCache, copies: torch.Tensor) -> KVCache:
     """For each row (source page, destination page, tokens) of copies int32 [n, 3] the first `tokens`
     tokens of the source page are copied into the destination page (all heads, keys and values); rows
     with a negative page are skipped."""
+    if (there := _elsewhere(copies)) is not None:
+        with there:
+            return kv_cache_copy(cache, copies)
     _copies(copies)
     _need_cuda(cache.k_codes, copies)
     _run(lib().kv_cache_copy, _kv(cache), _ptr(copies), copies.shape[0], _stream())
@@ -1539,6 +1576,9 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: int | None = None
     nothing), done bool or uint8 [batch, beams] (the beam has ended and offers end_token at its own
     score).  Returns (scores float32, parents int32, tokens int32), each [batch, k], best first, ties to the lowest
     beam, then token.  Places that are left: -inf, min(place, beams - 1), -1."""
+    if (there := _elsewhere(logits)) is not None:
+        with there:
+            return beam_select(logits, scores, k, done, end_token, out, workspace)
     dt = _dt(logits)
     if logits.dim() != 2:
         raise ValueError(f"logits must be [batch * beams, vocab], got {tuple(logits.shape)}")
@@ -1563,9 +1603,8 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: int | None = None
     if out is None:
         if not 1 <= k <= 64:
             raise ValueError(f"k must be in [1, 64], got {k}")
-        dev = logits.device
-        out = (torch.empty((batch, k), dtype=torch.float32, device=dev), torch.empty((batch, k), dtype=torch.int32, device=dev),
-               torch.empty((batch, k), dtype=torch.int32, device=dev))
+        parts = torch.empty(3, batch, k, dtype=torch.int32, device=logits.device).unbind(0)
+        out = (parts[0].view(torch.float32), parts[1], parts[2])
     else:
         for t, d, name in zip(out, (torch.float32, torch.int32, torch.int32), ("scores", "parents", "tokens"), strict=True):
             if t.dtype != d or not t.is_contiguous():

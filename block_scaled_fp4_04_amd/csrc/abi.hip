@@ -20,6 +20,9 @@ fp4_status check_device()
 {
     int dev = 0;
     int count = 0;
+    if (hipGetDevice(&dev) == hipSuccess && dev >= 0 && dev < kMaxDevices &&
+        g_dev_state[dev].load(std::memory_order_relaxed) == 1)
+        return FP4_OK;  // seen before
     if (hipGetDeviceCount(&count) != hipSuccess || count <= 0) {
         (void)hipGetLastError();
         return FP4_ERR_NO_DEVICE;
@@ -1259,7 +1262,6 @@ HeadNormArgs norm_args(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t 
     a.tokens = tokens;
     a.heads = (int)heads;
     a.kv_heads = (int)kv_heads;
-    a.rows = (int)(heads + kv_heads);
     a.dim = (int)dim;
     a.rot = (int)rot;
     a.interleaved = interleaved;
@@ -1400,7 +1402,6 @@ fp4_status qk_norm_rope_append(const fp4_kv_cache *cache, const void *q, const v
     FP4_TRY(check_device());
     HeadNormArgs a = norm_args(tokens, heads, cache->kv_heads, dim, q_weight, k_weight, q_weight_stride, k_weight_stride, eps,
                                positions, freqs, rot, interleaved);
-    a.rows += (int)cache->kv_heads;
     set_rows(a, 0, q, {q_token_stride, q_head_stride});
     set_rows(a, 1, k, {k_token_stride, k_head_stride});
     set_rows(a, 2, v, {v_token_stride, v_head_stride});

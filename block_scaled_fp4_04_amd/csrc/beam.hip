@@ -110,6 +110,9 @@ __device__ __forceinline__ float wave_top(float v)
     return fmaxf(fmaxf(lane_of(v, 0), lane_of(v, 16)), fmaxf(lane_of(v, 32), lane_of(v, 48)));
 }
 
+// e^d, d <= 0, by v_exp_f32: the rounding of its argument, 2^-24 |d|, weighs e^d
+__device__ __forceinline__ double exp_of(double d) { return (double)__builtin_amdgcn_exp2f((float)(d * 1.4426950408889634)); }
+
 template <typename Get>
 __device__ __forceinline__ double moved(double v, Get get)
 {
@@ -128,6 +131,61 @@ __device__ __forceinline__ double wave_sum(double v)
     v += moved(v, [](int x) { return lane_xor<15>(x); });
     auto row = [&](int r) { return moved(v, [r](int x) { return __builtin_amdgcn_readlane(x, r); }); };
     return (row(0) + row(16)) + (row(32) + row(48));
+}
+
+// Sorted runs of KP lanes, best first.  Best: a value of a row; Entry: a total of a group.
+
+struct Entry {
+    double total;
+    uint32_t flat;  // beam * vocab + token
+};
+
+__device__ __forceinline__ bool better(const Best &x, const Best &y) { return x.v > y.v || (x.v == y.v && x.i < y.i); }
+__device__ __forceinline__ bool better(const Entry &x, const Entry &y)
+{
+    return x.total > y.total || (x.total == y.total && x.flat < y.flat);
+}
+
+template <int M>
+__device__ __forceinline__ Best lane_xor(const Best &x)
+{
+    return Best{__int_as_float(lane_xor<M>(__float_as_int(x.v))), lane_xor<M>(x.i)};
+}
+template <int M>
+__device__ __forceinline__ Entry lane_xor(const Entry &x)
+{
+    return Entry{moved(x.total, [](int v) { return lane_xor<M>(v); }), (uint32_t)lane_xor<M>((int)x.flat)};
+}
+
+// x: a bitonic run of 2 D lanes -> sorted, best first
+template <int D, typename E>
+__device__ __forceinline__ void settle(E &x, int lane)
+{
+    const E y = lane_xor<D>(x);
+    if ((lane & D) ? better(x, y) : better(y, x)) x = y;
+    if constexpr (D > 1) settle<D / 2>(x, lane);
+}
+
+// Sorted runs x and y of KP lanes: the best of both, sorted.  Against the reverse of y, the better of each
+// pair are the KP best, and form a bitonic run.
+template <int KP, typename E>
+__device__ __forceinline__ void merge(E &x, const E &y, int lane)
+{
+    const E z = lane_xor<KP - 1>(y);
+    if (better(z, x)) x = z;
+    settle<KP / 2>(x, lane);
+}
+
+// all runs of a wave into one (every run ends up as it), H lanes of them done
+template <int KP, int H, typename E>
+__device__ __forceinline__ void merge_wave(E &x, int lane)
+{
+    if constexpr (H < 64) {
+        const E z = lane_xor<(H | (KP - 1))>(x);
+        if (better(z, x)) x = z;
+        settle<KP / 2>(x, lane);
+        merge_wave<KP, 2 * H>(x, lane);
+    }
 }
 
 // A group of vectors from token e0 on.  Vectors begin at multiples of kPer tokens whatever the row's address
@@ -162,13 +220,15 @@ __device__ __forceinline__ float widen(T v)
     else return v;
 }
 
-// A wave walks over a part of a row, a.groups groups, the next group's loads in flight.
+// A workgroup takes a part of a row, each of its waves a.groups groups one behind the other, the next group's loads in
+// flight; then one wave adds up the four sums and merges the four lists (k = 16, 8 beams of 131072: without that
+// the join has four times the lists, and takes 4 us longer in a batch of 64 groups, 15 us in one of a single group).
 //
 // First pass: sums of exponentials, and every vector's maximum into LDS.  The k-th largest of the lanes'
 // maxima is then a bar that at least k values reach and all of the k best do.  Second pass: the vectors whose
 // maximum reaches it (about k of them) are listed and read again, and their values put in their places one at a
 // time, the bar rising.
-template <typename T>
+template <typename T, int KP>
 __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a)
 {
     constexpr int kPer = Row<T>::kPer, kGroup = kVec * 64 * kPer;
@@ -176,14 +236,16 @@ __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a)
     const float kInf = __builtin_inff();
     __shared__ float4 sm_top[4][kMost][64];
     __shared__ int sm_listed[4][kListed + kVec * 64];
+    __shared__ float sm_ref[4];
+    __shared__ double sm_sum[4];
+    __shared__ Best sm_best[4][KP];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int64_t id = (int64_t)blockIdx.x * 4 + wave;
-    if (id >= (int64_t)a.batch * a.beams * a.parts) return;
+    const int64_t id = blockIdx.x;
     const int row = (int)(id / a.parts), part = (int)(id - (int64_t)row * a.parts);
     if (a.done && a.done[row]) return;
     const T *x = reinterpret_cast<const T *>(a.logits) + row * a.ld;
-    const int first = part * a.groups * kGroup;
-    const int groups = min(a.groups, (a.vocab - first + kGroup - 1) / kGroup);
+    const int first = (part * 4 + wave) * a.groups * kGroup;
+    const int groups = min(a.groups, (a.vocab - first + kGroup - 1) / kGroup);  // (<= 0 past the row's end)
     uint32_t w[kVec][4];
     load_group(w, x, first, a.vocab, lane);
 
@@ -234,8 +296,8 @@ __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a)
     }
     sum = wave_sum(sum);
     if (lane == 0) {
-        a.part_top[id] = ref;
-        a.part_sum[id] = sum;
+        sm_ref[wave] = ref;
+        sm_sum[wave] = sum;
     }
 
     // the bar, bit by bit from the top, by counting lanes; what counts is above it
@@ -291,60 +353,30 @@ __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a)
         if (n >= kListed) look();
     }
     look();
+    if (lane < KP) sm_best[wave][lane] = s;  // (lanes from k on are empty)
+    __syncthreads();
+    if (wave > 0) return;
+    constexpr int kRuns = 64 / KP < 4 ? 64 / KP : 4;
+    const int run = lane / KP;
+    Best best = run < 4 ? sm_best[run < 4 ? run : 0][lane % KP] : Best{-kInf, 0x7FFFFFFF};
+#pragma unroll
+    for (int r = kRuns; r < 4; r += kRuns) merge<KP>(best, sm_best[r + run][lane % KP], lane);
+    merge_wave<KP, KP>(best, lane);
     if (lane < a.k) {
-        a.part_value[id * a.k + lane] = s.v;
-        a.part_token[id * a.k + lane] = s.i;
+        a.part_value[id * a.k + lane] = best.v;
+        a.part_token[id * a.k + lane] = best.i;
+    }
+    if (lane == 0) {
+        const float most = fmaxf(fmaxf(sm_ref[0], sm_ref[1]), fmaxf(sm_ref[2], sm_ref[3]));
+        double all = 0.0;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) all += sm_sum[r] * exp_of((double)sm_ref[r] - (double)most);
+        a.part_top[id] = most;
+        a.part_sum[id] = all;
     }
 }
 
 // ---------------------------------------------------------------- join --
-
-struct Entry {
-    double total;
-    uint32_t flat;  // beam * vocab + token
-};
-
-__device__ __forceinline__ bool better(const Entry &x, const Entry &y)
-{
-    return x.total > y.total || (x.total == y.total && x.flat < y.flat);
-}
-
-template <int M>
-__device__ __forceinline__ Entry lane_xor(const Entry &x)
-{
-    return Entry{moved(x.total, [](int v) { return lane_xor<M>(v); }), (uint32_t)lane_xor<M>((int)x.flat)};
-}
-
-// x: a bitonic run of 2 D lanes -> sorted, best first
-template <int D>
-__device__ __forceinline__ void settle(Entry &x, int lane)
-{
-    const Entry y = lane_xor<D>(x);
-    if ((lane & D) ? better(x, y) : better(y, x)) x = y;
-    if constexpr (D > 1) settle<D / 2>(x, lane);
-}
-
-// Sorted runs x and y of KP lanes: the best of both, sorted.  Against the reverse of y, the better of each
-// pair are the KP best, and form a bitonic run.
-template <int KP>
-__device__ __forceinline__ void merge(Entry &x, const Entry &y, int lane)
-{
-    const Entry z = lane_xor<KP - 1>(y);
-    if (better(z, x)) x = z;
-    settle<KP / 2>(x, lane);
-}
-
-// all runs of a wave into one (every run ends up as it), H lanes of them done
-template <int KP, int H>
-__device__ __forceinline__ void merge_wave(Entry &x, int lane)
-{
-    if constexpr (H < 64) {
-        const Entry z = lane_xor<(H | (KP - 1))>(x);
-        if (better(z, x)) x = z;
-        settle<KP / 2>(x, lane);
-        merge_wave<KP, 2 * H>(x, lane);
-    }
-}
 
 // One workgroup a group of beams; lists of KP places, a.k of them in use
 template <int KP>
@@ -392,9 +424,8 @@ __global__ __launch_bounds__(1024) void k_beam_join(BeamArgs a)
             const float t = p < a.parts ? a.part_top[at + p] : -__builtin_inff();
             const double u = p < a.parts ? a.part_sum[at + p] : 0.0;
             const float now = fmaxf(top, wave_top(t));
-            // e^d <= 1 by v_exp_f32: its argument's rounding, 2^-24 |d|, weighs e^d
-            auto share = [&](float x) { return (double)__builtin_amdgcn_exp2f((float)(((double)x - (double)now) * 1.4426950408889634)); };
-            sum = (top == -__builtin_inff() ? 0.0 : sum * share(top)) + (p < a.parts ? u * share(t) : 0.0);
+            sum = (top == -__builtin_inff() ? 0.0 : sum * exp_of((double)top - (double)now)) +
+                  (p < a.parts ? u * exp_of((double)t - (double)now) : 0.0);
             top = now;
         }
         if (!ended) b -= (double)top + log(wave_sum(sum));
@@ -435,21 +466,35 @@ __global__ __launch_bounds__(1024) void k_beam_join(BeamArgs a)
     }
 }
 
-// a wave a list step and a beam, up to 16
-template <int KP>
-void launch_join(const BeamArgs &a, int64_t lists, hipStream_t st)
+template <typename T, int KP>
+void launch_kp(const BeamArgs &a, int64_t grid, hipStream_t st)
 {
-    const int64_t steps = (lists + 64 / KP - 1) / (64 / KP), most = steps > a.beams ? steps : a.beams;
+    hipLaunchKernelGGL((k_beam_rows<T, KP>), dim3((unsigned)grid), dim3(256), 0, st, a);
+    // a wave a list step and a beam, up to 8, or 16 where there are very many lists
+    const int64_t lists = (int64_t)a.beams * a.parts, steps = (lists + 64 / KP - 1) / (64 / KP), most = steps > a.beams ? steps : a.beams;
+    const int cap = steps > 128 ? 16 : 8;
     int waves = 1;
-    while (waves < most && waves < 16) waves <<= 1;
+    while (waves < most && waves < cap) waves <<= 1;
     hipLaunchKernelGGL(k_beam_join<KP>, dim3((unsigned)a.batch), dim3(64 * waves), 0, st, a);
 }
 
-// Groups of a part: as many as leave the chip four waves a SIMD
+// lists of a power of two of places
+template <typename T>
+void launch_k(const BeamArgs &a, int64_t grid, hipStream_t st)
+{
+    if (a.k <= 4) launch_kp<T, 4>(a, grid, st);
+    else if (a.k <= 8) launch_kp<T, 8>(a, grid, st);
+    else if (a.k <= 16) launch_kp<T, 16>(a, grid, st);
+    else if (a.k <= 32) launch_kp<T, 32>(a, grid, st);
+    else launch_kp<T, 64>(a, grid, st);
+}
+
+// Groups of a wave: as many as leave the chip a wave a SIMD (fewer lists to join; 4 / 2 / 1 waves a SIMD: 16 groups of 8
+// beams of 131072 tokens 21.3 / 19.5 / 19.1 us, 32 of 5 of 50003 19.9 / 20.0 / 16.2 us, the others alike)
 int groups_of(int64_t rows, int64_t vocab, fp4_dtype xt)
 {
     const int64_t group = kVec * 64 * (xt == FP4_BF16 ? 8 : 4);
-    const int64_t all = rows * ((vocab + group - 1) / group) / (16 * device_cu_count());
+    const int64_t all = rows * ((vocab + group - 1) / group) / (4 * device_cu_count());
     return all < 1 ? 1 : all > kMost ? kMost : (int)all;
 }
 
@@ -457,7 +502,7 @@ int groups_of(int64_t rows, int64_t vocab, fp4_dtype xt)
 
 int64_t beam_parts(int64_t rows, int64_t vocab, fp4_dtype xt)
 {
-    const int64_t part = kVec * 64 * (xt == FP4_BF16 ? 8 : 4) * groups_of(rows, vocab, xt);
+    const int64_t part = 4 * kVec * 64 * (xt == FP4_BF16 ? 8 : 4) * groups_of(rows, vocab, xt);
     return (vocab + part - 1) / part;
 }
 
@@ -466,15 +511,8 @@ fp4_status launch_beam_select(BeamArgs a, fp4_dtype xt, hipStream_t st)
     const int64_t rows = (int64_t)a.batch * a.beams;
     a.parts = (int)beam_parts(rows, a.vocab, xt);
     a.groups = groups_of(rows, a.vocab, xt);
-    const dim3 grid((unsigned)((rows * a.parts + 3) / 4));
-    if (xt == FP4_BF16) hipLaunchKernelGGL(k_beam_rows<uint16_t>, grid, dim3(256), 0, st, a);
-    else hipLaunchKernelGGL(k_beam_rows<float>, grid, dim3(256), 0, st, a);
-    const int64_t lists = (int64_t)a.beams * a.parts;
-    if (a.k <= 4) launch_join<4>(a, lists, st);
-    else if (a.k <= 8) launch_join<8>(a, lists, st);
-    else if (a.k <= 16) launch_join<16>(a, lists, st);
-    else if (a.k <= 32) launch_join<32>(a, lists, st);
-    else launch_join<64>(a, lists, st);
+    if (xt == FP4_BF16) launch_k<uint16_t>(a, rows * a.parts, st);
+    else launch_k<float>(a, rows * a.parts, st);
     return hipGetLastError() == hipSuccess ? FP4_OK : FP4_ERR_HIP;
 }
 

@@ -94,15 +94,79 @@ __device__ __forceinline__ void cache8(const KvArgs &a, int side, int head, int6
 
 constexpr int kRowsOut = -1;  // FMT: key rows are outputs, there is no cache
 
-template <typename TI, typename TO, int FMT>
+// How the two values of a pair meet: neighbours of a lane (interleaved), lanes 8 or 4 apart by DPP (half-split, rot
+// 128 or 64), or any lanes by a shuffle
+enum { kPairLane = 0, kPair8 = 1, kPair4 = 2, kPairAny = 3 };
+
+template <int PAIR>
+__device__ __forceinline__ float partner_of(float v, int lane)
+{
+    if constexpr (PAIR == kPair8) return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x128, 0xF, 0xF, false));
+    else if constexpr (PAIR == kPair4)  // lane ^ 7, then ^ 3
+        return __int_as_float(__builtin_amdgcn_mov_dpp(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x141, 0xF, 0xF, false), 0x1B, 0xF, 0xF, false));
+    else return __shfl(v, lane, kWave);
+}
+
+template <typename T>
+struct Raw {  // 8 values as they are in memory
+    uint4 w[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T *p)
+    {
+        w[0] = *reinterpret_cast<const uint4 *>(p);
+        if constexpr (sizeof(T) == 4) w[1] = *reinterpret_cast<const uint4 *>(p + 4);
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                v[i] = __uint_as_float((&w[0].x)[i]);
+                v[4 + i] = __uint_as_float((&w[1].x)[i]);
+            } else {
+                v[2 * i] = __uint_as_float((&w[0].x)[i] << 16);
+                v[2 * i + 1] = __uint_as_float((&w[0].x)[i] & 0xFFFF0000u);
+            }
+        }
+    }
+};
+
+// A wave's passes go over the heads of q, then k, then v, each a multiple of the rows that a pass holds, so
+// that the side of a pass is the same in all lanes.  The rows of U passes are requested together.
+template <typename TI, typename TO, int FMT, int PAIR>
 __global__ __launch_bounds__(256) void k_head_norm_rope(HeadNormArgs a, int lane_shift)
 {
-    const int64_t token = a.first + (int64_t)blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6);
+    constexpr int U = 2;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t token = a.first + (int64_t)blockIdx.x * (blockDim.x >> 6) + wave;
     if (token >= a.tokens) return;  // a whole wave
-    const int lane = threadIdx.x & 63;
+    const int lane = threadIdx.x & 63, row = lane >> lane_shift;
     const uint32_t c8 = lane & ((1u << lane_shift) - 1u);
-    const int e0 = (int)c8 * 8;
-    const bool live = e0 < a.dim;
+    const int e0 = (int)c8 * 8, once = 64 >> lane_shift;
+    const int p0 = (int)blockIdx.y * a.slice_passes, p1 = min(a.passes[2], p0 + a.slice_passes);
+
+    struct Pass {
+        int side, head;
+        bool here;
+    };
+    auto pass = [&](int p) {
+        Pass x;
+        x.side = p < a.passes[0] ? 0 : p < a.passes[1] ? 1 : 2;
+        x.head = (p - (x.side == 0 ? 0 : x.side == 1 ? a.passes[0] : a.passes[1])) * once + row;
+        x.here = e0 < a.dim && p < p1 && x.head < (x.side == 0 ? a.heads : a.kv_heads);
+        return x;
+    };
+    auto request = [&](int p, Raw<TI> &raw) {
+        const Pass x = pass(p);
+        const TI *base = reinterpret_cast<const TI *>(x.side == 0 ? a.x[0] : x.side == 1 ? a.x[1] : a.x[2]);
+        const int64_t tok = x.side == 0 ? a.x_tok[0] : x.side == 1 ? a.x_tok[1] : a.x_tok[2];
+        const int64_t step = x.side == 0 ? a.x_head[0] : x.side == 1 ? a.x_head[1] : a.x_head[2];
+#pragma unroll
+        for (uint4 &w : raw.w) w = make_uint4(0, 0, 0, 0);
+        if (x.here) raw.load(base + token * tok + x.head * step + e0);
+    };
+    Raw<TI> raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) request(p0 + u, raw[u]);
 
     // cosines and sines of this lane's values: the sign of the partner's share is in sn
     const bool turns = e0 < a.rot;
@@ -111,7 +175,7 @@ __global__ __launch_bounds__(256) void k_head_norm_rope(HeadNormArgs a, int lane
     int partner = lane;
     if (turns) {
         const double pos = (double)a.positions[token];
-        if (a.interleaved) {
+        if constexpr (PAIR == kPairLane) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float c, s;
@@ -134,68 +198,85 @@ __global__ __launch_bounds__(256) void k_head_norm_rope(HeadNormArgs a, int lane
     if constexpr (FMT != kRowsOut) slot = a.kv.slots[token];
     const bool stored = FMT != kRowsOut && slot >= 0 && slot < (a.kv.pages << a.kv.page_shift);
 
-    const int last = min(a.rows, (int)(blockIdx.y + 1) * a.slice_rows);
-    for (int r = (int)blockIdx.y * a.slice_rows + (lane >> lane_shift); r - (lane >> lane_shift) < last; r += 64 >> lane_shift) {
-        const int side = r < a.heads ? 0 : r < a.heads + a.kv_heads ? 1 : 2;
-        const int head = r - (side == 0 ? 0 : side == 1 ? a.heads : a.heads + a.kv_heads);
-        const bool here = live && r < last;
-        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (here) Vec8<TI>::load(reinterpret_cast<const TI *>(a.x[side]) + token * a.x_tok[side] + head * a.x_head[side] + e0, v);
-        if (side < 2) {
-            if (a.norm) {
-                float ss = 0.0f;
+    for (int p = p0; p < p1; p += U) {
+        Raw<TI> next[U];
+        if (p + U < p1) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(v[i], v[i], ss);
-                const float inv = __builtin_amdgcn_rsqf(__builtin_fmaf(row_sum(ss, lane_shift), a.inv_dim, a.eps));
-                float w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                if (here) Vec8<float>::load(a.w[side] + head * a.w_head[side] + e0, w);
+            for (int u = 0; u < U; ++u) request(p + U + u, next[u]);
+        }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = v[i] * inv * w[i];
+        for (int u = 0; u < U; ++u) {
+            if (p + u >= p1) break;
+            const Pass x = pass(p + u);
+            float v[8];
+            raw[u].get(v);
+            if (x.side < 2) {
+                if (a.norm) {
+                    float ss = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(v[i], v[i], ss);
+                    const float inv = __builtin_amdgcn_rsqf(__builtin_fmaf(row_sum(ss, lane_shift), a.inv_dim, a.eps));
+                    float w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                    if (x.here) Vec8<float>::load((x.side ? a.w[1] : a.w[0]) + x.head * (x.side ? a.w_head[1] : a.w_head[0]) + e0, w);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = v[i] * inv * w[i];
+                }
+                if (a.rot > 0) {
+                    float q[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) q[i] = PAIR == kPairLane ? v[i ^ 1] : partner_of<PAIR>(v[i], partner);
+                    if (turns) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] = __builtin_fmaf(v[i], cs[i], q[i] * sn[i]);
+                    }
+                }
             }
-            if (a.rot > 0) {
-                float p[8];
-                if (a.interleaved) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) p[i] = v[i ^ 1];
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) p[i] = __shfl(v[i], partner, kWave);
-                }
-                if (turns) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = __builtin_fmaf(v[i], cs[i], p[i] * sn[i]);
-                }
+            if (!x.here) continue;
+            if (FMT == kRowsOut || x.side == 0) {
+                TO *base = reinterpret_cast<TO *>(x.side ? a.y[1] : a.y[0]);
+                store8(base + token * (x.side ? a.y_tok[1] : a.y_tok[0]) + x.head * (x.side ? a.y_head[1] : a.y_head[0]) + e0, v);
+            }
+            if constexpr (FMT != kRowsOut) {
+                if (x.side > 0 && stored) cache8<FMT>(a.kv, x.side - 1, x.head, slot, c8, lane_shift, v);
             }
         }
-        if (!here) continue;
-        if (FMT == kRowsOut || side == 0)
-            store8(reinterpret_cast<TO *>(a.y[side & 1]) + token * a.y_tok[side & 1] + head * a.y_head[side & 1] + e0, v);
-        if constexpr (FMT != kRowsOut) {
-            if (side > 0 && stored) cache8<FMT>(a.kv, side - 1, head, slot, c8, lane_shift, v);
-        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) raw[u] = next[u];
     }
 }
 
 }  // namespace
 
-template <typename TI, typename TO, int FMT>
-static void launch_form(HeadNormArgs a, hipStream_t st)
+template <typename TI, typename TO, int FMT, int PAIR>
+static void launch_pair(HeadNormArgs a, int lane_shift, hipStream_t st)
 {
-    int lane_shift = 0;
-    while ((8 << lane_shift) < a.dim) ++lane_shift;
-    const int at_once = 64 >> lane_shift, passes = (a.rows + at_once - 1) / at_once;
+    const int once = 64 >> lane_shift;
+    a.passes[0] = (a.heads + once - 1) / once;
+    a.passes[1] = a.passes[0] + (a.kv_heads + once - 1) / once;
+    a.passes[2] = a.passes[1] + (FMT == kRowsOut ? 0 : (a.kv_heads + once - 1) / once);
+    // a wave a token where there are enough, else its heads are spread over several
     int64_t slices = 4096 / a.tokens;
-    slices = slices < 1 ? 1 : slices > passes ? passes : slices;
-    const int per = (int)((passes + slices - 1) / slices);
-    a.slice_rows = per * at_once;
+    slices = slices < 1 ? 1 : slices > a.passes[2] ? a.passes[2] : slices;
+    a.slice_passes = (int)((a.passes[2] + slices - 1) / slices);
     const int waves = a.tokens >= 1024 ? 4 : 1;
     // a launch holds fewer than 2^32 threads
-    const int64_t slabs = (passes + per - 1) / per, most = (int64_t(1) << 25) / slabs / waves * waves;
+    const int64_t slabs = (a.passes[2] + a.slice_passes - 1) / a.slice_passes, most = (int64_t(1) << 25) / slabs / waves * waves;
     for (a.first = 0; a.first < a.tokens; a.first += most) {
         const int64_t n = a.tokens - a.first < most ? a.tokens - a.first : most;
         const dim3 grid((unsigned)((n + waves - 1) / waves), (unsigned)slabs);
-        hipLaunchKernelGGL((k_head_norm_rope<TI, TO, FMT>), grid, dim3(64 * waves), 0, st, a, lane_shift);
+        hipLaunchKernelGGL((k_head_norm_rope<TI, TO, FMT, PAIR>), grid, dim3(64 * waves), 0, st, a, lane_shift);
     }
+}
+
+template <typename TI, typename TO, int FMT>
+static void launch_form(const HeadNormArgs &a, hipStream_t st)
+{
+    int lane_shift = 0;
+    while ((8 << lane_shift) < a.dim) ++lane_shift;
+    if (a.rot == 0 || a.interleaved) launch_pair<TI, TO, FMT, kPairLane>(a, lane_shift, st);
+    else if (a.rot == 128) launch_pair<TI, TO, FMT, kPair8>(a, lane_shift, st);
+    else if (a.rot == 64) launch_pair<TI, TO, FMT, kPair4>(a, lane_shift, st);
+    else launch_pair<TI, TO, FMT, kPairAny>(a, lane_shift, st);
 }
 
 template <int FMT>

@@ -239,10 +239,11 @@ struct HeadNormArgs {
     const int32_t *positions;
     const double *freqs;
     int64_t tokens, first;        // first token of this launch (set by the launcher)
-    int heads, kv_heads, rows;    // rows of a token: heads, kv_heads and, with a cache, kv_heads again
+    int heads, kv_heads;
     int dim, rot, interleaved, norm;
     float eps, inv_dim;
-    int slice_rows;               // rows of a wave (set by the launcher)
+    int passes[3];                // passes of q; of q and k; of all (set by the launcher)
+    int slice_passes;             // passes of a wave (set by the launcher)
     KvArgs kv;                    // the cache: codes, scales, slots, rule, nonfinite
 };
 

@@ -179,7 +179,7 @@ __global__ __launch_bounds__(256) void k_pages_place(PageArgs a)
 
 constexpr int kRangeWords = 8192, kRangePages = kRangeWords * 32;  // 32 KiB of LDS
 
-// the rows first, first + step, .. of the table, a wave a row
+// the rows first, first + step, .. of the table, a wave a row, four loads in flight
 __device__ __forceinline__ void mark_pages(const PageArgs &a, uint32_t *bits, int32_t low, int first, int step)
 {
     const int lane = threadIdx.x & 63;
@@ -187,10 +187,14 @@ __device__ __forceinline__ void mark_pages(const PageArgs &a, uint32_t *bits, in
         const int64_t n = (int64_t)max(a.seq_lens[b], 0) + (1 << a.page_shift) - 1;
         const int entries = (int)min(n >> a.page_shift, (int64_t)a.width);
         const int32_t *row = a.table + b * a.table_stride;
-        for (int i = lane; i < entries; i += 64) {
-            const int32_t id = row[i];
-            if (id >= 0 && id < a.pages && id >= low && id < low + kRangePages)
-                atomicOr(&bits[(id - low) >> 5], 1u << ((id - low) & 31));
+        for (int i = lane; i < entries; i += 256) {
+            int32_t id[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) id[u] = i + 64 * u < entries ? row[i + 64 * u] : -1;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (id[u] >= 0 && id[u] < a.pages && id[u] >= low && id[u] < low + kRangePages)
+                    atomicOr(&bits[(id[u] - low) >> 5], 1u << ((id[u] - low) & 31));
         }
     }
 }
@@ -235,41 +239,41 @@ __global__ __launch_bounds__(1024) void k_pages_collect_small(PageArgs a)
     if (threadIdx.x == 0) a.state_out[0] = (int32_t)done;
 }
 
-// Large pools: grid (parts, ranges); a part of the rows marks one range of the pages
-__global__ __launch_bounds__(1024) void k_pages_mark(PageArgs a)
+// Large pools and tables: grid (parts, ranges); a part of the rows marks one range of the pages.  The bitmap of
+// part p is at ws + p * words.
+constexpr int kMarkParts = 16;
+
+__global__ __launch_bounds__(1024) void k_pages_mark(PageArgs a, int64_t words)
 {
     __shared__ uint32_t bits[kRangeWords];
-    for (int i = threadIdx.x; i < kRangeWords; i += blockDim.x) bits[i] = 0;
+    const int64_t word0 = (int64_t)blockIdx.y * kRangeWords;
+    const int n = (int)min(words - word0, (int64_t)kRangeWords), waves = blockDim.x >> 6;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) bits[i] = 0;
     __syncthreads();
-    const int waves = blockDim.x >> 6;
-    mark_pages(a, bits, (int32_t)(blockIdx.y * (uint32_t)kRangePages), (int)blockIdx.x * waves + (int)(threadIdx.x >> 6),
-               (int)gridDim.x * waves);
+    mark_pages(a, bits, (int32_t)(word0 * 32), (int)blockIdx.x * waves + (int)(threadIdx.x >> 6), (int)gridDim.x * waves);
     __syncthreads();
-    uint32_t *out = reinterpret_cast<uint32_t *>(a.ws) + ((int64_t)blockIdx.x * gridDim.y + blockIdx.y) * kRangeWords;
-    for (int i = threadIdx.x; i < kRangeWords; i += blockDim.x) out[i] = bits[i];
+    uint32_t *out = reinterpret_cast<uint32_t *>(a.ws) + blockIdx.x * words + word0;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) out[i] = bits[i];
+}
+
+__device__ __forceinline__ uint32_t marked(const uint32_t *ws, int64_t words, int64_t i)
+{
+    uint32_t w = 0;
+#pragma unroll
+    for (int p = 0; p < kMarkParts; ++p) w |= ws[p * words + i];
+    return w;
 }
 
 // one workgroup a 1024 words: what is free before them, then their own
-__global__ __launch_bounds__(1024) void k_pages_sweep(PageArgs a, int parts, int64_t part_words)
+__global__ __launch_bounds__(1024) void k_pages_sweep(PageArgs a, int64_t words)
 {
     __shared__ uint32_t red[16];
     const uint32_t *ws = reinterpret_cast<const uint32_t *>(a.ws);
-    const int64_t words = ((int64_t)a.pages + 31) >> 5;
-    uint32_t before = 0, total;
-    for (int64_t i = threadIdx.x; i < (int64_t)blockIdx.x * 1024; i += 1024) {
-        uint32_t w = 0;
-        for (int p = 0; p < parts; ++p) w |= ws[p * part_words + i];
-        before += __builtin_popcount(~w);
-    }
-    block_scan(before, red, total);
-    const uint32_t base = total;
     const int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x;
-    uint32_t w = ~0u;
-    if (i < words) {
-        w = 0;
-        for (int p = 0; p < parts; ++p) w |= ws[p * part_words + i];
-        w = pool_word(w, i * 32, a.pages);
-    }
+    const uint32_t w = i < words ? pool_word(marked(ws, words, i), i * 32, a.pages) : ~0u;
+    uint32_t before = 0, base = 0, total;
+    for (int64_t j = threadIdx.x; j < (int64_t)blockIdx.x * 1024; j += 1024) before += __builtin_popcount(~marked(ws, words, j));
+    if (blockIdx.x > 0) block_scan(before, red, base);
     const uint32_t n = __builtin_popcount(~w), upto = block_scan(n, red, total);
     list_pages(a, w, (int32_t)((i & ~int64_t(63)) * 32), base + upto - n);
     if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) a.state_out[0] = (int32_t)(base + total);
@@ -370,10 +374,6 @@ __global__ __launch_bounds__(256) void k_kv_copy(KvArgs a, const int32_t *copies
     }
 }
 
-constexpr int kMarkParts = 8;
-
-int64_t ranges_of(int64_t pages) { return (pages + kRangePages - 1) / kRangePages; }
-
 unsigned whole_waves(int64_t n) { return n >= 1024 ? 1024u : n <= 64 ? 64u : (unsigned)((n + 63) & ~int64_t(63)); }
 
 }  // namespace
@@ -401,7 +401,7 @@ static bool collect_small(int64_t pages, int64_t seqs, int64_t width) { return p
 
 size_t pages_collect_bytes(int64_t pages, int64_t seqs, int64_t width)
 {
-    return collect_small(pages, seqs, width) ? 0 : (size_t)(kMarkParts * ranges_of(pages)) * kRangeWords * 4;
+    return collect_small(pages, seqs, width) ? 0 : align256((size_t)kMarkParts * ((pages + 31) / 32) * 4);
 }
 
 fp4_status launch_pages_collect(const PageArgs &a, hipStream_t st)
@@ -409,10 +409,9 @@ fp4_status launch_pages_collect(const PageArgs &a, hipStream_t st)
     if (collect_small(a.pages, a.seqs, a.width)) {
         hipLaunchKernelGGL(k_pages_collect_small, dim3(1), dim3(1024), 0, st, a);
     } else {
-        const int64_t ranges = ranges_of(a.pages), words = ((int64_t)a.pages + 31) / 32;
-        hipLaunchKernelGGL(k_pages_mark, dim3(kMarkParts, (unsigned)ranges), dim3(1024), 0, st, a);
-        hipLaunchKernelGGL(k_pages_sweep, dim3((unsigned)((words + 1023) / 1024)), dim3(1024), 0, st, a, kMarkParts,
-                           ranges * kRangeWords);
+        const int64_t words = ((int64_t)a.pages + 31) / 32;
+        hipLaunchKernelGGL(k_pages_mark, dim3(kMarkParts, (unsigned)((words + kRangeWords - 1) / kRangeWords)), dim3(1024), 0, st, a, words);
+        hipLaunchKernelGGL(k_pages_sweep, dim3((unsigned)((words + 1023) / 1024)), dim3(1024), 0, st, a, words);
     }
     return hipGetLastError() == hipSuccess ? FP4_OK : FP4_ERR_HIP;
 }
