@@ -1336,10 +1336,11 @@ BeamSpace beam_space(int64_t rows, int64_t vocab, int64_t k, fp4_dtype xt)
     return s;
 }
 
+// (a launch holds fewer than 2^32 threads: 256 for at least 4096 logits, 1024 for a group)
 bool beam_sizes_ok(int64_t batch, int64_t beams, int64_t vocab, int64_t k)
 {
-    return batch > 0 && batch < (1 << 24) && beams > 0 && beams <= 64 && vocab > 0 && vocab <= (int64_t(1) << 30) / beams &&
-           k > 0 && k <= 64 && batch * beams < (int64_t(1) << 40) / vocab;
+    return batch > 0 && batch < (1 << 21) && beams > 0 && beams <= 64 && vocab > 0 && vocab <= (int64_t(1) << 30) / beams &&
+           k > 0 && k <= 64 && batch * beams * ((vocab + 4095) / 4096) < (1 << 24);
 }
 
 }  // namespace

@@ -10,7 +10,9 @@
 //
 // Order: totals are compared in 64 bits (in 32, sums of scores around -50 and small differences of logits
 // would merge neighbours), equal ones by beam * vocab + token.  The sums of exponentials are fp32 over 8
-// neighbours and 64 bits from there on; the exponentials are fp32 (v_exp_f32, 1 ulp).
+// neighbours of each vector and 64 bits from there on.  The exponentials are fp32 (v_exp_f32, 1 ulp, of an argument
+// d with two roundings): a term e^-d is off by at most (1 + 2 d) 2^-23 of itself, so a sum by less than 2^-18 where
+// what is 30 below the maximum does not count, and by about 2^-25 in practice, as the errors have either sign.
 #include "device_common.h"
 #include "internal.h"
 
@@ -353,7 +355,7 @@ __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a)
         if (n >= kListed) look();
     }
     look();
-    if (lane < KP) sm_best[wave][lane] = s;  // (lanes from k on are empty)
+    if (lane < KP) sm_best[wave][lane] = s;  // (lanes from k on hold what was displaced, in order)
     __syncthreads();
     if (wave > 0) return;
     constexpr int kRuns = 64 / KP < 4 ? 64 / KP : 4;
@@ -382,7 +384,8 @@ __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a)
 template <int KP>
 __global__ __launch_bounds__(1024) void k_beam_join(BeamArgs a)
 {
-    __shared__ double base[64];
+    __shared__ double base[64];  // score - log of the sum against ...
+    __shared__ float from[64];   // ... this logit
     __shared__ Entry found[16][KP];
     const double kInf = __builtin_inf();
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
@@ -416,7 +419,7 @@ __global__ __launch_bounds__(1024) void k_beam_join(BeamArgs a)
         const int row = row0 + i;
         const int64_t at = (int64_t)row * a.parts;
         const uint8_t ended = a.done ? a.done[row] : 0;
-        double b = (double)a.scores[row];
+        const double b = (double)a.scores[row];
         float top = -__builtin_inff();
         double sum = 0.0;
         for (int p0 = 0; p0 < a.parts; p0 += 64) {
@@ -428,8 +431,11 @@ __global__ __launch_bounds__(1024) void k_beam_join(BeamArgs a)
                   (p < a.parts ? u * exp_of((double)t - (double)now) : 0.0);
             top = now;
         }
-        if (!ended) b -= (double)top + log(wave_sum(sum));
-        if (lane == 0) base[i] = b;
+        const double rest = log(wave_sum(sum));
+        if (lane == 0) {
+            base[i] = ended ? b : b - rest;
+            from[i] = ended ? 0.0f : top;
+        }
     }
     __syncthreads();
 
@@ -438,7 +444,7 @@ __global__ __launch_bounds__(1024) void k_beam_join(BeamArgs a)
         if (l0 != wave * kPer) load(l0 + lane / KP, v, token, beam);
         Entry e{-kInf, ~0u};
         if (v > -__builtin_inff()) {
-            const double total = base[beam] + (double)v;
+            const double total = ((double)v - (double)from[beam]) + base[beam];
             if (total > -kInf) e = Entry{total, (uint32_t)beam * (uint32_t)a.vocab + token};  // (NaN is not)
         }
         if (l0 == wave * kPer) best = e;

@@ -179,23 +179,42 @@ __global__ __launch_bounds__(256) void k_pages_place(PageArgs a)
 
 constexpr int kRangeWords = 8192, kRangePages = kRangeWords * 32;  // 32 KiB of LDS
 
-// the rows first, first + step, .. of the table, a wave a row, four loads in flight
-__device__ __forceinline__ void mark_pages(const PageArgs &a, uint32_t *bits, int32_t low, int first, int step)
+// The rows of wave `wave` of `waves`: as many at a time as fit its lanes (a row takes a power of two of them, up to all),
+// four such steps in flight.
+__device__ __forceinline__ void mark_pages(const PageArgs &a, uint32_t *bits, int32_t low, int wave, int waves)
 {
+    constexpr int U = 4;
     const int lane = threadIdx.x & 63;
-    for (int b = first; b < a.seqs; b += step) {
-        const int64_t n = (int64_t)max(a.seq_lens[b], 0) + (1 << a.page_shift) - 1;
-        const int entries = (int)min(n >> a.page_shift, (int64_t)a.width);
-        const int32_t *row = a.table + b * a.table_stride;
-        for (int i = lane; i < entries; i += 256) {
-            int32_t id[4];
+    int span = 1;
+    while (span < a.width && span < 64) span <<= 1;
+    const int once = 64 / span, col = lane & (span - 1);
+    auto mark = [&](int32_t id) {
+        if (id >= 0 && id < a.pages && id >= low && id < low + kRangePages) atomicOr(&bits[(id - low) >> 5], 1u << ((id - low) & 31));
+    };
+    for (int64_t b0 = (int64_t)wave * once; b0 < a.seqs; b0 += (int64_t)U * waves * once) {
+        int entries[U];
+        const int32_t *row[U];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) id[u] = i + 64 * u < entries ? row[i + 64 * u] : -1;
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (id[u] >= 0 && id[u] < a.pages && id[u] >= low && id[u] < low + kRangePages)
-                    atomicOr(&bits[(id[u] - low) >> 5], 1u << ((id[u] - low) & 31));
+        for (int u = 0; u < U; ++u) {
+            const int64_t b = b0 + (int64_t)u * waves * once + lane / span;
+            const int64_t n = b < a.seqs ? (int64_t)max(a.seq_lens[b], 0) + (1 << a.page_shift) - 1 : 0;
+            entries[u] = (int)min(n >> a.page_shift, (int64_t)a.width);
+            row[u] = a.table + b * a.table_stride;
         }
+        int32_t id[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) id[u] = col < entries[u] ? row[u][col] : -1;
+#pragma unroll
+        for (int u = 0; u < U; ++u) mark(id[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            for (int i = col + 64; i < entries[u]; i += 256) {  // (wider rows take all lanes)
+                int32_t more[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) more[c] = i + 64 * c < entries[u] ? row[u][i + 64 * c] : -1;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) mark(more[c]);
+            }
     }
 }
 

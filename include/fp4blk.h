@@ -699,8 +699,9 @@ size_t beam_select_workspace(int64_t batch, int64_t beams, int64_t vocab, int64_
  * holds a NaN or +infinity offers nothing).  Places that are left get score -infinity, token -1 and parent
  * min(place, beams - 1).
  *  ws     beam_select_workspace() bytes, 16-byte aligned.
- * Totals are compared in 64 bits; a row's sum is within 2^-22 relative.  1 <= k <= 64,
- * beams <= 64, beams * vocab <= 2^30, 0 <= end_token < vocab, batch * beams * vocab < 2^40 (FP4_ERR_SHAPE). */
+ * Totals are compared in 64 bits; a row's sum is within 2^-18 relative.  1 <= k <= 64,
+ * beams <= 64, beams * vocab <= 2^30, 0 <= end_token < vocab, batch < 2^21,
+ * batch * beams * ceil(vocab / 4096) < 2^24 (FP4_ERR_SHAPE). */
 fp4_status beam_select(const void *logits, fp4_dtype xt, int64_t batch, int64_t beams, int64_t vocab, int64_t ld,
                        const float *scores, const uint8_t *done, int64_t end_token, int64_t k, float *out_scores,
                        int32_t *out_parents, int32_t *out_tokens, void *ws, size_t ws_bytes, hipStream_t stream);

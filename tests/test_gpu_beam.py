@@ -17,7 +17,8 @@ def _totals(logits, scores, done, end):
     """float64 [batch, beams * vocab] on the host; what is not offered is -inf."""
     batch, beams = scores.shape
     z = logits.cpu().double().view(batch, beams, -1)
-    t = scores.cpu().double()[..., None] + z - torch.logsumexp(z, -1, keepdim=True)
+    d = z - z.amax(-1, keepdim=True)  # (differences first: logits near the type's lowest value would swallow the sum)
+    t = scores.cpu().double()[..., None] + (d - torch.log(torch.exp(d).sum(-1, keepdim=True)))
     if done is not None:
         d = done.cpu().bool()
         t[d] = -math.inf
@@ -26,9 +27,10 @@ def _totals(logits, scores, done, end):
 
 
 def _check(logits, scores, k, done=None, end=0, exact=False, **kw):
-    """Scores within 2^-20 of the definition's (a sum's exponentials, additions and logarithm together 2^-22 of 1, the
-    result's rounding 2^-24 of it); the choice is the definition's, but that totals nearer than the sums'
-    errors (2^-20) may stand in either order (`exact`: never)."""
+    """A term e^-d of a row's sum is off by at most (1 + 2 d) 2^-23 of itself (v_exp_f32 and two roundings of its
+    argument) and the terms that count have d < 30, so the sum's logarithm is within 2^-17, and a score its own rounding,
+    2^-24 of it, more.  The choice is the definition's, but that totals nearer than that may stand in either
+    order (`exact`: never)."""
     fp4 = _fp4()
     s, p, t = fp4.beam_select(logits, scores, k=k, done=done, end_token=end, **kw)
     batch, beams = scores.shape
@@ -44,7 +46,7 @@ def _check(logits, scores, k, done=None, end=0, exact=False, **kw):
     assert torch.equal(s > -math.inf, real)
     assert bool((s[~real] == -math.inf).all()) and bool((t[~real] == -1).all())
     assert torch.equal(p[~real], torch.arange(k).clamp(max=beams - 1).expand(batch, k)[~real])
-    tol = 2.0 ** -20 * (1 + best.abs())
+    tol = 2.0 ** -17 + 2.0 ** -24 * best.abs()
     assert bool(((s.double() - best).abs() <= tol)[real].all()), float((s.double() - best).abs()[real].max())
     flat = p * vocab + t
     same = flat == at
@@ -52,7 +54,7 @@ def _check(logits, scores, k, done=None, end=0, exact=False, **kw):
     if exact:
         assert bool(same[real].all()), (flat[~same & real], at[~same & real])
     chosen = total.gather(1, flat.clamp(min=0))
-    assert bool(((chosen - best).abs() <= tol)[real].all())
+    assert bool(((chosen - best).abs() <= 2 * tol)[real].all())
     for b in range(batch):  # nothing twice
         f = flat[b][real[b]]
         assert f.unique().numel() == f.numel()

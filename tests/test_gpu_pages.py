@@ -158,14 +158,15 @@ def test_extend_nothing():
 
 @pytest.mark.parametrize("seqs,width,page,pages,longest", [(1, 1, 16, 1, 16), (1, 40, 16, 31, 0), (5, 7, 32, 40, 200), (64, 64, 16, 5000, 1000),
                                                            (300, 200, 16, 70000, 3200), (40, 900, 256, 40000, 200000),
-                                                           (16, 3000, 16, 600000, 40000)])
+                                                           (16, 3000, 16, 600000, 40000), (9000, 1, 16, 9100, 16),
+                                                           (700, 23, 16, 20000, 360), (5, 65, 16, 400, 1040), (3, 400, 16, 1300, 6400)])
 def test_collect(seqs, width, page, pages, longest):
     fp4 = _fp4()
     rng = torch.Generator().manual_seed(pages)
     lens = [min(width * page, int(x * (longest + 1))) for x in torch.rand(seqs, generator=rng).tolist()]
     host, pool, table, _ = _start(fp4, seqs, width, page, pages, lens, 2, wide=1)
     now = [0 if i % 3 == 1 else n // 2 if i % 3 == 2 else n for i, n in enumerate(lens)]
-    if seqs > 4:  # shared pages, entries outside the pool, a length past the row
+    if seqs > 4 and width >= 4:  # shared pages, entries outside the pool, a length past the row
         host.table[3][:4] = host.table[0][:4]
         host.table[4][:2] = [-1, pages]
         now[4] = max(now[4], 2 * page)
