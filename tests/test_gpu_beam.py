@@ -211,3 +211,47 @@ def test_many_parts():
     for i, a in enumerate(at):
         x[0, a], x[1, a] = 20.0 - i, 13.0 + i / 2
     _check(x, torch.tensor([[0.0, -0.25]], device="cuda"), 12)
+
+
+def test_rows_past_4gib():
+    rows, vocab, ld = 4, 5000, 3 * (1 << 28) + 1
+    room = torch.empty(rows * ld, dtype=torch.bfloat16, device="cuda")
+    x = room.as_strided((rows, vocab), (ld, 1))
+    x.copy_(_logits(rows, vocab, torch.bfloat16, 3))
+    scores = -torch.rand(2, 2, device="cuda")
+    got, want = _check(x, scores, 6), _check(x.contiguous(), scores, 6)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_recorded_and_on_another_stream():
+    fp4 = _fp4()
+    x, scores = _logits(6, 3001, torch.bfloat16, 1), torch.zeros(2, 3, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = []
+        call = fp4.prepare(lambda: got.extend(fp4.beam_select(x, scores)))
+        x.copy_(_logits(6, 3001, torch.bfloat16, 2))
+        call()
+        want = fp4.beam_select(x, scores)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_steps_of_every_size():
+    """Lengths around the borders of a vector, a group and a part, the best tokens at their ends."""
+    fp4 = _fp4()
+    for dtype, per in ((torch.bfloat16, 8), (torch.float32, 4)):
+        for edge in (per, 64 * per, 256 * per, 1024 * per, 4096 * per):
+            for vocab in (edge - 1, edge, edge + 1):
+                x = _logits(2, vocab, dtype, vocab)
+                x[0, -1], x[1, 0], x[1, vocab // 2] = 12.0, 12.5, 13.0
+                _check(x, torch.tensor([[0.0, -0.3]], device="cuda"), 5)
+
+
+def test_sorted_rows():
+    """Logits in rising and falling order: all of the best in one lane's, one wave's, one part's reach."""
+    for dtype in (torch.bfloat16, torch.float32):
+        for vocab in (700, 20000, 70000):
+            up = torch.linspace(-9, 9, vocab, device="cuda")
+            _check(torch.stack([up, up.flip(0), up.abs()]).to(dtype), torch.tensor([[0.0, -0.5, -0.1]], device="cuda"), 48)

@@ -265,3 +265,46 @@ def test_captured_and_on_another_stream():
             side.synchronize()
             assert torch.equal(out, got)
             _same(cache, want)
+
+
+def test_cache_past_4gib():
+    """Pages whose codes lie past 4 GiB of the cache."""
+    fp4 = _fp4()
+    kv, page, dim, pages = 2, 128, 128, 70000
+    cache = fp4.KVCache.alloc("bf16", pages, kv, page, dim)
+    n = 5
+    whole = _rows(n, 4 + 2 * kv, dim, torch.bfloat16, 3)
+    q, k, v = whole.split([4, kv, kv], 1)
+    pos = torch.arange(n, dtype=torch.int32, device="cuda") + 100
+    slots = torch.tensor([0, pages * page - 1, 66000 * page + 7, -1, 33000 * page], device="cuda")
+    freqs = fp4.rope_frequencies(dim)
+    fp4.qk_norm_rope_append(cache, q, k, v, pos, slots, freqs)
+    want = fp4.qk_norm_rope(q, k, pos, freqs)[1]
+    for i, s in enumerate(slots.tolist()):
+        if s >= 0:
+            assert torch.equal(cache.k_codes[s // page, :, s % page], want[i])
+            assert torch.equal(cache.v_codes[s // page, :, s % page], v[i])
+    copies = torch.tensor([[66000, 69998, 8], [pages - 1, 1, page]], dtype=torch.int32, device="cuda")
+    fp4.kv_cache_copy(cache, copies)
+    assert torch.equal(cache.k_codes[69998, :, 7], want[2]) and torch.equal(cache.v_codes[1, :, page - 1], v[1])
+
+
+def test_recorded_calls():
+    """prepare() replays both forms on the same memory."""
+    fp4 = _fp4()
+    whole = _rows(3, 8, 64, torch.bfloat16, 1)
+    q, k, v = whole.split([4, 2, 2], 1)
+    pos = torch.arange(3, dtype=torch.int32, device="cuda")
+    cache = _cache(fp4, "mxfp8", 2, 2, 16, 64)
+    slots = torch.arange(3, device="cuda")
+    freqs, w = fp4.rope_frequencies(64), _weight((64,), 2)
+    outs = []
+    call = fp4.prepare(lambda: outs.extend((*fp4.qk_norm_rope(q, k, pos, freqs, w, w, eps=1e-6),
+                                            fp4.qk_norm_rope_append(cache, q, k, v, pos, slots, freqs, w, w, eps=1e-6))))
+    whole.copy_(_rows(3, 8, 64, torch.bfloat16, 9))
+    call()
+    want = fp4.qk_norm_rope(q, k, pos, freqs, w, w, eps=1e-6)
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1]) and torch.equal(outs[2], want[0])
+    other = _cache(fp4, "mxfp8", 2, 2, 16, 64)
+    fp4.qk_norm_rope_append(other, q, k, v, pos, slots, freqs, w, w, eps=1e-6)
+    _same(cache, other)

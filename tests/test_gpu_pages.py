@@ -330,3 +330,43 @@ def test_copy(fmt, dim, heads, page):
     for got, ref in zip(parts, want):
         assert torch.equal(got.view(torch.uint8), ref.view(torch.uint8))
     fp4.kv_cache_copy(cache, torch.empty((0, 3), dtype=torch.int32, device="cuda"))
+
+
+def test_recorded_calls():
+    """prepare() replays a step's planning: pages dealt, rows reordered, pages taken back."""
+    fp4 = _fp4()
+    host, pool, table, _ = _start(fp4, 4, 6, 16, 40, [15, 15, 31, 31], 3)
+    lens, one = _i32([15, 15, 31, 31]), _i32([1] * 4)
+    parents = _i32([[1, 1], [0, 0]])
+    plans, copies = [], []
+
+    def step():
+        plans.append(fp4.kv_pages_extend(pool, table, lens, one, 4))
+        copies.append(fp4.kv_pages_reorder(table, lens, parents, 16))
+        fp4.kv_pages_collect(pool, table, lens)
+
+    call = fp4.prepare(step)
+    want = [15, 15, 31, 31]
+    for _ in range(3):
+        call()
+        want, slots, positions, cu_q, cu_k = host.extend(want, [1] * 4, 4)
+        recs = []
+        for b, p in ((0, [1, 1]), (2, [0, 0])):
+            rows, rec = _reorder_host(host.table[b:b + 2], want[b:b + 2], p, 16)
+            host.table[b:b + 2] = rows
+            recs += rec
+        host.collect(want)
+        assert plans[0].slots.tolist() == slots and lens.tolist() == want and copies[0].tolist() == recs
+        _equal(host, pool, table, "replay")
+
+
+def test_two_plans_of_one_pool_in_a_row():
+    """Calls in order on one stream see each other's pages, without a wait between them."""
+    fp4 = _fp4()
+    host, pool, table, _ = _start(fp4, 6, 9, 16, 50, [0] * 6, 9)
+    lens, dl = [0] * 6, _i32([0] * 6)
+    plans = [fp4.kv_pages_extend(pool, table, dl, _i32([i, 3, 0, 7 * i, 20, 1]), 24 + 8 * i) for i in range(6)]
+    for i, plan in enumerate(plans):
+        lens, slots, positions, cu_q, cu_k = host.extend(lens, [i, 3, 0, 7 * i, 20, 1], 24 + 8 * i)
+        assert (plan.slots.tolist(), plan.positions.tolist(), plan.cu_q.tolist(), plan.cu_k.tolist()) == (slots, positions, cu_q, cu_k), i
+    _equal(host, pool, table, "all")
