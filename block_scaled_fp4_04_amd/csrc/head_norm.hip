@@ -9,7 +9,10 @@
 // One lane holds 8 consecutive values, dim / 8 lanes (rounded up to a power of two) a row, so a wave
 // holds up to 64 / that many rows at a time.  A wave takes one token and walks over its heads: the 8
 // cosines and sines of a lane depend on the token and the lane's place in the row only, and are formed
-// once a token.  Bound by memory where there are many tokens, by the launch where there are few.
+// once a token, in place of a table that would have to be read.  Bound by memory where there are many tokens: 16384
+// tokens of 40 + 8 heads of 128 in bf16, 403 MB, take 87 us (4.6 TB/s; a large copy runs at 5.2), one row a lane group
+// at a time 128 us; 6001 tokens of 16 + 4 + 4 heads of 256 into a bf16 cache, 148 MB, 33 us.  By the launch where
+// there are few: one token 3.9 us.
 #include "quant_device.h"
 
 namespace fp4k {
@@ -133,13 +136,11 @@ struct Raw {  // 8 values as they are in memory
 // A wave's passes go over the heads of q, then k, then v, each a multiple of the rows that a pass holds, so
 // that the side of a pass is the same in all lanes.  The rows of U passes are requested together.
 template <typename TI, typename TO, int FMT, int PAIR>
-__global__ __launch_bounds__(256) void k_head_norm_rope(HeadNormArgs a, int lane_shift)
+__global__ __launch_bounds__(64) void k_head_norm_rope(HeadNormArgs a, int lane_shift)
 {
     constexpr int U = 2;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t token = a.first + (int64_t)blockIdx.x * (blockDim.x >> 6) + wave;
-    if (token >= a.tokens) return;  // a whole wave
-    const int lane = threadIdx.x & 63, row = lane >> lane_shift;
+    const int64_t token = a.first + (int64_t)blockIdx.x;
+    const int lane = threadIdx.x, row = lane >> lane_shift;
     const uint32_t c8 = lane & ((1u << lane_shift) - 1u);
     const int e0 = (int)c8 * 8, once = 64 >> lane_shift;
     const int p0 = (int)blockIdx.y * a.slice_passes, p1 = min(a.passes[2], p0 + a.slice_passes);
@@ -254,17 +255,17 @@ static void launch_pair(HeadNormArgs a, int lane_shift, hipStream_t st)
     a.passes[0] = (a.heads + once - 1) / once;
     a.passes[1] = a.passes[0] + (a.kv_heads + once - 1) / once;
     a.passes[2] = a.passes[1] + (FMT == kRowsOut ? 0 : (a.kv_heads + once - 1) / once);
-    // a wave a token where there are enough, else its heads are spread over several
-    int64_t slices = 4096 / a.tokens;
+    // A wave a token (the angles are formed once), or as many as give the chip 8 waves a SIMD, the most it holds (2 / 4 / 8 /
+    // 16: 512 tokens of 40 + 8 heads of 128 6.3 / 6.1 / 6.8 / 6.9 us, 2048 17.2 / 13.9 / 13.5 / 14.3, 4096 22.4 / 22.4 / 19.7 /
+    // 21.8).  Workgroups of one wave: four take the same time.
+    int64_t slices = 32 * device_cu_count() / a.tokens;
     slices = slices < 1 ? 1 : slices > a.passes[2] ? a.passes[2] : slices;
     a.slice_passes = (int)((a.passes[2] + slices - 1) / slices);
-    const int waves = a.tokens >= 1024 ? 4 : 1;
     // a launch holds fewer than 2^32 threads
-    const int64_t slabs = (a.passes[2] + a.slice_passes - 1) / a.slice_passes, most = (int64_t(1) << 25) / slabs / waves * waves;
+    const int64_t slabs = (a.passes[2] + a.slice_passes - 1) / a.slice_passes, most = (int64_t(1) << 25) / slabs;
     for (a.first = 0; a.first < a.tokens; a.first += most) {
         const int64_t n = a.tokens - a.first < most ? a.tokens - a.first : most;
-        const dim3 grid((unsigned)((n + waves - 1) / waves), (unsigned)slabs);
-        hipLaunchKernelGGL((k_head_norm_rope<TI, TO, FMT, PAIR>), grid, dim3(64 * waves), 0, st, a, lane_shift);
+        hipLaunchKernelGGL((k_head_norm_rope<TI, TO, FMT, PAIR>), dim3((unsigned)n, (unsigned)slabs), dim3(64), 0, st, a, lane_shift);
     }
 }
 

@@ -2,8 +2,10 @@
 // positions from request lengths, the free list from the tables that are alive, block tables and partly
 // filled pages of beams after a selection.  (quant.hip fills the slots, the attention kernels read the tables.)
 //
-// All of it is a few integers a sequence, a token or a table entry: bound by the launch and by the chain
-// of scans, not by bytes, so the small calls are one workgroup and one launch.  Results do not depend on
+// All of it is a few integers a sequence, a token or a table entry: bound by the launch and by chains of
+// dependent loads and scans, not by bytes, so the small calls are one workgroup and one launch (64 sequences of one token
+// 3.6 us; 300 sequences and 32000 tokens in two launches 5.0 + 4.4 us; the free list of 26000 pages from 512 rows
+// 4.3 + 5.4 us; tables of 288 beams 4.5 us and their page copies 5.4 us).  Results do not depend on
 // the order of workgroups: sums are prefix sums, and no entry is written by one workgroup and read by another
 // of the same launch.
 #include "device_common.h"
@@ -144,7 +146,9 @@ __device__ __forceinline__ int span_of(const Span *spans, int seqs, uint32_t t)
     return lo;
 }
 
-constexpr int kSmallSeqs = 1024, kSmallTokens = 4096;
+// One workgroup, one launch, up to these sizes (one / two launches, the host's part of a launch, 3 us, aside: 64 sequences of
+// 1 token 3.1 / 4.6 us, of 16 7.3 / 7.0, of 64 9.9 / 7.5; one of 2048 5.9 / 4.6, of 8192 9.1 / 4.7; 1000 of 1 6.2 / 8.9)
+constexpr int kSmallSeqs = 1024, kSmallTokens = 2048;
 
 // Everything in one workgroup
 __global__ __launch_bounds__(1024) void k_pages_extend_small(PageArgs a)
@@ -219,14 +223,23 @@ __device__ __forceinline__ void mark_pages(const PageArgs &a, uint32_t *bits, in
 }
 
 // 32 pages a thread, `held` its word (all ones past the pool): free ids from place `at` on.  A wave
-// writes two words' ids at a time.
+// writes two words' ids at a time, as far as a word has any.
 __device__ __forceinline__ void list_pages(const PageArgs &a, uint32_t held, int32_t first, uint32_t at)
 {
     const int lane = threadIdx.x & 63, half = lane >> 5, bit = lane & 31;
     const uint32_t open = ~held;
-    for (int i = 0; i < 64; i += 2) {
-        const uint32_t w = __shfl(open, i + half, kWave), p = __shfl(at, i + half, kWave);
-        if ((w >> bit) & 1u) a.free_list[p + __builtin_popcount(w & ((1u << bit) - 1u))] = first + (i + half) * 32 + bit;
+    const uint64_t some = __ballot(open != 0);
+    const int words = some ? 64 - __builtin_clzll(some) : 0;
+    for (int i = 0; i < words; i += 8) {
+        uint32_t w[4], p[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            w[u] = __shfl(open, i + 2 * u + half, kWave);
+            p[u] = __shfl(at, i + 2 * u + half, kWave);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if ((w[u] >> bit) & 1u) a.free_list[p[u] + __builtin_popcount(w[u] & ((1u << bit) - 1u))] = first + (i + 2 * u) * 32 + lane;
     }
 }
 
@@ -416,7 +429,9 @@ fp4_status launch_pages_extend(const PageArgs &a, hipStream_t st)
     return hipGetLastError() == hipSuccess ? FP4_OK : FP4_ERR_HIP;
 }
 
-static bool collect_small(int64_t pages, int64_t seqs, int64_t width) { return pages <= kRangePages && seqs * width <= 16384; }
+// One workgroup, one launch, for small tables and pools that fit its bitmap (one / two launches, the host's part of a launch aside:
+// tables of 16 x 16 entries 3.5 / 4.4 us, 64 x 64 6.7 / 7.7, 64 x 128 8.2 / 8.2, 256 x 64 10.0 / 7.9, 512 x 512 51 / 14)
+static bool collect_small(int64_t pages, int64_t seqs, int64_t width) { return pages <= kRangePages && seqs * width <= 8192; }
 
 size_t pages_collect_bytes(int64_t pages, int64_t seqs, int64_t width)
 {
