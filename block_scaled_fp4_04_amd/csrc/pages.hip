@@ -4,8 +4,8 @@
 //
 // All of it is a few integers a sequence, a token or a table entry: bound by the launch and by chains of
 // dependent loads and scans, not by bytes, so the small calls are one workgroup and one launch (64 sequences of one token
-// 3.6 us; 300 sequences and 32000 tokens in two launches 5.0 + 4.4 us; the free list of 26000 pages from 512 rows
-// 4.3 + 5.4 us; tables of 288 beams 4.5 us and their page copies 5.4 us).  Results do not depend on
+// 3.6 us; 300 sequences and 32000 tokens in two launches 5.0 + 4.6 us; the free list of 26000 pages from 512 rows
+// 4.3 + 5.2 us; tables of 288 beams 4.4 us and their page copies 5.1 us).  Results do not depend on
 // the order of workgroups: sums are prefix sums, and no entry is written by one workgroup and read by another
 // of the same launch.
 #include "device_common.h"
@@ -430,7 +430,7 @@ fp4_status launch_pages_extend(const PageArgs &a, hipStream_t st)
 }
 
 // One workgroup, one launch, for small tables and pools that fit its bitmap (one / two launches, the host's part of a launch aside:
-// tables of 16 x 16 entries 3.5 / 4.4 us, 64 x 64 6.7 / 7.7, 64 x 128 8.2 / 8.2, 256 x 64 10.0 / 7.9, 512 x 512 51 / 14)
+// tables of 16 x 16 entries 3.4 / 4.3 us, 64 x 64 5.6 / 6.7, 64 x 128 7.1 / 7.2, 256 x 64 9.1 / 7.0, 512 x 512 52 / 14)
 static bool collect_small(int64_t pages, int64_t seqs, int64_t width) { return pages <= kRangePages && seqs * width <= 8192; }
 
 size_t pages_collect_bytes(int64_t pages, int64_t seqs, int64_t width)
