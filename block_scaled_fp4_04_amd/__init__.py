@@ -225,7 +225,7 @@ def _out_dt(dtype) -> int:
 
 
 def _need_cuda(*ts):
-    """Every tensor given is a device tensor, and all are on one device."""
+    """Every tensor given is a device tensor, and all are on one device: its index."""
     first = None
     for t in ts:
         if t is None:
@@ -237,6 +237,7 @@ def _need_cuda(*ts):
             first = d
         elif d != first:
             raise ValueError(f"tensors on several devices: {sorted({str(x.device) for x in ts if x is not None})}")
+    return first
 
 
 # Argument checks.  The C ABI receives bare pointers and sizes, so it cannot see a
@@ -1262,15 +1263,16 @@ def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q
 
 # ------------------------------------------------- around the attention ---
 
-def _elsewhere(t: torch.Tensor):
-    """None where t's device is the current one (or t is on the host, which later checks refuse); else the
-    context in which the call has to be made, since the library launches on the current device."""
-    dev = t.get_device()
-    if dev < 0 or dev == torch._C._cuda_getDevice():
-        return None
+def _run_on(device: int, fn, *args):
+    """_run on `device`, the tensors' own, where it is not the current one too (the library launches on the current
+    device).  The stream, the device's current one, is the last argument."""
+    if device == torch._C._cuda_getDevice():
+        _run(fn, *args, torch._C._cuda_getCurrentRawStream(device))
+        return
     if _recording is not None:
         raise ValueError("prepare() records calls on the current device only")
-    return torch.cuda.device(dev)
+    with torch.cuda.device(device):
+        _run(fn, *args, torch._C._cuda_getCurrentRawStream(device))
 
 
 def rope_frequencies(rot: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -1328,9 +1330,6 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tenso
     rotated by positions (int32 [tokens]) times freqs (float64, `rope_frequencies`; None: not):
     value i with i + rot / 2, or neighbours when `interleaved`.  q_out and k_out may be q and k.
     Returns (q_out, k_out)."""
-    if (there := _elsewhere(q)) is not None:
-        with there:
-            return qk_norm_rope(q, k, positions, freqs, q_weight, k_weight, eps, interleaved, dtype, q_out, k_out)
     n, h, d, qt, qh = _heads(q, _F32_BF16, "q")
     hk = kt = kh = kot = koh = 0
     if k is not None:
@@ -1347,10 +1346,10 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tenso
         k_out, kot, koh = _out_heads(k_out, n, hk, d, q_out.dtype, k, "k_out")
         if k_out.dtype != q_out.dtype:
             raise TypeError("q_out and k_out must have the same dtype")
-    _need_cuda(q, k, positions if rot else None, freqs, q_weight, k_weight, q_out, k_out)
-    _run(lib().qk_norm_rope, _ptr(q), _ptr(k), _dt(q), n, h, hk, d, qt, qh, kt, kh, _ptr(q_weight), _ptr(k_weight), qs, ks,
-         eps, _ptr(positions) if rot else None, _ptr(freqs), rot, int(bool(interleaved)), _ptr(q_out), _ptr(k_out),
-         _dt(q_out), qot, qoh, kot, koh, _stream())
+    device = _need_cuda(q, k, positions if rot else None, freqs, q_weight, k_weight, q_out, k_out)
+    _run_on(device, lib().qk_norm_rope, _ptr(q), _ptr(k), _dt(q), n, h, hk, d, qt, qh, kt, kh, _ptr(q_weight),
+            _ptr(k_weight), qs, ks, eps, _ptr(positions) if rot else None, _ptr(freqs), rot, int(bool(interleaved)),
+            _ptr(q_out), _ptr(k_out), _dt(q_out), qot, qoh, kot, koh)
     return q_out, k_out
 
 
@@ -1362,10 +1361,6 @@ def qk_norm_rope_append(cache: KVCache, q: torch.Tensor, k: torch.Tensor, v: tor
                         q_out: torch.Tensor | None = None) -> torch.Tensor:
     """qk_norm_rope with the keys, and v as it is, quantized into the cache at `slots` as
     kv_cache_append does (the keys from fp32, not from rows rounded before).  Returns q_out."""
-    if (there := _elsewhere(cache.k_codes)) is not None:
-        with there:
-            return qk_norm_rope_append(cache, q, k, v, positions, slots, freqs, q_weight, k_weight, eps, interleaved, rule, nonfinite,
-                                       dtype, q_out)
     n, h, d, qt, qh = _heads(q, _F32_BF16, "q")
     nk, hk, dk, kt, kh = _heads(k, _F32_BF16, "k")
     nv, hv, dv, vt, vh = _heads(v, _F32_BF16, "v")
@@ -1379,10 +1374,11 @@ def qk_norm_rope_append(cache: KVCache, q: torch.Tensor, k: torch.Tensor, v: tor
     if nonfinite is not None and (nonfinite.dtype != torch.int32 or nonfinite.numel() < 1):
         raise ValueError("nonfinite must be an int32 tensor of at least one element")
     q_out, qot, qoh = _out_heads(q_out, n, h, d, dtype, q, "q_out")
-    _need_cuda(cache.k_codes, q, k, v, positions if rot else None, freqs, slots, q_weight, k_weight, nonfinite, q_out)
-    _run(lib().qk_norm_rope_append, _kv(cache), _ptr(q), _ptr(k), _ptr(v), _dt(q), n, h, qt, qh, kt, kh, vt, vh,
-         _ptr(q_weight), _ptr(k_weight), qs, ks, eps, _ptr(positions) if rot else None, _ptr(freqs), rot,
-         int(bool(interleaved)), _ptr(slots), _rule(rule), _ptr(nonfinite), _ptr(q_out), _dt(q_out), qot, qoh, _stream())
+    device = _need_cuda(cache.k_codes, q, k, v, positions if rot else None, freqs, slots, q_weight, k_weight, nonfinite,
+                        q_out)
+    _run_on(device, lib().qk_norm_rope_append, _kv(cache), _ptr(q), _ptr(k), _ptr(v), _dt(q), n, h, qt, qh, kt, kh, vt,
+            vh, _ptr(q_weight), _ptr(k_weight), qs, ks, eps, _ptr(positions) if rot else None, _ptr(freqs), rot,
+            int(bool(interleaved)), _ptr(slots), _rule(rule), _ptr(nonfinite), _ptr(q_out), _dt(q_out), qot, qoh)
     return q_out
 
 
@@ -1450,9 +1446,6 @@ def kv_pages_extend(pages: KVPages, block_table: torch.Tensor, seq_lens: torch.T
     caller, so that nothing waits for the device).  in_place: seq_lens and the pool's state become
     those after the call; else the plan holds new ones.  A sequence that cannot be served whole is
     left as it is: its slots are -1 and state[1] counts it.  `out`: a plan of the same sizes to write into."""
-    if (there := _elsewhere(block_table)) is not None:
-        with there:
-            return kv_pages_extend(pages, block_table, seq_lens, new_lens, tokens, in_place, offsets, out, workspace)
     seqs, width, stride = _block_table(block_table)
     _i32_vec(seq_lens, seqs, "seq_lens")
     _i32_vec(new_lens, seqs, "new_lens")
@@ -1480,11 +1473,11 @@ def kv_pages_extend(pages: KVPages, block_table: torch.Tensor, seq_lens: torch.T
         space = workspace
     if workspace is not None or (need and space is None):
         space = _workspace(workspace, need, block_table)
-    _need_cuda(pages.free, block_table, seq_lens, new_lens, out.slots, out.positions, out.cu_q, out.cu_k, out.seq_lens,
-               out.state, space)
-    _run(lib().kv_pages_extend, _pool(pages), _ptr(block_table), seqs, width, stride, _ptr(seq_lens), _ptr(new_lens),
-         tokens, _ptr(out.seq_lens), _ptr(out.state), _ptr(out.slots), _ptr(out.positions), _ptr(out.cu_q),
-         _ptr(out.cu_k), _ptr(space), need, _stream())
+    device = _need_cuda(pages.free, block_table, seq_lens, new_lens, out.slots, out.positions, out.cu_q, out.cu_k,
+                        out.seq_lens, out.state, space)
+    _run_on(device, lib().kv_pages_extend, _pool(pages), _ptr(block_table), seqs, width, stride, _ptr(seq_lens),
+            _ptr(new_lens), tokens, _ptr(out.seq_lens), _ptr(out.state), _ptr(out.slots), _ptr(out.positions),
+            _ptr(out.cu_q), _ptr(out.cu_k), _ptr(space), need)
     return out
 
 
@@ -1497,17 +1490,14 @@ def kv_pages_collect(pages: KVPages, block_table: torch.Tensor, seq_lens: torch.
                      workspace: torch.Tensor | None = None) -> KVPages:
     """The pool's free list anew: every page that no row of the block table holds within its
     length, in ascending order.  A sequence that ended gives its pages back by a length of 0."""
-    if (there := _elsewhere(block_table)) is not None:
-        with there:
-            return kv_pages_collect(pages, block_table, seq_lens, workspace)
     seqs, width, stride = _block_table(block_table)
     _i32_vec(seq_lens, seqs, "seq_lens")
     need = lib().kv_pages_collect_workspace(pages.pages, seqs, width)
     if need or workspace is not None:
         workspace = _workspace(workspace, need, block_table)
-    _need_cuda(pages.free, block_table, seq_lens, workspace)
-    _run(lib().kv_pages_collect, _pool(pages), _ptr(block_table), seqs, width, stride, _ptr(seq_lens), _ptr(workspace),
-         need, _stream())
+    device = _need_cuda(pages.free, block_table, seq_lens, workspace)
+    _run_on(device, lib().kv_pages_collect, _pool(pages), _ptr(block_table), seqs, width, stride, _ptr(seq_lens),
+            _ptr(workspace), need)
     return pages
 
 
@@ -1517,9 +1507,6 @@ def kv_pages_reorder(block_table: torch.Tensor, seq_lens: torch.Tensor, parents:
     j of a group takes the row of beam parents[j], in place or into `out`.  The rows of a group have
     the same length.  Returns int32 [batch * beams, 3]: what kv_cache_copy has to copy in every layer's cache,
     because a partly filled page belongs to one row only."""
-    if (there := _elsewhere(block_table)) is not None:
-        with there:
-            return kv_pages_reorder(block_table, seq_lens, parents, page_size, out, copies)
     seqs, width, stride = _block_table(block_table)
     if parents.dtype != torch.int32:
         raise TypeError(f"parents must be int32, got {parents.dtype}")
@@ -1539,9 +1526,9 @@ def kv_pages_reorder(block_table: torch.Tensor, seq_lens: torch.Tensor, parents:
     else:
         _copies(copies)
         _shape(copies, (seqs, 3), "copies")
-    _need_cuda(block_table, seq_lens, parents, out, copies)
-    _run(lib().kv_pages_reorder, _ptr(block_table), batch, beams, width, stride, _ptr(seq_lens), _ptr(parents),
-         page_size, _ptr(out), ostride, _ptr(copies), _stream())
+    device = _need_cuda(block_table, seq_lens, parents, out, copies)
+    _run_on(device, lib().kv_pages_reorder, _ptr(block_table), batch, beams, width, stride, _ptr(seq_lens),
+            _ptr(parents), page_size, _ptr(out), ostride, _ptr(copies))
     return copies
 
 
@@ -1556,12 +1543,9 @@ def kv_cache_copy(cache: KVCache, copies: torch.Tensor) -> KVCache:
     """For each row (source page, destination page, tokens) of copies int32 [n, 3] the first `tokens`
     tokens of the source page are copied into the destination page (all heads, keys and values); rows
     with a negative page are skipped."""
-    if (there := _elsewhere(copies)) is not None:
-        with there:
-            return kv_cache_copy(cache, copies)
     _copies(copies)
-    _need_cuda(cache.k_codes, copies)
-    _run(lib().kv_cache_copy, _kv(cache), _ptr(copies), copies.shape[0], _stream())
+    device = _need_cuda(cache.k_codes, copies)
+    _run_on(device, lib().kv_cache_copy, _kv(cache), _ptr(copies), copies.shape[0])
     return cache
 
 
@@ -1576,9 +1560,6 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: int | None = None
     nothing), done bool or uint8 [batch, beams] (the beam has ended and offers end_token at its own
     score).  Returns (scores float32, parents int32, tokens int32), each [batch, k], best first, ties to the lowest
     beam, then token.  Places that are left: -inf, min(place, beams - 1), -1."""
-    if (there := _elsewhere(logits)) is not None:
-        with there:
-            return beam_select(logits, scores, k, done, end_token, out, workspace)
     dt = _dt(logits)
     if logits.dim() != 2:
         raise ValueError(f"logits must be [batch * beams, vocab], got {tuple(logits.shape)}")
@@ -1610,7 +1591,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: int | None = None
             if t.dtype != d or not t.is_contiguous():
                 raise TypeError(f"out's {name} must be contiguous {d}")
             _shape(t, (batch, k), f"out's {name}")
-    _need_cuda(logits, scores, done, workspace, *out)
-    _run(lib().beam_select, _ptr(logits), dt, batch, beams, vocab, ld, _ptr(scores), _ptr(done), end_token, k,
-         _ptr(out[0]), _ptr(out[1]), _ptr(out[2]), _ptr(workspace), need, _stream())
+    device = _need_cuda(logits, scores, done, workspace, *out)
+    _run_on(device, lib().beam_select, _ptr(logits), dt, batch, beams, vocab, ld, _ptr(scores), _ptr(done), end_token,
+            k, _ptr(out[0]), _ptr(out[1]), _ptr(out[2]), _ptr(workspace), need)
     return out

@@ -240,3 +240,33 @@ def test_binding_refuses_selection(fp4):
                      (dict(workspace=torch.zeros(4)), ValueError), (dict(), ValueError)):
         with pytest.raises(err):
             fp4.beam_select(**{**good, **bad})
+
+
+def test_calls_go_to_the_tensors_device(fp4, monkeypatch):
+    """The launch is made on the tensors' device and its current stream; prepare() records on the current one only."""
+    now, seen = [0], []
+
+    class On:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            self.old, now[0] = now[0], self.device
+
+        def __exit__(self, *a):
+            now[0] = self.old
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: now[0], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 1000 + d, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", On)
+
+    def call(*args):
+        seen.append((now[0], args))
+        return 0
+
+    fp4._run_on(0, call, 7)
+    fp4._run_on(3, call, 8)
+    assert seen == [(0, (7, 1000)), (3, (8, 1003))] and now == [0]
+    with pytest.raises(ValueError, match="current device"):
+        fp4.prepare(lambda: fp4._run_on(3, call, 9))
+    assert fp4._recording is None
