@@ -1559,7 +1559,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: int | None = None
     bf16, scores float32 [batch, beams] (the beams' log probabilities so far; -inf: the beam offers
     nothing), done bool or uint8 [batch, beams] (the beam has ended and offers end_token at its own
     score).  Returns (scores float32, parents int32, tokens int32), each [batch, k], best first, ties to the lowest
-    beam, then token.  Places that are left: -inf, min(place, beams - 1), -1."""
+    beam, then token; what nothing speaks for (-inf) comes last in that order."""
     dt = _dt(logits)
     if logits.dim() != 2:
         raise ValueError(f"logits must be [batch * beams, vocab], got {tuple(logits.shape)}")

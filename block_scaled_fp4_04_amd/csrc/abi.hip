@@ -1340,7 +1340,7 @@ BeamSpace beam_space(int64_t rows, int64_t vocab, int64_t k, fp4_dtype xt)
 bool beam_sizes_ok(int64_t batch, int64_t beams, int64_t vocab, int64_t k)
 {
     return batch > 0 && batch < (1 << 21) && beams > 0 && beams <= 64 && vocab > 0 && vocab <= (int64_t(1) << 30) / beams &&
-           k > 0 && k <= 64 && batch * beams * ((vocab + 4095) / 4096) < (1 << 24);
+           k > 0 && k <= 64 && k <= beams * vocab && batch * beams * ((vocab + 4095) / 4096) < (1 << 24);
 }
 
 }  // namespace

@@ -463,13 +463,26 @@ __global__ __launch_bounds__(1024) void k_beam_join(BeamArgs a)
         }
         merge_wave<KP, KP>(best, lane);
     }
+    // Fewer totals above -infinity than places: all of them are chosen, and the others follow in the order of beam and
+    // token, that is the n-th number that is not among the chosen ones: x = n + how many of them are <= x.
+    const int real = __builtin_popcountll(__ballot(lane < a.k && best.flat != ~0u));
+    if (real < a.k) {
+        const uint32_t n = (uint32_t)(lane - real);
+        uint32_t x = n;
+        for (bool more = true; more;) {
+            uint32_t y = n;
+            for (int i = 0; i < real; ++i) y += (uint32_t)__builtin_amdgcn_readlane((int)best.flat, i) <= x;
+            more = __ballot(lane >= real && y != x) != 0;
+            x = y;
+        }
+        if (lane >= real) best = Entry{-kInf, x};
+    }
     if (lane < a.k) {
         const int64_t at = (int64_t)blockIdx.x * a.k + lane;
-        const bool real = best.flat != ~0u;
-        const uint32_t i = real ? best.flat / (uint32_t)a.vocab : (uint32_t)min(lane, a.beams - 1);
+        const uint32_t i = best.flat / (uint32_t)a.vocab;
         a.out_scores[at] = (float)best.total;
         a.out_parents[at] = (int32_t)i;
-        a.out_tokens[at] = real ? (int32_t)(best.flat - i * (uint32_t)a.vocab) : -1;
+        a.out_tokens[at] = (int32_t)(best.flat - i * (uint32_t)a.vocab);
     }
 }
 

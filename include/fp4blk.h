@@ -691,16 +691,15 @@ size_t beam_select_workspace(int64_t batch, int64_t beams, int64_t vocab, int64_
  *   total(i, v) = score_i + logit_iv - log sum_u exp(logit_iu),
  * best first, equal ones by beam, then token.
  *  logits [batch * beams][ld] fp32 or bf16 (xt), ld >= vocab, any alignment of an element.
- *  scores fp32 [batch * beams], finite, or -infinity: the beam offers nothing.
+ *  scores fp32 [batch * beams], finite, or -infinity (NaN counts as such): the beam offers nothing.
  *  done   optional uint8 [batch * beams]: nonzero: the beam has ended and offers one
  *         continuation, end_token at its own score; its logits are not read.
  *  out_scores fp32, out_parents (the beam within its group) and out_tokens int32, [batch][k].
- * Only totals above -infinity are chosen (logits of -infinity are masked tokens; a row that
- * holds a NaN or +infinity offers nothing).  Places that are left get score -infinity, token -1 and parent
- * min(place, beams - 1).
+ * Totals of -infinity (masked tokens, beams that offer nothing; a row that holds a NaN or +infinity counts as
+ * such) come last, in the order of beam and token, so that every place names a beam and a token.
  *  ws     beam_select_workspace() bytes, 16-byte aligned.
  * Totals are compared in 64 bits; a row's sum is within 2^-18 relative.  1 <= k <= 64,
- * beams <= 64, beams * vocab <= 2^30, 0 <= end_token < vocab, batch < 2^21,
+ * k <= beams * vocab, beams <= 64, beams * vocab <= 2^30, 0 <= end_token < vocab, batch < 2^21,
  * batch * beams * ceil(vocab / 4096) < 2^24 (FP4_ERR_SHAPE). */
 fp4_status beam_select(const void *logits, fp4_dtype xt, int64_t batch, int64_t beams, int64_t vocab, int64_t ld,
                        const float *scores, const uint8_t *done, int64_t end_token, int64_t k, float *out_scores,

@@ -154,7 +154,7 @@ def test_reorder_and_copy(fp4):
 
 def test_select(fp4):
     assert _select(fp4, xt=2) == DTYPE
-    for bad in (dict(batch=0), dict(beams=0), dict(beams=65), dict(vocab=0), dict(vocab=1 << 30, ld=1 << 30), dict(k=0), dict(k=65),
+    for bad in (dict(batch=0), dict(beams=0), dict(beams=65), dict(vocab=0), dict(vocab=1 << 30, ld=1 << 30), dict(k=0), dict(k=65), dict(vocab=1, ld=1, k=4),
                 dict(end=-1), dict(end=1000), dict(batch=1 << 21), dict(batch=1 << 20, beams=16, vocab=5, ld=5)):
         assert _select(fp4, **bad) == SHAPE, bad
     for bad in (dict(logits=None), dict(scores=None), dict(so=None), dict(po=None), dict(to=None)):

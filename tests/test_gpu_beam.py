@@ -37,15 +37,12 @@ def _check(logits, scores, k, done=None, end=0, exact=False, **kw):
     vocab = logits.shape[1]
     total = _totals(logits, scores, done, end)
     best, at = torch.sort(total, dim=-1, descending=True, stable=True)
-    pad = k - min(k, beams * vocab)
-    best = torch.cat([best[:, :k], torch.full((batch, pad), -math.inf, dtype=torch.float64)], 1)
-    at = torch.cat([at[:, :k], torch.zeros(batch, pad, dtype=torch.long)], 1)
+    best, at = best[:, :k], at[:, :k]
     real = best > -math.inf
     s, p, t = s.cpu(), p.cpu().long(), t.cpu().long()
     assert s.shape == p.shape == t.shape == (batch, k)
     assert torch.equal(s > -math.inf, real)
-    assert bool((s[~real] == -math.inf).all()) and bool((t[~real] == -1).all())
-    assert torch.equal(p[~real], torch.arange(k).clamp(max=beams - 1).expand(batch, k)[~real])
+    assert bool((s[~real] == -math.inf).all()) and torch.equal((p * vocab + t)[~real], at[~real])  # in order
     tol = 2.0 ** -17 + 2.0 ** -24 * best.abs()
     assert bool(((s.double() - best).abs() <= tol)[real].all()), float((s.double() - best).abs()[real].max())
     flat = p * vocab + t
@@ -56,8 +53,7 @@ def _check(logits, scores, k, done=None, end=0, exact=False, **kw):
     chosen = total.gather(1, flat.clamp(min=0))
     assert bool(((chosen - best).abs() <= 2 * tol)[real].all())
     for b in range(batch):  # nothing twice
-        f = flat[b][real[b]]
-        assert f.unique().numel() == f.numel()
+        assert flat[b].unique().numel() == k
     return s, p, t
 
 
@@ -69,7 +65,7 @@ def _logits(rows, vocab, dtype, seed, spread=2.0):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("batch,beams,vocab,k", [(1, 1, 1, 1), (1, 1, 7, 3), (2, 3, 5, 16), (3, 4, 257, 4), (1, 4, 32000, 4), (5, 2, 2047, 2), (4, 5, 2049, 10),
+@pytest.mark.parametrize("batch,beams,vocab,k", [(1, 1, 1, 1), (1, 1, 7, 3), (2, 3, 5, 15), (3, 4, 257, 4), (1, 4, 32000, 4), (5, 2, 2047, 2), (4, 5, 2049, 10),
                                                  (2, 8, 8191, 16), (2, 7, 50003, 14), (1, 64, 1000, 64), (3, 16, 5000, 33), (40, 8, 131072, 8),
                                                  (65, 8, 40009, 16)])
 def test_select(batch, beams, vocab, k, dtype):
@@ -137,7 +133,7 @@ def test_masked_and_nonfinite(vocab):
     y = torch.full((4, vocab), -inf, dtype=torch.bfloat16, device="cuda")
     y[2, vocab - 1] = -3.0
     s, p, t = fp4.beam_select(y, torch.zeros(1, 4, device="cuda"))
-    assert t.tolist() == [[vocab - 1, -1, -1, -1]] and p.tolist() == [[2, 1, 2, 3]] and s[0, 0] == 0.0
+    assert t.tolist() == [[vocab - 1, 0, 1, 2]] and p.tolist() == [[2, 0, 0, 0]] and s[0, 0] == 0.0
 
 
 @pytest.mark.parametrize("kind", [torch.bool, torch.uint8])
@@ -155,7 +151,7 @@ def test_ended_beams(kind):
     for k in (5, 10):
         _check(x, scores, k, done=d, end=vocab - 1)
     s, p, t = fp4.beam_select(x, scores, k=10, done=d, end_token=77)
-    assert t[0].tolist() == [77] * 5 + [-1] * 5
+    assert t[0].tolist() == [77] * 5 + [0, 1, 2, 3, 4] and p[0, 5:].tolist() == [0] * 5
     order = torch.sort(scores[0], descending=True, stable=True)
     assert p[0, :5].tolist() == order.indices.tolist() and torch.equal(s[0, :5], order.values)
 
@@ -255,3 +251,17 @@ def test_sorted_rows():
         for vocab in (700, 20000, 70000):
             up = torch.linspace(-9, 9, vocab, device="cuda")
             _check(torch.stack([up, up.flip(0), up.abs()]).to(dtype), torch.tensor([[0.0, -0.5, -0.1]], device="cuda"), 48)
+
+
+def test_fewer_continuations_than_places():
+    """Masked rows, dead and ended beams: what is left comes in the order of beam and token, around what was chosen."""
+    inf = math.inf
+    for vocab in (6, 70, 5000):
+        x = torch.full((8, vocab), -inf, device="cuda")
+        x[0, 0], x[0, 2], x[1, 1], x[2, 5], x[3, vocab - 1] = 1.0, 2.0, 0.5, 0.0, 3.0
+        x[5] = 1.0
+        scores = torch.tensor([[0.0, -1.0, -inf, -0.5], [-inf, -inf, float("nan"), -2.0]], device="cuda")
+        done = torch.tensor([[False, False, False, False], [False, False, False, True]], device="cuda")
+        for k in (1, 4, 5, 16, 24):
+            _check(x, scores, k, done=done, end=2)
+            _check(x.bfloat16(), scores, k, done=done, end=2)
