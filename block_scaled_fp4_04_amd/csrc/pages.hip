@@ -4,7 +4,7 @@
 //
 // All of it is a few integers a sequence, a token or a table entry: bound by the launch and by chains of
 // dependent loads and scans, not by bytes, so the small calls are one workgroup and one launch (64 sequences of one token
-// 3.6 us; 300 sequences and 32000 tokens in two launches 5.0 + 4.6 us; the free list of 26000 pages from 512 rows
+// 3.1 us; 300 sequences and 32000 tokens in two launches 4.6 + 3.3 us; the free list of 26000 pages from 512 rows
 // 4.3 + 5.2 us; tables of 288 beams 4.4 us and their page copies 5.1 us).  Results do not depend on
 // the order of workgroups: sums are prefix sums, and no entry is written by one workgroup and read by another
 // of the same launch.
@@ -23,18 +23,27 @@ __device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b)
     return s > kFull ? kFull : s;
 }
 
+// lane i takes lane i - SHIFT's value of its row of 16 (0 where there is none), or the last one of the row or the two
+// rows before
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t before(uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+
 // Inclusive prefix sum over the workgroup's threads (saturating sums of non-negative numbers are
 // associative).  `red` holds one value a wave; `total` is the sum of all.
 __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *red, uint32_t &total)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t up = __shfl_up(v, d, kWave);
-        if (lane >= d) v = sat_add(v, up);
-    }
+    v = sat_add(v, before<0x111, 0xF>(v));  // row_shr 1, 2, 4, 8
+    v = sat_add(v, before<0x112, 0xF>(v));
+    v = sat_add(v, before<0x114, 0xF>(v));
+    v = sat_add(v, before<0x118, 0xF>(v));
+    v = sat_add(v, before<0x142, 0xA>(v));  // rows 1 and 3 take the last of rows 0 and 2
+    v = sat_add(v, before<0x143, 0xC>(v));  // rows 2 and 3 that of row 1
     if (waves == 1) {
-        total = __shfl(v, 63, kWave);
+        total = (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
         return v;
     }
     __syncthreads();  // the last scan's readers
@@ -134,7 +143,7 @@ __device__ __forceinline__ void place_token(const PageArgs &a, const Span *spans
     a.positions[t] = pos;
 }
 
-// the first sequence whose new tokens end past t
+// the first sequence whose new tokens end past t (in LDS, a search a lane)
 __device__ __forceinline__ int span_of(const Span *spans, int seqs, uint32_t t)
 {
     int lo = 0, hi = seqs;
@@ -147,7 +156,7 @@ __device__ __forceinline__ int span_of(const Span *spans, int seqs, uint32_t t)
 }
 
 // One workgroup, one launch, up to these sizes (one / two launches, the host's part of a launch, 3 us, aside: 64 sequences of
-// 1 token 3.1 / 4.6 us, of 16 7.3 / 7.0, of 64 9.9 / 7.5; one of 2048 5.9 / 4.6, of 8192 9.1 / 4.7; 1000 of 1 6.2 / 8.9)
+// 1 token 2.6 / 5.3 us, of 16 6.6 / 6.0, of 64 9.2 / 6.2; one of 2048 5.2 / 4.2, of 8192 8.3 / 4.3; 1000 of 1 5.5 / 8.5)
 constexpr int kSmallSeqs = 1024, kSmallTokens = 2048;
 
 // Everything in one workgroup
@@ -168,12 +177,38 @@ __global__ __launch_bounds__(1024) void k_pages_deal(PageArgs a)
     if (threadIdx.x == 0) a.ws[0] = count;
 }
 
+// The same in memory for the 64 consecutive tokens of a wave: 64 ends at a time down to the first token's, then those behind
+// it (300 sequences, 32000 tokens: 4.6 us with a search a lane, 3.3 us; in LDS the search a lane is the faster one, 2.6
+// against 4.2 us for 64 tokens)
+__device__ __forceinline__ int wave_span_of(const Span *spans, int seqs, uint32_t t)
+{
+    const int lane = threadIdx.x & 63;
+    const uint32_t t0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)t);
+    int lo = 0;
+    for (int span = seqs; span > 0;) {  // the answer for t0 is in [lo, lo + span]
+        const int step = (span + 63) >> 6, at = lo + (lane + 1) * step - 1;
+        const bool past = at < lo + span && spans[at].end <= t0;
+        const int skip = __builtin_popcountll(__ballot(past)) * step;
+        lo += skip;
+        span = min(step - 1, span - skip);
+    }
+    int b = lo;
+    for (int base = lo; base < seqs; base += 64) {
+        const uint32_t end = base + lane < seqs ? spans[base + lane].end : kFull;
+        const uint64_t over = __ballot(end > t0 + 63);  // past the last lane's token
+        const int n = over ? __builtin_ctzll(over) : 64;
+        for (int i = 0; i < n; ++i) b += (uint32_t)__builtin_amdgcn_readlane((int)end, i) <= t;
+        if (over) break;
+    }
+    return b;
+}
+
 __global__ __launch_bounds__(256) void k_pages_place(PageArgs a)
 {
     const Span *spans = reinterpret_cast<const Span *>(a.ws + 4);
     const uint32_t t = blockIdx.x * 256u + threadIdx.x;
-    if (t >= (uint32_t)a.tokens) return;
-    place_token(a, spans, a.ws[0], t, span_of(spans, a.seqs, t));
+    const int b = wave_span_of(spans, a.seqs, t);
+    if (t < (uint32_t)a.tokens) place_token(a, spans, a.ws[0], t, b);
 }
 
 // ------------------------------------------------- pages nobody holds --

@@ -370,3 +370,20 @@ def test_two_plans_of_one_pool_in_a_row():
         lens, slots, positions, cu_q, cu_k = host.extend(lens, [i, 3, 0, 7 * i, 20, 1], 24 + 8 * i)
         assert (plan.slots.tolist(), plan.positions.tolist(), plan.cu_q.tolist(), plan.cu_k.tolist()) == (slots, positions, cu_q, cu_k), i
     _equal(host, pool, table, "all")
+
+
+@pytest.mark.parametrize("seqs", [300, 5000])
+def test_extend_among_empty_sequences(seqs):
+    """Few sequences take tokens, far apart and next to each other, in both forms of the call."""
+    fp4 = _fp4()
+    for counts in ({0: 3, 70: 1, 71: 200, 131: 64, 299: 65}, {299: 1}, {0: 1}, {64: 63, 128: 1, 192: 64}, {5: 3000, 290: 1}):
+        lens, new = [7] * seqs, [0] * seqs
+        for b, n in counts.items():
+            new[b + (seqs - 300) if b > 200 else b] = n
+        host, pool, table, _ = _start(fp4, seqs, 200, 16, seqs + 220, lens, 1)
+        dl, tokens = _i32(lens), sum(new) + 2
+        plan = fp4.kv_pages_extend(pool, table, dl, _i32(new), tokens)
+        lens, slots, positions, cu_q, cu_k = host.extend(lens, new, tokens)
+        assert (dl.tolist(), plan.slots.tolist(), plan.positions.tolist()) == (lens, slots, positions)
+        assert (plan.cu_q.tolist(), plan.cu_k.tolist()) == (cu_q, cu_k)
+        _equal(host, pool, table, counts)
