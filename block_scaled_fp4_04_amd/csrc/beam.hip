@@ -10,8 +10,8 @@
 // selection, 19 us is the time of a load-only pass) and the join of 64 groups, k = 16, 6.6 us.
 //
 // Order: totals are compared in 64 bits (in 32, sums of scores around -50 and small differences of logits
-// would merge neighbours), equal ones by beam * vocab + token.  The sums of exponentials are fp32 over 8
-// neighbours of each vector and 64 bits from there on.  The exponentials are fp32 (v_exp_f32, 1 ulp, of an argument
+// would merge neighbours), equal ones by beam * vocab + token.  The sums of exponentials are fp32 over a lane's values of
+// a group (32 or 16, by halves) and 64 bits from there on.  The exponentials are fp32 (v_exp_f32, 1 ulp, of an argument
 // d with two roundings): a term e^-d is off by at most (1 + 2 d) 2^-23 of itself, so a sum by less than 2^-18 where
 // what is 30 below the maximum does not count, and by about 2^-25 in practice, as the errors have either sign.
 #include "device_common.h"

@@ -10,9 +10,9 @@
 // holds up to 64 / that many rows at a time.  A wave takes one token and walks over its heads: the 8
 // cosines and sines of a lane depend on the token and the lane's place in the row only, and are formed
 // once a token, in place of a table that would have to be read.  Bound by memory where there are many tokens: 16384
-// tokens of 40 + 8 heads of 128 in bf16, 403 MB, take 87 us (4.6 TB/s; a large copy runs at 5.2), one row a lane group
+// tokens of 40 + 8 heads of 128 in bf16, 403 MB, take 74 us (5.4 TB/s; a plain copy runs at 5.2), one row a lane group
 // at a time 128 us; 6001 tokens of 16 + 4 + 4 heads of 256 into a bf16 cache, 148 MB, 33 us.  By the launch where
-// there are few: one token 3.9 us.
+// there are few: one token 3.8 us.
 #include "quant_device.h"
 
 namespace fp4k {
@@ -106,17 +106,23 @@ __device__ __forceinline__ float partner_of(float v, int lane)
 {
     if constexpr (PAIR == kPair8) return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x128, 0xF, 0xF, false));
     else if constexpr (PAIR == kPair4)  // lane ^ 7, then ^ 3
-        return __int_as_float(__builtin_amdgcn_mov_dpp(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x141, 0xF, 0xF, false), 0x1B, 0xF, 0xF, false));
+        return __int_as_float(__builtin_amdgcn_mov_dpp(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x141, 0xF, 0xF, false),
+                                                       0x1B, 0xF, 0xF, false));
     else return __shfl(v, lane, kWave);
 }
 
 template <typename T>
 struct Raw {  // 8 values as they are in memory
     uint4 w[sizeof(T) / 2];
+    template <bool ONCE>
     __device__ __forceinline__ void load(const T *p)
     {
-        w[0] = *reinterpret_cast<const uint4 *>(p);
-        if constexpr (sizeof(T) == 4) w[1] = *reinterpret_cast<const uint4 *>(p + 4);
+        const u32x4 *q = reinterpret_cast<const u32x4 *>(p);
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+            const u32x4 r = ONCE ? __builtin_nontemporal_load(q + i) : q[i];
+            w[i] = make_uint4(r[0], r[1], r[2], r[3]);
+        }
     }
     __device__ __forceinline__ void get(float (&v)[8]) const
     {
@@ -135,7 +141,7 @@ struct Raw {  // 8 values as they are in memory
 
 // A wave's passes go over the heads of q, then k, then v, each a multiple of the rows that a pass holds, so
 // that the side of a pass is the same in all lanes.  The rows of U passes are requested together.
-template <typename TI, typename TO, int FMT, int PAIR>
+template <typename TI, typename TO, int FMT, int PAIR, bool ONCE>
 __global__ __launch_bounds__(64) void k_head_norm_rope(HeadNormArgs a, int lane_shift)
 {
     constexpr int U = 2;
@@ -163,7 +169,7 @@ __global__ __launch_bounds__(64) void k_head_norm_rope(HeadNormArgs a, int lane_
         const int64_t step = x.side == 0 ? a.x_head[0] : x.side == 1 ? a.x_head[1] : a.x_head[2];
 #pragma unroll
         for (uint4 &w : raw.w) w = make_uint4(0, 0, 0, 0);
-        if (x.here) raw.load(base + token * tok + x.head * step + e0);
+        if (x.here) raw.template load<ONCE>(base + token * tok + x.head * step + e0);
     };
     Raw<TI> raw[U];
 #pragma unroll
@@ -261,11 +267,20 @@ static void launch_pair(HeadNormArgs a, int lane_shift, hipStream_t st)
     int64_t slices = 32 * device_cu_count() / a.tokens;
     slices = slices < 1 ? 1 : slices > a.passes[2] ? a.passes[2] : slices;
     a.slice_passes = (int)((a.passes[2] + slices - 1) / slices);
+    // Rows past the caches' size are read with the non-temporal hint: 403 MB in and out 74 us, 87 us without it; between
+    // a projection and the attention of its 8192 tokens (117 MB in) 1 to 2.5% of the whole chain's 640 us, at 16384 0.5%,
+    // at 4096 (59 MB) and below none, while there rows that were used shortly before come back from the caches (4096
+    // tokens read again and again: 25 us, 31 us with the hint).  Streaming stores would make the attention that reads the
+    // rows next wait for them (4096 tokens: the chain 331 -> 335 us).
+    const int64_t bytes = a.tokens * (a.heads + (FMT == kRowsOut ? 1 : 2) * a.kv_heads) * a.dim * (int64_t)sizeof(TI);
+    const bool once_only = bytes >= (int64_t(96) << 20);
     // a launch holds fewer than 2^32 threads
     const int64_t slabs = (a.passes[2] + a.slice_passes - 1) / a.slice_passes, most = (int64_t(1) << 25) / slabs;
     for (a.first = 0; a.first < a.tokens; a.first += most) {
         const int64_t n = a.tokens - a.first < most ? a.tokens - a.first : most;
-        hipLaunchKernelGGL((k_head_norm_rope<TI, TO, FMT, PAIR>), dim3((unsigned)n, (unsigned)slabs), dim3(64), 0, st, a, lane_shift);
+        const dim3 grid((unsigned)n, (unsigned)slabs);
+        if (once_only) hipLaunchKernelGGL((k_head_norm_rope<TI, TO, FMT, PAIR, true>), grid, dim3(64), 0, st, a, lane_shift);
+        else hipLaunchKernelGGL((k_head_norm_rope<TI, TO, FMT, PAIR, false>), grid, dim3(64), 0, st, a, lane_shift);
     }
 }
 

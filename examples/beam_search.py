@@ -152,7 +152,8 @@ def run(fmt="mxfp8", prompts=(37, 5, 64), beams=4, steps=20, layers=2, vocab=100
 
     step = search.step
     if graph:
-        # the warm-up and the capture run on what a copy of the state holds, which is put back
+        # The warm-up changes the state, which is put back.  The pages may stay as they are: here all beams of a group
+        # still hold the same text, and the slots behind it are written again.
         kept = [t.clone() for t in (search.table, search.lens, search.pool.free, search.pool.state, search.scores, search.tokens, search.done)]
         step()
         torch.cuda.synchronize()
