@@ -1360,7 +1360,7 @@ def qk_norm_rope_append(cache: KVCache, q: torch.Tensor, k: torch.Tensor, v: tor
                         nonfinite: torch.Tensor | None = None, dtype=torch.bfloat16,
                         q_out: torch.Tensor | None = None) -> torch.Tensor:
     """qk_norm_rope with the keys, and v as it is, quantized into the cache at `slots` as
-    kv_cache_append does (the keys from fp32, not from rows rounded before).  Returns q_out."""
+    kv_cache_append does (the keys from fp32, not from rows rounded before).  q_out may be q.  Returns q_out."""
     n, h, d, qt, qh = _heads(q, _F32_BF16, "q")
     nk, hk, dk, kt, kh = _heads(k, _F32_BF16, "k")
     nv, hv, dv, vt, vh = _heads(v, _F32_BF16, "v")
@@ -1559,7 +1559,8 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: int | None = None
     bf16, scores float32 [batch, beams] (the beams' log probabilities so far; -inf: the beam offers
     nothing), done bool or uint8 [batch, beams] (the beam has ended and offers end_token at its own
     score).  Returns (scores float32, parents int32, tokens int32), each [batch, k], best first, ties to the lowest
-    beam, then token; what nothing speaks for (-inf) comes last in that order."""
+    beam, then token; what nothing speaks for (-inf) comes last in that order.  `out`: those three, to write
+    into; its scores may be `scores`."""
     dt = _dt(logits)
     if logits.dim() != 2:
         raise ValueError(f"logits must be [batch * beams, vocab], got {tuple(logits.shape)}")

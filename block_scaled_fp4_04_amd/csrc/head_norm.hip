@@ -10,7 +10,7 @@
 // holds up to 64 / that many rows at a time.  A wave takes one token and walks over its heads: the 8
 // cosines and sines of a lane depend on the token and the lane's place in the row only, and are formed
 // once a token, in place of a table that would have to be read.  Bound by memory where there are many tokens: 16384
-// tokens of 40 + 8 heads of 128 in bf16, 403 MB, take 74 us (5.4 TB/s; a plain copy runs at 5.2), one row a lane group
+// tokens of 40 + 8 heads of 128 in bf16, 403 MB, take 84 us (4.8 TB/s; a large copy runs at 5.2), one row a lane group
 // at a time 128 us; 6001 tokens of 16 + 4 + 4 heads of 256 into a bf16 cache, 148 MB, 33 us.  By the launch where
 // there are few: one token 3.8 us.
 #include "quant_device.h"
@@ -267,7 +267,8 @@ static void launch_pair(HeadNormArgs a, int lane_shift, hipStream_t st)
     int64_t slices = 32 * device_cu_count() / a.tokens;
     slices = slices < 1 ? 1 : slices > a.passes[2] ? a.passes[2] : slices;
     a.slice_passes = (int)((a.passes[2] + slices - 1) / slices);
-    // Rows past the caches' size are read with the non-temporal hint: 403 MB in and out 74 us, 87 us without it; between
+    // Rows past the caches' size are read with the non-temporal hint: 403 MB in and out 84 us, 87 us without it
+    // (74 and 87 when the outputs' memory is used again and again); between
     // a projection and the attention of its 8192 tokens (117 MB in) 1 to 2.5% of the whole chain's 640 us, at 16384 0.5%,
     // at 4096 (59 MB) and below none, while there rows that were used shortly before come back from the caches (4096
     // tokens read again and again: 25 us, 31 us with the hint).  Streaming stores would make the attention that reads the

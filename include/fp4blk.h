@@ -694,7 +694,8 @@ size_t beam_select_workspace(int64_t batch, int64_t beams, int64_t vocab, int64_
  *  scores fp32 [batch * beams], finite, or -infinity (NaN counts as such): the beam offers nothing.
  *  done   optional uint8 [batch * beams]: nonzero: the beam has ended and offers one
  *         continuation, end_token at its own score; its logits are not read.
- *  out_scores fp32, out_parents (the beam within its group) and out_tokens int32, [batch][k].
+ *  out_scores fp32, out_parents (the beam within its group) and out_tokens int32, [batch][k];
+ *         out_scores may be scores (k == beams).
  * Totals of -infinity (masked tokens, beams that offer nothing; a row that holds a NaN or +infinity counts as
  * such) come last, in the order of beam and token, so that every place names a beam and a token.
  *  ws     beam_select_workspace() bytes, 16-byte aligned.

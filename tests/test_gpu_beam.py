@@ -265,3 +265,14 @@ def test_fewer_continuations_than_places():
         for k in (1, 4, 5, 16, 24):
             _check(x, scores, k, done=done, end=2)
             _check(x.bfloat16(), scores, k, done=done, end=2)
+
+
+@pytest.mark.parametrize("beams,vocab", [(1, 50), (8, 40000), (40, 300)])
+def test_scores_in_place(beams, vocab):
+    fp4 = _fp4()
+    x = _logits(5 * beams, vocab, torch.bfloat16, vocab)
+    scores = -9 * torch.rand(5, beams, device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+    want = fp4.beam_select(x, scores)
+    out = (scores, torch.empty_like(want[1]), torch.empty_like(want[2]))
+    fp4.beam_select(x, scores, out=out)
+    assert all(torch.equal(a, b) for a, b in zip(out, want))

@@ -223,6 +223,12 @@ def test_append_is_the_two_calls(fmt, dim, heads, kv, page):
         assert torch.equal(got, want.to(torch.bfloat16))
         _same(one, two)
         assert int(bad) == 0
+        if xt == torch.bfloat16:  # q in place
+            again, three = whole.clone(), _cache(fp4, fmt, pages, kv, page, dim)
+            qq, kk, vv = again.split([heads, kv, kv], 1)
+            fp4.qk_norm_rope_append(three, qq, kk, vv, pos, slots, freqs, qw, kw, eps=eps, interleaved=inter, rule=rule, q_out=qq)
+            assert torch.equal(qq, got) and torch.equal(again[:, heads:], whole[:, heads:])
+            _same(three, two)
         if n > 5 and fmt != "bf16":
             v = v.clone()
             v[2, 0, 0] = float("nan")  # a token that is not stored
