@@ -193,14 +193,20 @@ __device__ __forceinline__ void merge_wave(E &x, int lane)
 
 // A group of vectors from token e0 on.  Vectors begin at multiples of kPer tokens whatever the row's address
 // (unaligned 16-byte loads), so that equal rows have equal sums and their ties go to the lowest beam.
-template <typename T>
+template <bool ONCE, typename T>
 __device__ __forceinline__ void load_group(uint32_t (&w)[kVec][4], const T *x, int e0, int vocab, int lane)
 {
+    typedef u32x4 vec __attribute__((aligned(2)));
     constexpr int kPer = Row<T>::kPer;
     int e = e0 + lane * kPer;
     if (e0 + kVec * 64 * kPer <= vocab) {
 #pragma unroll
-        for (int v = 0; v < kVec; ++v) __builtin_memcpy(w[v], x + e + v * 64 * kPer, 16);
+        for (int v = 0; v < kVec; ++v) {
+            const vec *p = reinterpret_cast<const vec *>(x + e + v * 64 * kPer);
+            const u32x4 r = ONCE ? __builtin_nontemporal_load(p) : *p;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) w[v][c] = r[c];
+        }
         return;
     }
 #pragma unroll
@@ -231,7 +237,7 @@ __device__ __forceinline__ float widen(T v)
 // maxima is then a bar that at least k values reach and all of the k best do.  Second pass: the vectors whose
 // maximum reaches it (about k of them) are listed and read again, and their values put in their places one at a
 // time, the bar rising.
-template <typename T, int KP>
+template <typename T, int KP, bool ONCE>
 __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a)
 {
     constexpr int kPer = Row<T>::kPer, kGroup = kVec * 64 * kPer;
@@ -250,7 +256,7 @@ __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a)
     const int first = (part * 4 + wave) * a.groups * kGroup;
     const int groups = min(a.groups, (a.vocab - first + kGroup - 1) / kGroup);  // (<= 0 past the row's end)
     uint32_t w[kVec][4];
-    load_group(w, x, first, a.vocab, lane);
+    load_group<ONCE>(w, x, first, a.vocab, lane);
 
     // Exponentials are taken against the first group's maximum `ref` until one would be e^80 times as large.
     // (2^(x log2e - c) is one instruction less a value, but then not even the largest term is exact.)
@@ -263,7 +269,7 @@ __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a)
     double sum = 0.0;
     for (int g = 0; g < groups; ++g) {
         uint32_t next[kVec][4];
-        if (g + 1 < groups) load_group(next, x, first + (g + 1) * kGroup, a.vocab, lane);
+        if (g + 1 < groups) load_group<ONCE>(next, x, first + (g + 1) * kGroup, a.vocab, lane);
         float m[kVec];
 #pragma unroll
         for (int v = 0; v < kVec; ++v) {
@@ -489,7 +495,13 @@ __global__ __launch_bounds__(1024) void k_beam_join(BeamArgs a)
 template <typename T, int KP>
 void launch_kp(const BeamArgs &a, int64_t grid, hipStream_t st)
 {
-    hipLaunchKernelGGL((k_beam_rows<T, KP>), dim3((unsigned)grid), dim3(256), 0, st, a);
+    // Logits past the caches' size are read with the non-temporal hint (512 rows of 131072 in bf16, 134 MB: k = 4 36.3 -> 33.7
+    // us a call, k = 16 38.7 -> 37.5, behind the product that makes them 287.7 -> 285.8 together; 34 MB and less 0.2 to 1 us
+    // slower with it, when they have been read shortly before)
+    if ((int64_t)a.batch * a.beams * a.vocab * (int64_t)sizeof(T) >= (int64_t(96) << 20))
+        hipLaunchKernelGGL((k_beam_rows<T, KP, true>), dim3((unsigned)grid), dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL((k_beam_rows<T, KP, false>), dim3((unsigned)grid), dim3(256), 0, st, a);
     // a wave a list step and a beam, up to 8, or 16 where there are very many lists
     const int64_t lists = (int64_t)a.beams * a.parts, steps = (lists + 64 / KP - 1) / (64 / KP), most = steps > a.beams ? steps : a.beams;
     const int cap = steps > 128 ? 16 : 8;

@@ -276,3 +276,16 @@ def test_scores_in_place(beams, vocab):
     out = (scores, torch.empty_like(want[1]), torch.empty_like(want[2]))
     fp4.beam_select(x, scores, out=out)
     assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_logits_past_the_caches():
+    """Over 96 MB, rows at odd elements: the same bits as from aligned rows, and the definition's choice."""
+    batch, beams, vocab = 130, 4, 100003
+    x = _logits(batch * beams, vocab, torch.bfloat16, 6)
+    scores = -9 * torch.rand(batch, beams, device="cuda", generator=torch.Generator("cuda").manual_seed(3))
+    room = torch.zeros(batch * beams, vocab + 5, dtype=torch.bfloat16, device="cuda")
+    room[:, :vocab] = x
+    got = _check(x, scores, 8)
+    assert all(torch.equal(a, b) for a, b in zip(got, _check(room[:, :vocab], scores, 8)))
+    part = [t.cpu() for t in _fp4().beam_select(x[:4 * beams], scores[:4], k=8)]  # below that size
+    assert all(torch.equal(a, b[:4]) for a, b in zip(part[1:], got[1:]))

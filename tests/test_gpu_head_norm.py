@@ -314,3 +314,20 @@ def test_recorded_calls():
     other = _cache(fp4, "mxfp8", 2, 2, 16, 64)
     fp4.qk_norm_rope_append(other, q, k, v, pos, slots, freqs, w, w, eps=1e-6)
     _same(cache, other)
+
+
+@pytest.mark.parametrize("dtype,dim,rot", [(torch.bfloat16, 128, 128), (torch.float32, 80, 32), (torch.bfloat16, 64, 64)])
+def test_rows_past_the_caches(dtype, dim, rot):
+    """Over 96 MB of rows: every token is what it is in a small call."""
+    fp4 = _fp4()
+    heads, kv = 12, 4
+    n = (110 << 20) // ((heads + kv) * dim * dtype.itemsize)
+    whole = torch.randn(n, heads + kv, dim, device="cuda", generator=torch.Generator("cuda").manual_seed(2)).to(dtype)
+    q, k = whole.split([heads, kv], 1)
+    pos = torch.arange(n, dtype=torch.int32, device="cuda") * 3
+    freqs, w = fp4.rope_frequencies(rot), _weight((dim,), 4)
+    got = fp4.qk_norm_rope(q, k, pos, freqs, w, w, eps=1e-6, dtype=dtype)
+    for at in range(0, n, 9973):
+        s = slice(at, at + 1111)
+        alone = fp4.qk_norm_rope(q[s], k[s], pos[s], freqs, w, w, eps=1e-6, dtype=dtype)
+        assert torch.equal(got[0][s], alone[0]) and torch.equal(got[1][s], alone[1])
