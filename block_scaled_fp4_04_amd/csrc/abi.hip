@@ -1325,10 +1325,10 @@ struct BeamSpace {
     size_t top, value, token, bytes;
 };
 
-BeamSpace beam_space(int64_t rows, int64_t vocab, int64_t k, fp4_dtype xt)
+BeamSpace beam_space(int64_t batch, int64_t beams, int64_t vocab, int64_t k, fp4_dtype xt)
 {
     BeamSpace s;
-    s.parts = rows * beam_parts(rows, vocab, xt);
+    s.parts = batch * beams * beam_shape(batch * beams, beams, vocab, k, xt).parts;
     s.top = align256((size_t)s.parts * 8);
     s.value = s.top + align256((size_t)s.parts * 4);
     s.token = s.value + align256((size_t)(s.parts * k) * 4);
@@ -1505,7 +1505,7 @@ fp4_status kv_cache_copy(const fp4_kv_cache *cache, const int32_t *copies, int64
 size_t beam_select_workspace(int64_t batch, int64_t beams, int64_t vocab, int64_t k, fp4_dtype xt)
 {
     if (!valid_dtype(xt) || !beam_sizes_ok(batch, beams, vocab, k)) return 0;
-    return beam_space(batch * beams, vocab, k, xt).bytes;
+    return beam_space(batch, beams, vocab, k, xt).bytes;
 }
 
 fp4_status beam_select(const void *logits, fp4_dtype xt, int64_t batch, int64_t beams, int64_t vocab, int64_t ld,
@@ -1516,7 +1516,7 @@ fp4_status beam_select(const void *logits, fp4_dtype xt, int64_t batch, int64_t 
     if (!beam_sizes_ok(batch, beams, vocab, k) || end_token < 0 || end_token >= vocab) return FP4_ERR_SHAPE;
     if (!logits || !scores || !out_scores || !out_parents || !out_tokens) return FP4_ERR_NULL;
     if (ld < vocab || (reinterpret_cast<uintptr_t>(logits) % dsize(xt)) != 0) return FP4_ERR_LAYOUT;
-    const BeamSpace sp = beam_space(batch * beams, vocab, k, xt);
+    const BeamSpace sp = beam_space(batch, beams, vocab, k, xt);
     if (!ws || !aligned16(ws) || ws_bytes < sp.bytes) return FP4_ERR_WORKSPACE;
     FP4_TRY(check_device());
     uint8_t *base = reinterpret_cast<uint8_t *>(ws);

@@ -229,31 +229,30 @@ __device__ __forceinline__ float widen(T v)
     else return v;
 }
 
-// A workgroup takes a part of a row, each of its waves a.groups groups one behind the other, the next group's loads in
-// flight; then one wave adds up the four sums and merges the four lists (k = 16, 8 beams of 131072: without that
-// the join has four times the lists, and takes 4 us longer in a batch of 64 groups, 15 us in one of a single group).
+// A workgroup takes a part of a row, each of its W waves a.groups groups one behind the other, the next group's loads in
+// flight; with four waves one of them then adds up the four sums and merges the four lists.
 //
 // First pass: sums of exponentials, and every vector's maximum into LDS.  The k-th largest of the lanes'
 // maxima is then a bar that at least k values reach and all of the k best do.  Second pass: the vectors whose
 // maximum reaches it (about k of them) are listed and read again, and their values put in their places one at a
 // time, the bar rising.
-template <typename T, int KP, bool ONCE>
-__global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a)
+template <typename T, int KP, int W, bool ONCE>
+__global__ __launch_bounds__(64 * W) void k_beam_rows(BeamArgs a)
 {
     constexpr int kPer = Row<T>::kPer, kGroup = kVec * 64 * kPer;
     constexpr float kLowest = -3.4028234663852886e38f;
     const float kInf = __builtin_inff();
-    __shared__ float4 sm_top[4][kMost][64];
-    __shared__ int sm_listed[4][kListed + kVec * 64];
-    __shared__ float sm_ref[4];
-    __shared__ double sm_sum[4];
-    __shared__ Best sm_best[4][KP];
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    __shared__ float4 sm_top[W][kMost][64];
+    __shared__ int sm_listed[W][kListed + kVec * 64];
+    __shared__ float sm_ref[W];
+    __shared__ double sm_sum[W];
+    __shared__ Best sm_best[W][KP];
+    const int wave = W > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0, lane = threadIdx.x & 63;
     const int64_t id = blockIdx.x;
     const int row = (int)(id / a.parts), part = (int)(id - (int64_t)row * a.parts);
     if (a.done && a.done[row]) return;
     const T *x = reinterpret_cast<const T *>(a.logits) + row * a.ld;
-    const int first = (part * 4 + wave) * a.groups * kGroup;
+    const int first = (part * W + wave) * a.groups * kGroup;
     const int groups = min(a.groups, (a.vocab - first + kGroup - 1) / kGroup);  // (<= 0 past the row's end)
     uint32_t w[kVec][4];
     load_group<ONCE>(w, x, first, a.vocab, lane);
@@ -304,7 +303,7 @@ __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a)
             for (int c = 0; c < 4; ++c) w[v][c] = next[v][c];
     }
     sum = wave_sum(sum);
-    if (lane == 0) {
+    if (W > 1 && lane == 0) {
         sm_ref[wave] = ref;
         sm_sum[wave] = sum;
     }
@@ -362,26 +361,30 @@ __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a)
         if (n >= kListed) look();
     }
     look();
-    if (lane < KP) sm_best[wave][lane] = s;  // (lanes from k on hold what was displaced, in order)
-    __syncthreads();
-    if (wave > 0) return;
-    constexpr int kRuns = 64 / KP < 4 ? 64 / KP : 4;
-    const int run = lane / KP;
-    Best best = run < 4 ? sm_best[run < 4 ? run : 0][lane % KP] : Best{-kInf, 0x7FFFFFFF};
+    Best best = s;
+    if constexpr (W > 1) {
+        static_assert(W == 4, "four lists are merged");
+        if (lane < KP) sm_best[wave][lane] = s;  // (lanes from k on hold what was displaced, in order)
+        __syncthreads();
+        if (wave > 0) return;
+        constexpr int kRuns = 64 / KP < W ? 64 / KP : W;
+        const int run = lane / KP;
+        best = run < W ? sm_best[run < W ? run : 0][lane % KP] : Best{-kInf, 0x7FFFFFFF};
 #pragma unroll
-    for (int r = kRuns; r < 4; r += kRuns) merge<KP>(best, sm_best[r + run][lane % KP], lane);
-    merge_wave<KP, KP>(best, lane);
+        for (int r = kRuns; r < W; r += kRuns) merge<KP>(best, sm_best[r + run][lane % KP], lane);
+        merge_wave<KP, KP>(best, lane);
+        ref = fmaxf(fmaxf(sm_ref[0], sm_ref[1]), fmaxf(sm_ref[2], sm_ref[3]));
+        sum = 0.0;
+#pragma unroll
+        for (int r = 0; r < W; ++r) sum += sm_sum[r] * exp_of((double)sm_ref[r] - (double)ref);
+    }
     if (lane < a.k) {
         a.part_value[id * a.k + lane] = best.v;
         a.part_token[id * a.k + lane] = best.i;
     }
     if (lane == 0) {
-        const float most = fmaxf(fmaxf(sm_ref[0], sm_ref[1]), fmaxf(sm_ref[2], sm_ref[3]));
-        double all = 0.0;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) all += sm_sum[r] * exp_of((double)sm_ref[r] - (double)most);
-        a.part_top[id] = most;
-        a.part_sum[id] = all;
+        a.part_top[id] = ref;
+        a.part_sum[id] = sum;
     }
 }
 
@@ -493,15 +496,20 @@ __global__ __launch_bounds__(1024) void k_beam_join(BeamArgs a)
 }
 
 template <typename T, int KP>
-void launch_kp(const BeamArgs &a, int64_t grid, hipStream_t st)
+void launch_kp(const BeamArgs &a, const BeamShape &shape, hipStream_t st)
 {
+    const dim3 grid((unsigned)((int64_t)a.batch * a.beams * a.parts));
     // Logits past the caches' size are read with the non-temporal hint (512 rows of 131072 in bf16, 134 MB: k = 4 36.3 -> 33.7
     // us a call, k = 16 38.7 -> 37.5, behind the product that makes them 287.7 -> 285.8 together; 34 MB and less 0.2 to 1 us
     // slower with it, when they have been read shortly before)
-    if ((int64_t)a.batch * a.beams * a.vocab * (int64_t)sizeof(T) >= (int64_t(96) << 20))
-        hipLaunchKernelGGL((k_beam_rows<T, KP, true>), dim3((unsigned)grid), dim3(256), 0, st, a);
-    else
-        hipLaunchKernelGGL((k_beam_rows<T, KP, false>), dim3((unsigned)grid), dim3(256), 0, st, a);
+    const bool once = (int64_t)a.batch * a.beams * a.vocab * (int64_t)sizeof(T) >= (int64_t(96) << 20);
+    if (shape.waves == 1) {
+        if (once) hipLaunchKernelGGL((k_beam_rows<T, KP, 1, true>), grid, dim3(64), 0, st, a);
+        else hipLaunchKernelGGL((k_beam_rows<T, KP, 1, false>), grid, dim3(64), 0, st, a);
+    } else {
+        if (once) hipLaunchKernelGGL((k_beam_rows<T, KP, 4, true>), grid, dim3(256), 0, st, a);
+        else hipLaunchKernelGGL((k_beam_rows<T, KP, 4, false>), grid, dim3(256), 0, st, a);
+    }
     // a wave a list step and a beam, up to 8, or 16 where there are very many lists
     const int64_t lists = (int64_t)a.beams * a.parts, steps = (lists + 64 / KP - 1) / (64 / KP), most = steps > a.beams ? steps : a.beams;
     const int cap = steps > 128 ? 16 : 8;
@@ -510,41 +518,44 @@ void launch_kp(const BeamArgs &a, int64_t grid, hipStream_t st)
     hipLaunchKernelGGL(k_beam_join<KP>, dim3((unsigned)a.batch), dim3(64 * waves), 0, st, a);
 }
 
-// lists of a power of two of places
 template <typename T>
-void launch_k(const BeamArgs &a, int64_t grid, hipStream_t st)
+void launch_k(const BeamArgs &a, const BeamShape &shape, hipStream_t st)
 {
-    if (a.k <= 4) launch_kp<T, 4>(a, grid, st);
-    else if (a.k <= 8) launch_kp<T, 8>(a, grid, st);
-    else if (a.k <= 16) launch_kp<T, 16>(a, grid, st);
-    else if (a.k <= 32) launch_kp<T, 32>(a, grid, st);
-    else launch_kp<T, 64>(a, grid, st);
-}
-
-// Groups of a wave: as many as leave the chip a wave a SIMD (fewer lists to join; 4 / 2 / 1 waves a SIMD: 16 groups of 8
-// beams of 131072 tokens 21.3 / 19.5 / 19.1 us, 32 of 5 of 50003 19.9 / 20.0 / 16.2 us, the others alike)
-int groups_of(int64_t rows, int64_t vocab, fp4_dtype xt)
-{
-    const int64_t group = kVec * 64 * (xt == FP4_BF16 ? 8 : 4);
-    const int64_t all = rows * ((vocab + group - 1) / group) / (4 * device_cu_count());
-    return all < 1 ? 1 : all > kMost ? kMost : (int)all;
+    if (a.k <= 4) launch_kp<T, 4>(a, shape, st);
+    else if (a.k <= 8) launch_kp<T, 8>(a, shape, st);
+    else if (a.k <= 16) launch_kp<T, 16>(a, shape, st);
+    else if (a.k <= 32) launch_kp<T, 32>(a, shape, st);
+    else launch_kp<T, 64>(a, shape, st);
 }
 
 }  // namespace
 
-int64_t beam_parts(int64_t rows, int64_t vocab, fp4_dtype xt)
+// Groups of a wave: as many as leave the chip a wave a SIMD (fewer lists to join; 4 / 2 / 1 waves a SIMD: 16 groups of 8
+// beams of 131072 tokens 21.3 / 19.5 / 19.1 us, 32 of 5 of 50003 19.9 / 20.0 / 16.2 us, the others alike).
+// Waves of a workgroup: one where its lists are few enough for one step of the join's 8 waves, else four, which merge
+// theirs (one / four, us a call: 4 beams of 32000, k = 4, 10.1 / 11.6; 64 batches of it 13.5 / 15.1; 512 of 8 beams, k = 16,
+// 66.1 / 81.9; 4096 of 4 beams of 4000 tokens 66.6 / 147; past that step, 64 of 8 beams of 131072, k = 16, 39.1 / 37.5).
+BeamShape beam_shape(int64_t rows, int64_t beams, int64_t vocab, int64_t k, fp4_dtype xt)
 {
-    const int64_t part = 4 * kVec * 64 * (xt == FP4_BF16 ? 8 : 4) * groups_of(rows, vocab, xt);
-    return (vocab + part - 1) / part;
+    const int64_t group = kVec * 64 * (xt == FP4_BF16 ? 8 : 4);
+    const int64_t all = rows * ((vocab + group - 1) / group) / (4 * device_cu_count());
+    BeamShape s;
+    s.groups = all < 1 ? 1 : all > kMost ? kMost : (int)all;
+    int64_t kp = 4;  // places of a list (launch_k)
+    while (kp < k) kp <<= 1;
+    const int64_t alone = (vocab + group * s.groups - 1) / (group * s.groups);
+    s.waves = beams * alone * kp <= 8 * 64 ? 1 : 4;
+    s.parts = s.waves == 1 ? alone : (vocab + 4 * group * s.groups - 1) / (4 * group * s.groups);
+    return s;
 }
 
 fp4_status launch_beam_select(BeamArgs a, fp4_dtype xt, hipStream_t st)
 {
-    const int64_t rows = (int64_t)a.batch * a.beams;
-    a.parts = (int)beam_parts(rows, a.vocab, xt);
-    a.groups = groups_of(rows, a.vocab, xt);
-    if (xt == FP4_BF16) launch_k<uint16_t>(a, rows * a.parts, st);
-    else launch_k<float>(a, rows * a.parts, st);
+    const BeamShape shape = beam_shape((int64_t)a.batch * a.beams, a.beams, a.vocab, a.k, xt);
+    a.parts = (int)shape.parts;
+    a.groups = shape.groups;
+    if (xt == FP4_BF16) launch_k<uint16_t>(a, shape, st);
+    else launch_k<float>(a, shape, st);
     return hipGetLastError() == hipSuccess ? FP4_OK : FP4_ERR_HIP;
 }
 

@@ -300,7 +300,12 @@ struct BeamArgs {
     int32_t *out_parents, *out_tokens;
 };
 
-int64_t beam_parts(int64_t rows, int64_t vocab, fp4_dtype xt);  // of a row
+struct BeamShape {
+    int waves, groups;  // waves of a workgroup, groups of a wave
+    int64_t parts;      // workgroups of a row
+};
+
+BeamShape beam_shape(int64_t rows, int64_t beams, int64_t vocab, int64_t k, fp4_dtype xt);
 fp4_status launch_beam_select(BeamArgs a, fp4_dtype xt, hipStream_t st);
 
 }  // namespace fp4k

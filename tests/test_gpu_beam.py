@@ -289,3 +289,15 @@ def test_logits_past_the_caches():
     assert all(torch.equal(a, b) for a, b in zip(got, _check(room[:, :vocab], scores, 8)))
     part = [t.cpu() for t in _fp4().beam_select(x[:4 * beams], scores[:4], k=8)]  # below that size
     assert all(torch.equal(a, b[:4]) for a, b in zip(part[1:], got[1:]))
+
+
+@pytest.mark.parametrize("batch,beams,vocab,k,dtype", [(270, 4, 50001, 8, torch.bfloat16), (310, 7, 12503, 14, torch.float32)])
+def test_many_short_rows_past_the_caches(batch, beams, vocab, k, dtype):
+    """Over 96 MB in rows that few waves read, some of them ended: the definition's choice, alone and among others."""
+    x = _logits(batch * beams, vocab, dtype, 7)
+    g = torch.Generator("cuda").manual_seed(5)
+    scores = -9 * torch.rand(batch, beams, device="cuda", generator=g)
+    done = torch.rand(batch, beams, device="cuda", generator=g) < 0.2
+    got = _check(x, scores, k, done=done, end=3)
+    one = [t.cpu() for t in _fp4().beam_select(x[:beams], scores[:1], k=k, done=done[:1], end_token=3)]
+    assert all(torch.equal(a, b[:1]) for a, b in zip(one[1:], got[1:]))
