@@ -1505,7 +1505,8 @@ def kv_pages_reorder(block_table: torch.Tensor, seq_lens: torch.Tensor, parents:
                      out: torch.Tensor | None = None, copies: torch.Tensor | None = None) -> torch.Tensor:
     """Block-table rows of beams after a selection: parents int32 [batch, beams] (beam_select's), row
     j of a group takes the row of beam parents[j], in place or into `out`.  The rows of a group have
-    the same length.  Returns int32 [batch * beams, 3]: what kv_cache_copy has to copy in every layer's cache,
+    the same length (where the pool ran out under some of them, entries of -1 keep other sequences' pages
+    out).  Returns int32 [batch * beams, 3]: what kv_cache_copy has to copy in every layer's cache,
     because a partly filled page belongs to one row only."""
     seqs, width, stride = _block_table(block_table)
     if parents.dtype != torch.int32:

@@ -5,7 +5,7 @@
 // All of it is a few integers a sequence, a token or a table entry: bound by the launch and by chains of
 // dependent loads and scans, not by bytes, so the small calls are one workgroup and one launch (64 sequences of one token
 // 3.1 us; 300 sequences and 32000 tokens in two launches 4.6 + 3.3 us; the free list of 26000 pages from 512 rows
-// 4.3 + 5.2 us; tables of 288 beams 4.4 us and their page copies 5.1 us).  Results do not depend on
+// 4.3 + 5.2 us; tables of 288 beams 4.8 us and their page copies 5.2 us).  Results do not depend on
 // the order of workgroups: sums are prefix sums, and no entry is written by one workgroup and read by another
 // of the same launch.
 #include "device_common.h"
@@ -352,6 +352,9 @@ __global__ __launch_bounds__(1024) void k_pages_sweep(PageArgs a, int64_t words)
 // partly filled page belongs to one row alone, so of several children of a parent the first keeps its
 // page and each further one needs a copy.  There are as many further children as rows without a child,
 // and the m-th further child takes the page of the m-th such row to copy into: no page is dealt.
+// Rows of a group differ in length where a pool ran out under some of them.  Only a row's
+// own partly filled page is ever copied into (what its length does not cover may be another sequence's, full
+// pages may be shared), and entries that the parent does not give become -1.
 
 constexpr int kTile = 256;  // table columns of a workgroup
 
@@ -372,12 +375,13 @@ __global__ __launch_bounds__(256) void k_pages_reorder(BeamTableArgs a)
         tile[j * kTile + threadIdx.x] = col < a.width ? a.table[(row0 + j) * a.table_stride + col] : -1;
 
     // every wave: its lane's row, the rows with a child, the further children
-    int parent = lane, len = 0;
+    int parent = lane, own = 0;
     if (lane < a.beams) {
         const int p = a.parents[row0 + lane];
         if (p >= 0 && p < a.beams) parent = p;
-        len = max(a.seq_lens[row0 + parent], 0);
+        own = max(a.seq_lens[row0 + lane], 0);
     }
+    const int len = __shfl(own, parent, kWave);
     uint64_t children = 0;
     bool further = false;
     for (int s = 0; s < a.beams; ++s) {
@@ -387,17 +391,20 @@ __global__ __launch_bounds__(256) void k_pages_reorder(BeamTableArgs a)
     }
     const uint64_t more = __ballot(further && lane < a.beams);
     const uint64_t dropped = ~children & (~0ull >> (64 - a.beams));  // as many as `more`
+    // a further child's row to take the page of (-1: that row has no partly filled page there)
+    const int at = len >> a.page_shift, off = len & ((1 << a.page_shift) - 1);
+    int spare = further ? nth_bit(dropped, __builtin_popcountll(more & ((1ull << lane) - 1))) : lane;
+    if ((uint32_t)(__shfl(own, spare, kWave) - (len - off)) - 1u >= (1u << a.page_shift) - 1u) spare = -1;
     __syncthreads();
 
     if (threadIdx.x < 64 && lane < a.beams) {
-        const int at = len >> a.page_shift, off = len & ((1 << a.page_shift) - 1);
-        const bool copied = further && off > 0 && at < a.width;
+        const bool copied = further && off > 0 && at < a.width && spare >= 0;
         if ((copied ? at / kTile : 0) == part) {  // the workgroup of the last page's column
             int32_t *rec = a.copies + (row0 + lane) * 3;
             int32_t src = -1, dst = -1;
             if (copied) {
                 src = tile[parent * kTile + at % kTile];
-                dst = tile[nth_bit(dropped, __builtin_popcountll(more & ((1ull << lane) - 1))) * kTile + at % kTile];
+                dst = tile[spare * kTile + at % kTile];
             }
             rec[0] = src;
             rec[1] = dst;
@@ -406,11 +413,12 @@ __global__ __launch_bounds__(256) void k_pages_reorder(BeamTableArgs a)
     }
     for (int j = 0; j < a.beams; ++j) {
         const int p = __builtin_amdgcn_readlane(parent, j), n = __builtin_amdgcn_readlane(len, j);
-        const int at = n >> a.page_shift, off = n & ((1 << a.page_shift) - 1);
-        if (col >= a.width || col >= at + (off > 0)) continue;
-        const bool heir = col == at && ((more >> j) & 1ull);
-        const int from = heir ? nth_bit(dropped, __builtin_popcountll(more & ((1ull << j) - 1))) : p;
-        a.out[(row0 + j) * a.out_stride + col] = tile[from * kTile + threadIdx.x];
+        const int last = n >> a.page_shift, part_of = n & ((1 << a.page_shift) - 1), mine = __builtin_amdgcn_readlane(own, j);
+        const bool given = col < last + (part_of > 0);
+        if (col >= a.width || !(given || (int64_t)col << a.page_shift < mine)) continue;
+        const bool heir = col == last && ((more >> j) & 1ull);
+        const int from = !given ? -1 : heir ? __builtin_amdgcn_readlane(spare, j) : p;
+        a.out[(row0 + j) * a.out_stride + col] = from >= 0 ? tile[from * kTile + threadIdx.x] : -1;
     }
 }
 

@@ -663,7 +663,7 @@ fp4_status kv_pages_collect(const fp4_kv_pages *pool, const int32_t *block_table
  * its parent.
  *  block_table, out device int32 [batch * beams][stride]; out may be block_table itself (with the same
  *         stride; another overlap is not allowed).
- *  seq_lens int32 [batch * beams]; the rows of a group have the same length.
+ *  seq_lens int32 [batch * beams]; the rows of a group have the same length (below where they do not).
  *  parents int32 [batch * beams], each in [0, beams) (another value: the row keeps its own).
  *  copies int32 [batch * beams][3], out: {source page, destination page, tokens}, or
  *         {-1, -1, 0}.
@@ -672,6 +672,9 @@ fp4_status kv_pages_collect(const fp4_kv_pages *pool, const int32_t *block_table
  * the partly filled page of a row that has no child, into which the parent's tokens have to be copied
  * (kv_cache_copy, once for each layer's cache).  Pages that no row holds any more come back with
  * kv_pages_collect.  Entries past a row's pages are left as they are.
+ * Where the lengths differ (the pool ran out under some rows of a group) the group's tokens are lost, but no
+ * other sequence's: a child whose spare row has no partly filled page there gets entry -1 and no copy, and
+ * entries that a row's length covers but its parent's does not become -1.
  * beams <= 64; batch * ceil(table_width / 256) < 2^24 (FP4_ERR_SHAPE). */
 fp4_status kv_pages_reorder(const int32_t *block_table, int64_t batch, int64_t beams, int64_t table_width,
                             int64_t table_stride, const int32_t *seq_lens, const int32_t *parents,

@@ -301,6 +301,37 @@ def test_reorder_bad_lengths_stay_inside():
     assert torch.equal(room[mask], before[mask])
 
 
+@pytest.mark.parametrize("beams,width,page", [(4, 5, 16), (8, 300, 16), (64, 3, 32)])
+@pytest.mark.parametrize("aside", [False, True])
+def test_reorder_uneven_lengths_touch_no_other_page(beams, width, page, aside):
+    """A pool that ran out under some beams leaves lengths that differ and, past them, entries of earlier sequences:
+    none is copied into or from, or comes within a row's own or its parent's length."""
+    fp4 = _fp4()
+    batch, rows = 5, 5 * beams
+    rng = torch.Generator().manual_seed(beams)
+    for _ in range(6):
+        lens = torch.randint(0, width * page + 1, (rows,), generator=rng, dtype=torch.int32)
+        short = torch.randint(0, 2, (rows,), generator=rng, dtype=torch.int32)
+        lens[beams:] = lens[beams:].view(batch - 1, beams)[:, :1].repeat(1, beams).flatten()  # off by a token at most
+        lens[beams:] = (lens[beams:] - short[beams:]).clamp(min=0)
+        held = torch.arange(width) < -(-lens // page)[:, None]
+        own = torch.arange(rows * width, dtype=torch.int32).view(rows, width)
+        table = torch.where(held, own, 100000 + own)                       # from 100000 on: others' pages
+        parents = torch.randint(0, beams, (batch, beams), generator=rng, dtype=torch.int32)
+        dev = table.cuda()
+        out = torch.full_like(dev, 200000) if aside else dev
+        copies = fp4.kv_pages_reorder(dev, lens.cuda(), parents.cuda(), page, out=out).cpu()
+        assert int(copies[:, :2].max()) < 100000
+        of = (torch.arange(batch)[:, None] * beams + parents).flatten().long()
+        live = held | held[of]
+        assert int(out.cpu()[live].max()) < 100000
+        full = torch.arange(width) < (lens[of] // page)[:, None]           # the parent's full pages, whatever the lengths
+        assert torch.equal(out.cpu()[full], table[of][full])
+        to = copies[copies[:, 1] >= 0, 1]
+        assert to.unique().numel() == to.numel()
+        assert torch.equal(lens[to.long() // width] // page, to % width) and bool((lens[to.long() // width] % page > 0).all())
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "mxfp8", "nvfp4", "mxfp4"])
 @pytest.mark.parametrize("dim,heads,page", [(64, 1, 16), (128, 3, 64), (256, 2, 256)])
 def test_copy(fmt, dim, heads, page):
