@@ -1299,8 +1299,8 @@ def _norm_args(n, q_heads, k_heads, d, positions, freqs, q_weight, k_weight, eps
         if q_weight is not None or k_weight is not None:
             raise ValueError("weights belong to a norm: give eps")
     else:
-        if not eps > 0:
-            raise ValueError(f"eps must be positive (None: no norm), got {eps}")
+        if not 1e-30 <= eps <= 1e30:  # (a smaller one is 0 in fp32: no norm)
+            raise ValueError(f"eps must be in [1e-30, 1e30] (None: no norm), got {eps}")
         if q_weight is None or (k_weight is None and k_heads > 0):
             raise ValueError("a norm needs its weights (ones for none)")
         qs = _head_weight(q_weight, q_heads, d, "q_weight")

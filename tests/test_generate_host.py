@@ -193,6 +193,14 @@ def test_binding_refuses_norms(fp4):
             fp4.qk_norm_rope(**{**good, **bad})
 
 
+@pytest.mark.parametrize("eps", [1e-60, 1e-31, 0.0, -1e-6, 1e31, 1e300, float("nan"), float("inf")])
+def test_binding_refuses_eps(fp4, eps):
+    """1e-60 is 0 in fp32, which asks the library for no norm."""
+    q, w = torch.zeros(8, 4, 64, dtype=torch.bfloat16), torch.ones(64)
+    with pytest.raises(ValueError, match="eps"):
+        fp4.qk_norm_rope(q, None, None, None, w, None, eps)
+
+
 def test_binding_refuses_pages(fp4):
     with pytest.raises(ValueError):
         fp4.KVPages(_i32(4), _i32(2), 24)
