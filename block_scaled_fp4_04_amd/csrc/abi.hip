@@ -1336,7 +1336,7 @@ BeamSpace beam_space(int64_t batch, int64_t beams, int64_t vocab, int64_t k, fp4
     return s;
 }
 
-// (a launch holds fewer than 2^32 threads: 256 for at least 4096 logits, 1024 for a group)
+// (a launch holds fewer than 2^32 threads: 64 for every 1024 logits of a row or part of them, at most 1024 for a group)
 bool beam_sizes_ok(int64_t batch, int64_t beams, int64_t vocab, int64_t k)
 {
     return batch > 0 && batch < (1 << 21) && beams > 0 && beams <= 64 && vocab > 0 && vocab <= (int64_t(1) << 30) / beams &&
