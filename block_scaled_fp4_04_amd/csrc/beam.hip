@@ -11,9 +11,12 @@
 //
 // Order: totals are compared in 64 bits (in 32, sums of scores around -50 and small differences of logits
 // would merge neighbours), equal ones by beam * vocab + token.  The sums of exponentials are fp32 over a lane's values of
-// a group (32 or 16, by halves) and 64 bits from there on.  The exponentials are fp32 (v_exp_f32, 1 ulp, of an argument
-// d with two roundings): a term e^-d is off by at most (1 + 2 d) 2^-23 of itself, so a sum by less than 2^-18 where
-// what is 30 below the maximum does not count, and by about 2^-25 in practice, as the errors have either sign.
+// a group (32 or 16, by halves) and 64 bits from there on.  The exponentials are fp32, e^a of a = logit - reference: v_exp_f32
+// is within 1 ulp, and a's two roundings and that of log2 e weigh 1.2 |a| 2^-23 at most.  The reference is a wave's first
+// maximum until a value is more than 8 above it, so a term d below the row's maximum has |a| <= max(8, d), and the mean of that
+// over a row's N terms, each weighed by its share, is at most max(9, ln N) (entropy).  The additions and the exponentials
+// that match two references are 5 ulp at most.  So a row's sum is within (7 + 1.2 max(9, ln N)) 2^-23 of itself: less than
+// 2^-18 for any row, and about 2^-25 in practice, as the errors have either sign.
 #include "device_common.h"
 #include "internal.h"
 
@@ -113,8 +116,12 @@ __device__ __forceinline__ float wave_top(float v)
     return fmaxf(fmaxf(lane_of(v, 0), lane_of(v, 16)), fmaxf(lane_of(v, 32), lane_of(v, 48)));
 }
 
-// e^d, d <= 0, by v_exp_f32: the rounding of its argument, 2^-24 |d|, weighs e^d
-__device__ __forceinline__ double exp_of(double d) { return (double)__builtin_amdgcn_exp2f((float)(d * 1.4426950408889634)); }
+// e^d, d <= 0, by v_exp_f32 of what is left of a whole power of two: the rounding of that argument does not grow with d
+__device__ __forceinline__ double exp_of(double d)
+{
+    const double x = fmax(d * 1.4426950408889634, -2000.0), n = __builtin_rint(x);
+    return __builtin_amdgcn_ldexp((double)__builtin_amdgcn_exp2f((float)(x - n)), (int)n);
+}
 
 template <typename Get>
 __device__ __forceinline__ double moved(double v, Get get)
@@ -257,8 +264,8 @@ __global__ __launch_bounds__(64 * W) void k_beam_rows(BeamArgs a)
     uint32_t w[kVec][4];
     load_group<ONCE>(w, x, first, a.vocab, lane);
 
-    // Exponentials are taken against the first group's maximum `ref` until one would be e^80 times as large.
-    // (2^(x log2e - c) is one instruction less a value, but then not even the largest term is exact.)
+    // Exponentials are taken against the first group's maximum `ref` until a value is more than 8 above it (rounding, above).
+    // (2^(x log2e - c) is one instruction less a value, but then a term at the reference is not exact.)
     float top = -kInf;  // NaN is passed over here and spoils the sum
 #pragma unroll
     for (int v = 0; v < kVec; ++v)
@@ -279,7 +286,7 @@ __global__ __launch_bounds__(64 * W) void k_beam_rows(BeamArgs a)
         sm_top[wave][g][lane] = make_float4(m[0], m[1], m[2], m[3]);
         const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
         top = fmaxf(top, most);
-        if (__ballot(most - ref > 80.0f)) {
+        if (__ballot(most - ref > 8.0f)) {
             const float now = wave_top(most);
             sum *= exp((double)ref - (double)now);
             ref = now;
@@ -437,8 +444,8 @@ __global__ __launch_bounds__(1024) void k_beam_join(BeamArgs a)
             const float t = p < a.parts ? a.part_top[at + p] : -__builtin_inff();
             const double u = p < a.parts ? a.part_sum[at + p] : 0.0;
             const float now = fmaxf(top, wave_top(t));
-            sum = (top == -__builtin_inff() ? 0.0 : sum * exp_of((double)top - (double)now)) +
-                  (p < a.parts ? u * exp_of((double)t - (double)now) : 0.0);
+            if (p0 > 0 && now > top) sum *= exp((double)top - (double)now);
+            sum += p < a.parts ? u * exp_of((double)t - (double)now) : 0.0;
             top = now;
         }
         const double rest = log(wave_sum(sum));

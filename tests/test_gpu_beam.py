@@ -301,3 +301,27 @@ def test_many_short_rows_past_the_caches(batch, beams, vocab, k, dtype):
     got = _check(x, scores, k, done=done, end=3)
     one = [t.cpu() for t in _fp4().beam_select(x[:beams], scores[:1], k=k, done=done[:1], end_token=3)]
     assert all(torch.equal(a, b[:1]) for a, b in zip(one[1:], got[1:]))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("wide", [False, True])
+def test_best_far_above_where_a_row_begins(dtype, wide):
+    """Peaks (one value, or a plateau of 4096) from 0 to 90 above a row's first values, anywhere in it, in rows of which a wave
+    walks several groups: a row's sum is within the documented 2^-18 wherever its largest terms stand, and a score's own
+    rounding is 2^-24 of it more.  The peaks' tokens are the definition's."""
+    rows, vocab, k = 1024, 16384, 4
+    g = torch.Generator("cuda").manual_seed(11)
+    x = 16 * torch.rand(rows, vocab, device="cuda", generator=g) - 8
+    up = torch.linspace(0, 90, rows, device="cuda")
+    if wide:
+        x[:, vocab // 2:vocab // 2 + 4096] += up[:, None]
+    else:
+        at = torch.randint(0, vocab, (rows,), device="cuda", generator=g)
+        x[torch.arange(rows, device="cuda"), at] = 8 + up
+    x = x.to(dtype)
+    scores = torch.zeros(rows, 1, device="cuda")
+    s, p, t = _fp4().beam_select(x, scores, k=k)
+    best, order = torch.sort(_totals(x, scores, None, 0), dim=-1, descending=True, stable=True)
+    err = (s.cpu().double() - best[:, :k]).abs() - 2.0 ** -24 * best[:, :k].abs()
+    assert float(err.max()) <= 2.0 ** -18, (float(err.max()) * 2 ** 18, int((err > 2.0 ** -18).any(1).sum()))
+    assert torch.equal(t.cpu().long(), order[:, :k])  # (one beam: the order is that of its logits)
