@@ -1560,7 +1560,8 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: int | None = None
     bf16, scores float32 [batch, beams] (the beams' log probabilities so far; -inf: the beam offers
     nothing), done bool or uint8 [batch, beams] (the beam has ended and offers end_token at its own
     score).  Returns (scores float32, parents int32, tokens int32), each [batch, k], best first, ties to the lowest
-    beam, then token; what nothing speaks for (-inf) comes last in that order.  `out`: those three, to write
+    beam, then (of one beam) the larger logit, then token; what nothing speaks for (-inf) comes last in the order of beam
+    and token.  `out`: those three, to write
     into; its scores may be `scores`."""
     dt = _dt(logits)
     if logits.dim() != 2:

@@ -10,7 +10,8 @@
 // selection, 19 us is the time of a load-only pass) and the join of 64 groups, k = 16, 6.6 us.
 //
 // Order: totals are compared in 64 bits (in 32, sums of scores around -50 and small differences of logits
-// would merge neighbours), equal ones by beam * vocab + token.  The sums of exponentials are fp32 over a lane's values of
+// would merge neighbours), equal ones by beam, logit and token: beside a score of -10^30, or a maximum 10^17 times as large, 64 bits
+// hold no difference of logits either, and a beam's list has to be as sorted by totals as it is by logits.  The sums of exponentials are fp32 over a lane's values of
 // a group (32 or 16, by halves) and 64 bits from there on.  The exponentials are fp32, e^a of a = logit - reference: v_exp_f32
 // is within 1 ulp, and a's two roundings and that of log2 e weigh 1.2 |a| 2^-23 at most.  The reference is a wave's first
 // maximum until a value is more than 8 above it, so a term d below the row's maximum has |a| <= max(8, d), and the mean of that
@@ -123,9 +124,10 @@ __device__ __forceinline__ double exp_of(double d)
     return __builtin_amdgcn_ldexp((double)__builtin_amdgcn_exp2f((float)(x - n)), (int)n);
 }
 
-template <typename Get>
-__device__ __forceinline__ double moved(double v, Get get)
+template <typename V, typename Get>
+__device__ __forceinline__ V moved(V v, Get get)
 {
+    static_assert(sizeof(V) == 8, "two words");
     uint64_t u;
     __builtin_memcpy(&u, &v, 8);
     u = ((uint64_t)(uint32_t)get((int)(u >> 32)) << 32) | (uint32_t)get((int)u);
@@ -147,13 +149,14 @@ __device__ __forceinline__ double wave_sum(double v)
 
 struct Entry {
     double total;
-    uint32_t flat;  // beam * vocab + token
+    uint64_t place;  // beam, the logit's order from above, token; kNowhere: none
 };
+constexpr uint64_t kNowhere = ~0ull;  // (beams * vocab <= 2^30: beam and token take 31 bits at most)
 
 __device__ __forceinline__ bool better(const Best &x, const Best &y) { return x.v > y.v || (x.v == y.v && x.i < y.i); }
 __device__ __forceinline__ bool better(const Entry &x, const Entry &y)
 {
-    return x.total > y.total || (x.total == y.total && x.flat < y.flat);
+    return x.total > y.total || (x.total == y.total && x.place < y.place);
 }
 
 template <int M>
@@ -164,7 +167,8 @@ __device__ __forceinline__ Best lane_xor(const Best &x)
 template <int M>
 __device__ __forceinline__ Entry lane_xor(const Entry &x)
 {
-    return Entry{moved(x.total, [](int v) { return lane_xor<M>(v); }), (uint32_t)lane_xor<M>((int)x.flat)};
+    auto get = [](int v) { return lane_xor<M>(v); };
+    return Entry{moved(x.total, get), moved(x.place, get)};
 }
 
 // x: a bitonic run of 2 D lanes -> sorted, best first
@@ -456,13 +460,15 @@ __global__ __launch_bounds__(1024) void k_beam_join(BeamArgs a)
     }
     __syncthreads();
 
-    Entry best{-kInf, ~0u};
+    const int token_bits = 32 - __builtin_clz((a.vocab - 1) | 1);
+    Entry best{-kInf, kNowhere};
     for (int l0 = wave * kPer; l0 < lists; l0 += waves * kPer) {
         if (l0 != wave * kPer) load(l0 + lane / KP, v, token, beam);
-        Entry e{-kInf, ~0u};
+        Entry e{-kInf, kNowhere};
         if (v > -__builtin_inff()) {
             const double total = ((double)v - (double)from[beam]) + base[beam];
-            if (total > -kInf) e = Entry{total, (uint32_t)beam * (uint32_t)a.vocab + token};  // (NaN is not)
+            const uint32_t below = ~order_of(v + 0.0f);  // (-0 and 0 are equal)
+            if (total > -kInf) e = Entry{total, ((((uint64_t)beam << 32) | below) << token_bits) | token};  // (NaN is not)
         }
         if (l0 == wave * kPer) best = e;
         else merge<KP>(best, e, lane);
@@ -473,7 +479,7 @@ __global__ __launch_bounds__(1024) void k_beam_join(BeamArgs a)
         __syncthreads();
         if (wave > 0) return;
         for (int w = lane / KP; w - lane / KP < waves; w += kPer) {
-            const Entry e = w < waves ? found[w][slot] : Entry{-kInf, ~0u};
+            const Entry e = w < waves ? found[w][slot] : Entry{-kInf, kNowhere};
             if (w < kPer) best = e;
             else merge<KP>(best, e, lane);
         }
@@ -481,24 +487,30 @@ __global__ __launch_bounds__(1024) void k_beam_join(BeamArgs a)
     }
     // Fewer totals above -infinity than places: all of them are chosen, and the others follow in the order of beam and
     // token, that is the n-th number that is not among the chosen ones: x = n + how many of them are <= x.
-    const int real = __builtin_popcountll(__ballot(lane < a.k && best.flat != ~0u));
+    const bool is_real = best.place != kNowhere;
+    const int real = __builtin_popcountll(__ballot(lane < a.k && is_real));
+    uint32_t parent = (uint32_t)(best.place >> (32 + token_bits));
+    token = (uint32_t)best.place & ((1u << token_bits) - 1u);
     if (real < a.k) {
-        const uint32_t n = (uint32_t)(lane - real);
+        const uint32_t n = (uint32_t)(lane - real), flat = parent * (uint32_t)a.vocab + token;
         uint32_t x = n;
         for (bool more = true; more;) {
             uint32_t y = n;
-            for (int i = 0; i < real; ++i) y += (uint32_t)__builtin_amdgcn_readlane((int)best.flat, i) <= x;
+            for (int i = 0; i < real; ++i) y += (uint32_t)__builtin_amdgcn_readlane((int)flat, i) <= x;
             more = __ballot(lane >= real && y != x) != 0;
             x = y;
         }
-        if (lane >= real) best = Entry{-kInf, x};
+        if (lane >= real) {
+            best.total = -kInf;
+            parent = x / (uint32_t)a.vocab;
+            token = x - parent * (uint32_t)a.vocab;
+        }
     }
     if (lane < a.k) {
         const int64_t at = (int64_t)blockIdx.x * a.k + lane;
-        const uint32_t i = best.flat / (uint32_t)a.vocab;
         a.out_scores[at] = (float)best.total;
-        a.out_parents[at] = (int32_t)i;
-        a.out_tokens[at] = (int32_t)(best.flat - i * (uint32_t)a.vocab);
+        a.out_parents[at] = (int32_t)parent;
+        a.out_tokens[at] = (int32_t)token;
     }
 }
 

@@ -692,7 +692,8 @@ size_t beam_select_workspace(int64_t batch, int64_t beams, int64_t vocab, int64_
 
 /* Beam search's selection: for each of `batch` groups the k best of all beams' continuations,
  *   total(i, v) = score_i + logit_iv - log sum_u exp(logit_iu),
- * best first, equal ones by beam, then token.
+ * best first, equal ones by beam, then token (of one beam's: the larger logit first, also where its score leaves no
+ * difference of logits in 64 bits).
  *  logits [batch * beams][ld] fp32 or bf16 (xt), ld >= vocab, any alignment of an element.
  *  scores fp32 [batch * beams], finite, or -infinity (NaN counts as such): the beam offers nothing.
  *  done   optional uint8 [batch * beams]: nonzero: the beam has ended and offers one
@@ -702,7 +703,8 @@ size_t beam_select_workspace(int64_t batch, int64_t beams, int64_t vocab, int64_
  * Totals of -infinity (masked tokens, beams that offer nothing; a row that holds a NaN or +infinity counts as
  * such) come last, in the order of beam and token, so that every place names a beam and a token.
  *  ws     beam_select_workspace() bytes, 16-byte aligned.
- * Totals are compared in 64 bits; a row's sum is within 2^-18 relative.  1 <= k <= 64,
+ * Totals are compared in 64 bits.  A row's sum is within 2^-18 relative: totals of two beams nearer than 2^-17 may stand
+ * in either order, those of one beam always stand in the order of its logits.  1 <= k <= 64,
  * k <= beams * vocab, beams <= 64, beams * vocab <= 2^30, 0 <= end_token < vocab, batch < 2^21,
  * batch * beams * ceil(vocab / 4096) < 2^24 (FP4_ERR_SHAPE). */
 fp4_status beam_select(const void *logits, fp4_dtype xt, int64_t batch, int64_t beams, int64_t vocab, int64_t ld,

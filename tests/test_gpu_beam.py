@@ -325,3 +325,43 @@ def test_best_far_above_where_a_row_begins(dtype, wide):
     err = (s.cpu().double() - best[:, :k]).abs() - 2.0 ** -24 * best[:, :k].abs()
     assert float(err.max()) <= 2.0 ** -18, (float(err.max()) * 2 ** 18, int((err > 2.0 ** -18).any(1).sum()))
     assert torch.equal(t.cpu().long(), order[:, :k])  # (one beam: the order is that of its logits)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("low", [-1e30, torch.finfo(torch.float32).min])
+@pytest.mark.parametrize("vocab", [3, 7, 300, 20000, 140000])
+def test_scores_that_swallow_logits(vocab, low, dtype):
+    """Beams held back by a score beside which 64 bits hold no difference of logits: their totals are all equal, so they come by
+    beam, and within a beam in the order of its logits, then of its tokens."""
+    fp4 = _fp4()
+    x = _logits(4, vocab, dtype, vocab).cpu()
+    x[1] = x[1].flip(0)
+    x[2, : vocab // 2] = x[2, 0]  # equal logits: the lower token
+    order = [torch.sort(r.double(), descending=True, stable=True).indices.tolist() for r in x]
+    for k in (4, min(64, 4 * vocab)):
+        s, p, t = fp4.beam_select(x.cuda(), torch.full((1, 4), low, device="cuda"), k=k)
+        want = [(b, v) for b in range(4) for v in order[b][:64]][:k]
+        assert list(zip(p[0].tolist(), t[0].tolist())) == want, k
+        assert bool((s == torch.tensor(low)).all())
+    if vocab < 16:  # fewer continuations of the one live beam, and of an ended one, than places
+        scores = torch.tensor([[low, -1.0, low, low]], device="cuda")
+        done = torch.tensor([[False, False, False, True]], device="cuda")
+        p, t = fp4.beam_select(x.cuda(), scores, k=3 * vocab + 1, done=done, end_token=2)[1:]
+        want = [(b, v) for b in (1, 0, 2) for v in order[b]] + [(3, 2)]
+        assert list(zip(p[0].tolist(), t[0].tolist())) == want
+
+
+def test_logits_nearer_than_a_total_tells():
+    """One beam's logits that differ by less than the last bit of their totals, in one part of the row and in two."""
+    fp4 = _fp4()
+    for at in ([30, 17, 29, 5], [39000, 17, 20001, 5]):
+        x = torch.full((1, 40000), -20.0, device="cuda")
+        for i, a in enumerate(at):
+            x[0, a] = 0.25 - i * 2.0 ** -26
+        s, p, t = fp4.beam_select(x, torch.full((1, 1), -1e9, device="cuda"), k=4)
+        assert t.tolist() == [at]
+        y = torch.full((1, 40000), -50.0, device="cuda")
+        y[0, 100] = 9.0
+        for i, a in enumerate(at):
+            y[0, a] = 1e-20 * (4 - i)
+        assert fp4.beam_select(y, torch.zeros(1, 1, device="cuda"), k=5)[2].tolist() == [[100] + at]
