@@ -205,6 +205,7 @@ __global__ __launch_bounds__(64) void k_head_norm_rope(HeadNormArgs a, int lane_
     if constexpr (FMT != kRowsOut) slot = a.kv.slots[token];
     const bool stored = FMT != kRowsOut && slot >= 0 && slot < (a.kv.pages << a.kv.page_shift);
 
+    bool left = false;  // a row of this lane is not done yet
     for (int p = p0; p < p1; p += U) {
         Raw<TI> next[U];
         if (p + U < p1) {
@@ -215,6 +216,7 @@ __global__ __launch_bounds__(64) void k_head_norm_rope(HeadNormArgs a, int lane_
         for (int u = 0; u < U; ++u) {
             if (p + u >= p1) break;
             const Pass x = pass(p + u);
+            bool here = x.here;
             float v[8];
             raw[u].get(v);
             if (x.side < 2) {
@@ -225,6 +227,8 @@ __global__ __launch_bounds__(64) void k_head_norm_rope(HeadNormArgs a, int lane_
                     const float inv = __builtin_amdgcn_rsqf(__builtin_fmaf(row_sum(ss, lane_shift), a.inv_dim, a.eps));
                     float w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
                     if (x.here) Vec8<float>::load((x.side ? a.w[1] : a.w[0]) + x.head * (x.side ? a.w_head[1] : a.w_head[0]) + e0, w);
+                    here &= inv != 0.0f;
+                    left |= inv == 0.0f;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[i] = v[i] * inv * w[i];
                 }
@@ -238,7 +242,7 @@ __global__ __launch_bounds__(64) void k_head_norm_rope(HeadNormArgs a, int lane_
                     }
                 }
             }
-            if (!x.here) continue;
+            if (!here) continue;
             if (FMT == kRowsOut || x.side == 0) {
                 TO *base = reinterpret_cast<TO *>(x.side ? a.y[1] : a.y[0]);
                 store8(base + token * (x.side ? a.y_tok[1] : a.y_tok[0]) + x.head * (x.side ? a.y_head[1] : a.y_head[0]) + e0, v);
@@ -249,6 +253,48 @@ __global__ __launch_bounds__(64) void k_head_norm_rope(HeadNormArgs a, int lane_
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) raw[u] = next[u];
+    }
+
+    // Rows of values past 10^18, whose squares have no place in fp32 (the root's inverse is 0), were left as they are.  They are
+    // taken 2^-70 times: 512 squares of any size have room then (2^125), and only bits below 2^-79 are lost, of a row whose root
+    // mean square is above 2^59.  (A test within the loop, with this work behind it, kept its passes' chains from running beside
+    // each other: one token 3.22 -> 3.5 us, 16384 70 -> 73.  This way 3.26 and 70; 6001 tokens into a bf16 cache 27.0 -> 27.7.)
+    if (!__ballot(left)) return;
+    for (int p = p0; p < min(p1, a.passes[1]); ++p) {
+        const Pass x = pass(p);
+        request(p, raw[0]);
+        float v[8], ss = 0.0f, w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        raw[0].get(v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(v[i], v[i], ss);
+        const bool over = row_sum(ss, lane_shift) == __builtin_inff();
+        ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[i] *= 0x1p-70f;
+            ss = __builtin_fmaf(v[i], v[i], ss);
+        }
+        const float inv = __builtin_amdgcn_rsqf(__builtin_fmaf(row_sum(ss, lane_shift), a.inv_dim, a.eps * 0x1p-140f));
+        if (x.here) Vec8<float>::load((x.side ? a.w[1] : a.w[0]) + x.head * (x.side ? a.w_head[1] : a.w_head[0]) + e0, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = v[i] * inv * w[i];
+        if (a.rot > 0) {
+            float q[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) q[i] = PAIR == kPairLane ? v[i ^ 1] : partner_of<PAIR>(v[i], partner);
+            if (turns) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = __builtin_fmaf(v[i], cs[i], q[i] * sn[i]);
+            }
+        }
+        if (!x.here || !over) continue;
+        if (FMT == kRowsOut || x.side == 0) {
+            TO *base = reinterpret_cast<TO *>(x.side ? a.y[1] : a.y[0]);
+            store8(base + token * (x.side ? a.y_tok[1] : a.y_tok[0]) + x.head * (x.side ? a.y_head[1] : a.y_head[0]) + e0, v);
+        }
+        if constexpr (FMT != kRowsOut) {
+            if (x.side > 0 && stored) cache8<FMT>(a.kv, x.side - 1, x.head, slot, c8, lane_shift, v);
+        }
     }
 }
 

@@ -585,7 +585,8 @@ fp4_status attn_prefill(const void *q, int64_t q_tokens, int64_t heads, int64_t 
  *         (positions and freqs may be null).
  *  q_out, k_out fp32 or bf16 (yt), strides as above; the same memory and strides as q, k (with
  *         xt == yt) is allowed, another overlap is not.
- * fp32 throughout, rounded once to yt.  head_dim a multiple of 8 up to 512, rot a multiple of
+ * fp32 throughout, rounded once to yt; finite rows of any size are normed (squares past fp32 are taken of scaled values).
+ * head_dim a multiple of 8 up to 512, rot a multiple of
  * 16 up to head_dim, heads and kv_heads up to 65535, tokens < 2^31 (FP4_ERR_SHAPE).  tokens == 0 returns FP4_OK. */
 fp4_status qk_norm_rope(const void *q, const void *k, fp4_dtype xt, int64_t tokens, int64_t heads, int64_t kv_heads,
                         int64_t head_dim, int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride,

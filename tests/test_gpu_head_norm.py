@@ -331,3 +331,34 @@ def test_rows_past_the_caches(dtype, dim, rot):
         s = slice(at, at + 1111)
         alone = fp4.qk_norm_rope(q[s], k[s], pos[s], freqs, w, w, eps=1e-6, dtype=dtype)
         assert torch.equal(got[0][s], alone[0]) and torch.equal(got[1][s], alone[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dim,rot,interleaved", [(128, 128, False), (64, 64, False), (80, 32, True), (512, 0, False), (8, 0, False)])
+def test_rows_whose_squares_pass_fp32(dim, rot, interleaved, dtype):
+    """Finite rows of any size are normed: values past 10^18, whose squares (or their sum) have no place in fp32, up to the type's largest, beside
+    ordinary rows of the same wave."""
+    fp4 = _fp4()
+    n, h = 23, 5
+    x = torch.randn(n, h, dim, generator=torch.Generator().manual_seed(dim))
+    for i, size in enumerate((1e15, 1e18, 4e18, 2e19, 1e25, 1e37)):
+        x[i, ::2] *= size
+    x[7, 1] = 1e-3
+    x[7, 1, 3] = -3e38
+    x[8, 4] = torch.finfo(dtype).max
+    x[8, 4, ::3] *= -1
+    x = x.to(dtype).cuda()
+    pos = torch.arange(n, dtype=torch.int32).cuda() * 31
+    freqs, w = (fp4.rope_frequencies(rot) if rot else None), _weight((h, dim), 1)
+    for eps in (1e-30, 1e-6, 1e30):
+        got = fp4.qk_norm_rope(x, x[:, 1:4], pos, freqs, w, w[1:4].contiguous(), eps=eps, interleaved=interleaved, dtype=torch.float32)
+        want = _ref(x, pos, freqs, w, eps, interleaved)
+        _close(got[0], want, f"q {eps}")
+        _close(got[1], [t[:, 1:4] for t in want], f"k {eps}")
+    if dim >= 64 and dim != 80 and dim != 512:  # the cache write's keys, rounded once
+        cache = fp4.KVCache.alloc("bf16", 2, h, 16, dim, "cuda")
+        args = (pos, torch.arange(n).cuda(), freqs, w, w)
+        q = fp4.qk_norm_rope_append(cache, x, x, x, *args, eps=1e-6, interleaved=interleaved)
+        same = fp4.qk_norm_rope(x, x, pos, freqs, w, w, eps=1e-6, interleaved=interleaved)
+        assert torch.equal(q, same[0])
+        assert torch.equal(cache.k_codes.transpose(1, 2).reshape(32, h, dim)[:n].view(torch.bfloat16), same[1])
