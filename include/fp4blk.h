@@ -640,8 +640,11 @@ size_t kv_pages_extend_workspace(int64_t seqs, int64_t tokens);
  * Pages are dealt in the order of the sequences and their positions.  A sequence that cannot
  * be served whole (too few free pages are left, the table's row is too narrow, its tokens
  * lie past `tokens`, its length is negative) is refused: its length, its row and the pool stay as
- * they are, its slots are -1 (its positions are those it asked for), and state_out[1] counts it.  Later
- * sequences that need no page are still served.
+ * they are, its slots are -1 (its positions are those it asked for), and state_out[1] counts it.
+ * Sequences do not overtake each other: behind one that found too few free pages every later one that needs a page
+ * is refused too, whatever is free (with 5 free pages and needs of 6, 1 and 1 none is served), while those that need
+ * no page are served.  So what must not wait, such as decode rows, comes before long prompts.  A sequence refused for
+ * another reason holds nothing back.
  * No page id or length makes the call access anything outside the buffers.
  * seqs < 2^24, table_width * page_size < 2^30, tokens < 2^30 (FP4_ERR_SHAPE). */
 fp4_status kv_pages_extend(const fp4_kv_pages *pool, int32_t *block_table, int64_t seqs, int64_t table_width,

@@ -418,3 +418,19 @@ def test_extend_among_empty_sequences(seqs):
         assert (dl.tolist(), plan.slots.tolist(), plan.positions.tolist()) == (lens, slots, positions)
         assert (plan.cu_q.tolist(), plan.cu_k.tolist()) == (cu_q, cu_k)
         _equal(host, pool, table, counts)
+
+
+def test_a_refusal_holds_back_the_pages_behind_it():
+    """After a sequence that the pool cannot serve, all later ones that need a page are refused too, whatever is free; what
+    needs none is served, and a sequence refused for another reason holds nothing back."""
+    fp4 = _fp4()
+    for first, given in ((96, [False, False, True, True]), (129, [False, True, True, True]), (80, [True, False, True, True])):
+        pool = fp4.KVPages(_i32([10, 11, 12, 13, 14] + [-1] * 15), _i32([5, 0]), 16)
+        table = _i32([[-1] * 8, [0] + [-1] * 7, [1] + [-1] * 7, [2] + [-1] * 7])
+        lens, new = [0, 16, 3, 15], [first, 1, 13, 1]
+        dl = _i32(lens)
+        plan = fp4.kv_pages_extend(pool, table, dl, _i32(new), sum(new))
+        assert dl.tolist() == [a + b if g else a for a, b, g in zip(lens, new, given)], first
+        assert pool.state.tolist() == [5 - 5 * given[0] - given[1], given.count(False)]
+        slots = plan.slots.tolist()
+        assert (min(slots[:first]) >= 0) == given[0] and (slots[first] >= 0) == given[1] and min(slots[first + 1:]) >= 16
