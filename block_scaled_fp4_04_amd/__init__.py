@@ -1490,7 +1490,9 @@ def kv_pages_collect_workspace(pages: KVPages, seqs: int, table_width: int) -> t
 def kv_pages_collect(pages: KVPages, block_table: torch.Tensor, seq_lens: torch.Tensor,
                      workspace: torch.Tensor | None = None) -> KVPages:
     """The pool's free list anew: every page that no row of the block table holds within its
-    length, in ascending order.  A sequence that ended gives its pages back by a length of 0."""
+    length, in ascending order.  A sequence that ended gives its pages back by a length of 0.  Whatever holds pages of the
+    pool has to stand in this one table (other batches, prompts kept for later use: rows of their own), or its pages
+    are dealt a second time."""
     seqs, width, stride = _block_table(block_table)
     _i32_vec(seq_lens, seqs, "seq_lens")
     need = lib().kv_pages_collect_workspace(pages.pages, seqs, width)

@@ -658,7 +658,10 @@ size_t kv_pages_collect_workspace(int64_t pages, int64_t seqs, int64_t table_wid
 /* The free list anew: every page that no row holds in its first ceil(seq_lens[b] / page_size)
  * entries, in ascending order; state[0] is their number, entries past it are left.  So the pages of a
  * sequence that ended (its length set to 0), of dropped beams or of a shortened sequence come
- * back; a page held by several rows stays held.  Entries outside [0, pages) are passed over. */
+ * back; a page held by several rows stays held.  Entries outside [0, pages) are passed over.
+ * A page that no row of THIS table holds is free afterwards and is dealt again, so every holder of the pool's pages has to
+ * stand in the one table: batches that share a pool are views of its rows, and a prompt kept for later use has a row of
+ * its own there. */
 fp4_status kv_pages_collect(const fp4_kv_pages *pool, const int32_t *block_table, int64_t seqs, int64_t table_width,
                             int64_t table_stride, const int32_t *seq_lens, void *ws, size_t ws_bytes,
                             hipStream_t stream);

@@ -434,3 +434,26 @@ def test_a_refusal_holds_back_the_pages_behind_it():
         assert pool.state.tolist() == [5 - 5 * given[0] - given[1], given.count(False)]
         slots = plan.slots.tolist()
         assert (min(slots[:first]) >= 0) == given[0] and (slots[first] >= 0) == given[1] and min(slots[first + 1:]) >= 16
+
+
+def test_collect_over_all_holders():
+    """A pool that serves two batches' tables and a kept prompt: one table that holds the rows of all of them is collected."""
+    fp4 = _fp4()
+    pages, page, width = 40, 16, 6
+    pool = fp4.KVPages.alloc(pages, page)
+    rows = torch.full((7, width), -1, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(7, dtype=torch.int32, device="cuda")
+    parts = [slice(0, 3), slice(3, 6), slice(6, 7)]  # views of one table: two batches and the prompt
+    for part, new in zip(parts, ([20, 1, 60], [16, 33, 5], [48])):
+        fp4.kv_pages_extend(pool, rows[part], lens[part], _i32(new), sum(new))
+    held = {p for r, n in zip(rows.tolist(), lens.tolist()) for p in r[:-(-n // page)]}
+    assert len(held) == pages - int(pool.state[0]) == 2 + 1 + 4 + 1 + 3 + 1 + 3
+    lens[4] = 0  # one sequence of the second batch ends
+    back = set(rows[4, :3].tolist())
+    fp4.kv_pages_collect(pool, rows, lens)
+    assert set(pool.free[:int(pool.state[0])].tolist()) == set(range(pages)) - held | back
+    before = rows.clone()
+    plan = fp4.kv_pages_extend(pool, rows[parts[0]], lens[parts[0]], _i32([16, 16, 16]), 48)
+    got = {s // page for s in plan.slots.tolist()}
+    kept = {p for r, n in zip(before.tolist()[3:], lens.tolist()[3:]) for p in r[:-(-n // page)]}
+    assert not got & kept
