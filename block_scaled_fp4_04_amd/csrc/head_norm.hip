@@ -67,6 +67,16 @@ __device__ __forceinline__ void store8(T *p, const float (&v)[8])
     }
 }
 
+// the place of a lane's 8 values among those of a cache's pages
+__device__ __forceinline__ int64_t cache_unit(const KvArgs &a, int head, int64_t slot, uint32_t c8, int lane_shift)
+{
+    const int64_t page = slot >> a.page_shift;
+    const uint32_t off = (uint32_t)slot & ((1u << a.page_shift) - 1u);
+    return ((((page * a.kv_heads + head) << a.page_shift) + off) << lane_shift) + c8;
+}
+
+constexpr int kRowsOut = -1;  // FMT: key rows are outputs, there is no cache
+
 // 8 values of a row into the cache (the lanes of a block come here together)
 template <int FMT>
 __device__ __forceinline__ void cache8(const KvArgs &a, int side, int head, int64_t slot, uint32_t c8, int lane_shift,
@@ -76,7 +86,7 @@ __device__ __forceinline__ void cache8(const KvArgs &a, int side, int head, int6
     const uint32_t off = (uint32_t)slot & ((1u << a.page_shift) - 1u);
     const int64_t block = (page * a.kv_heads + head) << a.page_shift;
     uint8_t *codes = side ? a.codes[1] : a.codes[0], *scales = side ? a.scales[1] : a.scales[0];
-    const int64_t unit = ((block + off) << lane_shift) + c8;
+    const int64_t unit = cache_unit(a, head, slot, c8, lane_shift);
     if constexpr (FMT == FP4_KV_BF16) {
         store8(reinterpret_cast<uint16_t *>(codes) + unit * 8, v);
     } else {
@@ -95,7 +105,25 @@ __device__ __forceinline__ void cache8(const KvArgs &a, int side, int head, int6
     }
 }
 
-constexpr int kRowsOut = -1;  // FMT: key rows are outputs, there is no cache
+// 8 values to their place.  A bf16 cache takes the q rows' own store at another address: as two alternatives the compiler
+// joined their ends into a store of 4 bytes and one of 12 (6001 tokens from memory 35.3 us, this way 33.2).
+template <typename TO, int FMT>
+__device__ __forceinline__ void put8(const HeadNormArgs &a, int side, int head, int64_t token, int64_t slot, bool stored, uint32_t c8,
+                                     int lane_shift, const float (&v)[8])
+{
+    constexpr bool kSame = FMT == FP4_KV_BF16 && sizeof(TO) == 2;
+    if (FMT == kRowsOut || kSame || side == 0) {
+        const int64_t tok = FMT == kRowsOut && side ? a.y_tok[1] : a.y_tok[0], step = FMT == kRowsOut && side ? a.y_head[1] : a.y_head[0];
+        TO *p = reinterpret_cast<TO *>(FMT == kRowsOut && side ? a.y[1] : a.y[0]) + token * tok + head * step + c8 * 8;
+        if (kSame && side > 0) {
+            if (!stored) return;
+            p = reinterpret_cast<TO *>(side == 2 ? a.kv.codes[1] : a.kv.codes[0]) + cache_unit(a.kv, head, slot, c8, lane_shift) * 8;
+        }
+        store8(p, v);
+    } else if constexpr (FMT != kRowsOut) {
+        if (stored) cache8<FMT>(a.kv, side - 1, head, slot, c8, lane_shift, v);
+    }
+}
 
 // How the two values of a pair meet: neighbours of a lane (interleaved), lanes 8 or 4 apart by DPP (half-split, rot
 // 128 or 64), or any lanes by a shuffle
@@ -243,13 +271,7 @@ __global__ __launch_bounds__(64) void k_head_norm_rope(HeadNormArgs a, int lane_
                 }
             }
             if (!here) continue;
-            if (FMT == kRowsOut || x.side == 0) {
-                TO *base = reinterpret_cast<TO *>(x.side ? a.y[1] : a.y[0]);
-                store8(base + token * (x.side ? a.y_tok[1] : a.y_tok[0]) + x.head * (x.side ? a.y_head[1] : a.y_head[0]) + e0, v);
-            }
-            if constexpr (FMT != kRowsOut) {
-                if (x.side > 0 && stored) cache8<FMT>(a.kv, x.side - 1, x.head, slot, c8, lane_shift, v);
-            }
+            put8<TO, FMT>(a, x.side, x.head, token, slot, stored, c8, lane_shift, v);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) raw[u] = next[u];
@@ -258,7 +280,7 @@ __global__ __launch_bounds__(64) void k_head_norm_rope(HeadNormArgs a, int lane_
     // Rows of values past 10^18, whose squares have no place in fp32 (the root's inverse is 0), were left as they are.  They are
     // taken 2^-70 times: 512 squares of any size have room then (2^125), and only bits below 2^-79 are lost, of a row whose root
     // mean square is above 2^59.  (A test within the loop, with this work behind it, kept its passes' chains from running beside
-    // each other: one token 3.22 -> 3.5 us, 16384 70 -> 73.  This way 3.26 and 70; 6001 tokens into a bf16 cache 27.0 -> 27.7.)
+    // each other: one token 3.22 -> 3.5 us, 16384 70 -> 73.  This way 3.26 and 70.)
     if (!__ballot(left)) return;
     for (int p = p0; p < min(p1, a.passes[1]); ++p) {
         const Pass x = pass(p);
@@ -288,13 +310,7 @@ __global__ __launch_bounds__(64) void k_head_norm_rope(HeadNormArgs a, int lane_
             }
         }
         if (!x.here || !over) continue;
-        if (FMT == kRowsOut || x.side == 0) {
-            TO *base = reinterpret_cast<TO *>(x.side ? a.y[1] : a.y[0]);
-            store8(base + token * (x.side ? a.y_tok[1] : a.y_tok[0]) + x.head * (x.side ? a.y_head[1] : a.y_head[0]) + e0, v);
-        }
-        if constexpr (FMT != kRowsOut) {
-            if (x.side > 0 && stored) cache8<FMT>(a.kv, x.side - 1, x.head, slot, c8, lane_shift, v);
-        }
+        put8<TO, FMT>(a, x.side, x.head, token, slot, stored, c8, lane_shift, v);
     }
 }
 
