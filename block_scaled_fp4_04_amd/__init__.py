@@ -1445,8 +1445,10 @@ def kv_pages_extend(pages: KVPages, block_table: torch.Tensor, seq_lens: torch.T
     new token are listed, packed one sequence behind the other.  tokens = sum(new_lens), or more (known to the
     caller, so that nothing waits for the device).  in_place: seq_lens and the pool's state become
     those after the call; else the plan holds new ones.  A sequence that cannot be served whole is
-    left as it is: its slots are -1 and state[1] counts it.  Behind one for which the free pages did not suffice, all later ones
-    that need a page are refused too (put decode rows before long prompts).  `out`: a plan of the same sizes to write into."""
+    left as it is: its slots are -1 and state[1] counts it.  Behind one for which the free pages did not
+    suffice, all later ones that need a page are refused too (put decode rows before long prompts).  `out`: a plan
+    of the same sizes to write into; lengths, state and offsets then go where its members say, whatever
+    in_place and offsets are."""
     seqs, width, stride = _block_table(block_table)
     _i32_vec(seq_lens, seqs, "seq_lens")
     _i32_vec(new_lens, seqs, "new_lens")

@@ -6,8 +6,8 @@
 // Two launches.  k_beam_rows reads the logits once, a workgroup a part of a row: the part's maximum, its sum of
 // exponentials and its k best logits (within a row the order of the totals is that of the logits).  k_beam_join
 // adds up a row's sums, and merges the sorted lists of all parts of all beams.  Bound by reading the logits, and then by
-// what follows the last load: 461 rows of 131072 bf16 logits (121 MB) take 31 us (24 us without exponentials and
-// selection, 19 us is the time of a load-only pass) and the join of 64 groups, k = 16, 6.6 us.
+// what follows the last load: 461 rows of 131072 bf16 logits (121 MB) take 30 us (24 us without exponentials and
+// selection, 19 us is the time of a load-only pass) and the join of 64 groups, k = 16, 6.8 us.
 //
 // Order: totals are compared in 64 bits (in 32, sums of scores around -50 and small differences of logits
 // would merge neighbours), equal ones by beam, logit and token: beside a score of -10^30, or a maximum 10^17 times as large, 64 bits

@@ -10,7 +10,7 @@
 // holds up to 64 / that many rows at a time.  A wave takes one token and walks over its heads: the 8
 // cosines and sines of a lane depend on the token and the lane's place in the row only, and are formed
 // once a token, in place of a table that would have to be read.  Bound by memory where there are many tokens: 16384
-// tokens of 40 + 8 heads of 128 in bf16, 403 MB, take 84 us (4.8 TB/s; a large copy runs at 5.2), one row a lane group
+// tokens of 40 + 8 heads of 128 in bf16, 403 MB, take 85 us (4.7 TB/s; a large copy runs at 5.2), one row a lane group
 // at a time 128 us; 6001 tokens of 16 + 4 + 4 heads of 256 into a bf16 cache, 148 MB, 33 us.  By the launch where
 // there are few: one token 3.8 us.
 #include "quant_device.h"
@@ -126,7 +126,9 @@ __device__ __forceinline__ void put8(const HeadNormArgs &a, int side, int head, 
 }
 
 // How the two values of a pair meet: neighbours of a lane (interleaved), lanes 8 or 4 apart by DPP (half-split, rot
-// 128 or 64), or any lanes by a shuffle
+// 128 or 64), or any lanes by a shuffle.  (DPP / the shuffle for these too, us: in fp32 4096 tokens of 16 + 4 heads of 128
+// 16.9 / 18.2, 8192 of 32 + 8 of 64 26.9 / 29.3; in bf16 16384 of 40 + 8 of 128 71.1 / 72.3, of 32 + 8 of 64 30.7 / 30.7;
+// cache writes within 2% either way.)
 enum { kPairLane = 0, kPair8 = 1, kPair4 = 2, kPairAny = 3 };
 
 template <int PAIR>
@@ -333,8 +335,8 @@ static void launch_pair(HeadNormArgs a, int lane_shift, hipStream_t st)
     // (74 and 87 when the outputs' memory is used again and again); between
     // a projection and the attention of its 8192 tokens (117 MB in) 1 to 2.5% of the whole chain's 640 us, at 16384 0.5%,
     // at 4096 (59 MB) and below none, while there rows that were used shortly before come back from the caches (4096
-    // tokens read again and again: 25 us, 31 us with the hint).  Streaming stores would make the attention that reads the
-    // rows next wait for them (4096 tokens: the chain 331 -> 335 us).
+    // tokens read again and again: 25 us, 31 us with the hint).  Streaming stores are of no clear use there
+    // (the chain at 4096 tokens 331 -> 335 us, at 8192 647 -> 643, at 16384 1233 -> 1235).
     const int64_t bytes = a.tokens * (a.heads + (FMT == kRowsOut ? 1 : 2) * a.kv_heads) * a.dim * (int64_t)sizeof(TI);
     const bool once_only = bytes >= (int64_t(96) << 20);
     // a launch holds fewer than 2^32 threads

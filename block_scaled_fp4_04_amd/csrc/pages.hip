@@ -4,8 +4,8 @@
 //
 // All of it is a few integers a sequence, a token or a table entry: bound by the launch and by chains of
 // dependent loads and scans, not by bytes, so the small calls are one workgroup and one launch (64 sequences of one token
-// 3.1 us; 300 sequences and 32000 tokens in two launches 4.6 + 3.3 us; the free list of 26000 pages from 512 rows
-// 4.3 + 5.2 us; tables of 288 beams 4.8 us and their page copies 5.2 us).  Results do not depend on
+// 3.1 us; 300 sequences and 32000 tokens in two launches 4.6 + 3.1 us; the free list of 26000 pages from 512 rows
+// 4.4 + 5.0 us; tables of 288 beams 4.9 us and their page copies 5.3 us).  Results do not depend on
 // the order of workgroups: sums are prefix sums, and no entry is written by one workgroup and read by another
 // of the same launch.
 #include "device_common.h"
@@ -331,7 +331,8 @@ __device__ __forceinline__ uint32_t marked(const uint32_t *ws, int64_t words, in
     return w;
 }
 
-// one workgroup a 1024 words: what is free before them, then their own
+// One workgroup a 1024 words: what is free before them, then their own.  (Quadratic in the pool: of 4194304 pages the whole call
+// takes 102 us, of 16777216 827.)
 __global__ __launch_bounds__(1024) void k_pages_sweep(PageArgs a, int64_t words)
 {
     __shared__ uint32_t red[16];
