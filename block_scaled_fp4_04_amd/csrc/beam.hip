@@ -10,9 +10,11 @@
 // selection, 19 us is the time of a load-only pass) and the join of 64 groups, k = 16, 6.8 us.
 //
 // Order: totals are compared in 64 bits (in 32, sums of scores around -50 and small differences of logits
-// would merge neighbours), equal ones by beam, logit and token: beside a score of -10^30, or a maximum 10^17 times as large, 64 bits
-// hold no difference of logits either, and a beam's list has to be as sorted by totals as it is by logits.  The sums of exponentials are fp32 over a lane's values of
-// a group (32 or 16, by halves) and 64 bits from there on.  The exponentials are fp32, e^a of a = logit - reference: v_exp_f32
+// would merge neighbours), equal ones by beam, logit and token: beside a score of -10^30, or a maximum 10^17 times as
+// large, 64 bits hold no difference of logits either, and a beam's list has to be as sorted by totals as it is by logits.
+//
+// The sums of exponentials are fp32 over a lane's values of a group (32 or 16, by halves) and 64 bits from there on.  The
+// exponentials are fp32, e^a of a = logit - reference: v_exp_f32
 // is within 1 ulp, and a's two roundings and that of log2 e weigh 1.2 |a| 2^-23 at most.  The reference is a wave's first
 // maximum until a value is more than 8 above it, so a term d below the row's maximum has |a| <= max(8, d), and the mean of that
 // over a row's N terms, each weighed by its share, is at most max(9, ln N) (entropy).  The additions and the exponentials

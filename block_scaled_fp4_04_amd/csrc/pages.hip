@@ -65,7 +65,8 @@ struct Span {
     int32_t fresh;   // its place in the order of new pages; -1: refused
 };
 
-// One workgroup over all sequences (a refused one's pages stay in the running sum, so that nobody overtakes it): Span s to `spans`, lengths, offsets and the pool's state written.
+// One workgroup over all sequences (pages that a refused one asked for stay in the running sum, so that nobody overtakes
+// it): Span s to `spans`, lengths, offsets and the pool's state written.
 // Returns the free pages before the call.
 __device__ __forceinline__ int32_t deal_pages(const PageArgs &a, Span *spans)
 {
